@@ -75,7 +75,7 @@ def draw(rng):
                 "masked": rng.choice([0.0, 0.2]), "lo": 0.2, "hi": rng.choice([0.2, 0.28]),
                 "kl": rng.choice([0.0, 0.04]), "seq_mean": rng.random() < 0.5}
     vocab = _log_int(rng, 1000, 131072)
-    rows = _log_int(rng, 1 if kind == "logp" else 16, min(4096, (1 << 28) // vocab))
+    rows = _log_int(rng, 1 if kind == "logp" else 16, min(4096, (3 << 26) // vocab))
     case = {"kind": kind, "dtype": rng.choice(["f32", "f16", "bf16"]), "rows": rows, "vocab": vocab,
             "pad": rng.choice([0, 0, 5, 64]), "temperature": rng.choice([1.0, 0.7]),
             "ignored": rng.choice([0.0, 0.2]) if rows > 8 else 0.0, "banned": rng.choice([0.0, 0.2])}
