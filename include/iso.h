@@ -294,6 +294,128 @@ int iso_calib_apply(const double* xp, const double* fp, int64_t k, const double*
                     const int32_t* segment, int64_t m, double* out, void* stream);
 size_t iso_calib_workspace_bytes(int64_t n);
 
+/*
+ * Post-training losses: what turns calibrated rewards or preferences into
+ * gradients of a language model (calibrated scores: iso_calib_apply above).
+ * Token log-probabilities from logits with their backward pass, a paired
+ * preference loss, a clipped policy loss with a KL term, and the policy loss
+ * taken from the logits.  Logits are f32, f16 or bf16 (ISO_DT_*); every other
+ * real array is f32.  Softmax sums are f32 per thread over at most a few
+ * hundred terms and f64 where threads are joined; the losses' sums are f64;
+ * each output is rounded once.  No atomics: results do not depend on
+ * scheduling.  The calls only enqueue work on `stream` (they may be captured
+ * into a graph), allocate nothing, and use a caller workspace (256-byte
+ * aligned, no initialisation) of the size the matching *_workspace_bytes
+ * gives.  Statuses: ISO_OK, ISO_ERR_ARG, ISO_ERR_WORKSPACE, ISO_ERR_HIP;
+ * nothing is launched on an error.
+ *
+ * iso_token_logp - for each row t of logits, with x = logits[t] / temperature
+ * and target j = target[t]:
+ *     lse[t]     = log sum_k exp(x_k) ,       logp[t] = x_j - lse[t] ,
+ *     entropy[t] = lse[t] - sum_k p_k x_k ,   p_k = exp(x_k - lse[t]) .
+ *   logits  [rows][vocab] of `dtype`, device, row r at r*ld elements, aligned
+ *           to its element size; ld >= vocab (>= 1; at most 2^30).
+ *   target  [rows] int32, device.  A negative target marks an ignored row: the
+ *           row is not read and its outputs are 0.  A target >= vocab gives
+ *           NaN logp.
+ *   logp, lse [rows] f32, written.  entropy [rows] f32, written, or NULL.
+ *   temperature > 0, finite.
+ * A logit of -infinity (or far below the row's maximum) is a masked entry and
+ * adds nothing.  A row with a NaN or +infinity, or of -infinity alone, has no
+ * distribution: its outputs are NaN.
+ *
+ * iso_token_logp_vjp - the gradient of the logits, for gradients g_logp of
+ * logp and g_entropy of the entropy (NULL: none):
+ *     grad_k = ( g_logp ([k = j] - p_k) - g_entropy p_k (x_k - lse + entropy) ) / temperature .
+ *   lse     [rows] f32: the forward call's.  entropy [rows] f32: the forward
+ *           call's (needed with g_entropy only).
+ *   grad    [rows][vocab] of `dtype`, row r at r*ld_grad, written.  It may be
+ *           the logits themselves (same pointer and ld): the gradient then
+ *           takes the logits' place; any other overlap is an error.  Columns
+ *           past vocab are not touched.
+ * Ignored rows get zeros.  A row whose target is >= vocab gets NaN.
+ */
+enum { ISO_DT_F32 = 0, ISO_DT_F16 = 1, ISO_DT_BF16 = 2 };
+size_t iso_token_logp_workspace_bytes(int64_t rows, int64_t vocab, int dtype);
+int iso_token_logp(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                   const int32_t* target, double temperature, float* logp, float* lse,
+                   float* entropy, void* workspace, size_t workspace_bytes, void* stream);
+int iso_token_logp_vjp(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                       const int32_t* target, double temperature, const float* lse,
+                       const float* entropy, const float* g_logp, const float* g_entropy,
+                       void* grad, int64_t ld_grad, void* stream);
+
+/*
+ * Sequences of tokens, in both losses: packed one after another, sequence q
+ * the tokens seq_off[q] .. seq_off[q+1]-1 (seq_off [seqs+1] int32, device,
+ * non-decreasing, from 0 to `tokens`); with seq_off NULL all have the length
+ * tokens / seqs (which must divide).  Offsets that break this are held inside
+ * [0, tokens]: nothing outside the arrays is touched, the outputs are then
+ * unspecified.  mask [tokens] bytes, device, or NULL: a token with mask 0
+ * takes no part, whatever its values (NaN included), and its gradient is 0.
+ * A sequence may be empty or wholly masked.  tokens is at most 2^31 - 1.
+ *
+ * iso_pref_loss - the paired preference loss.  Sequence 2i is pair i's chosen
+ * answer, 2i+1 its rejected one.  With s_q the sum over q's tokens of
+ * logp - ref_logp (ISO_PREF_MEAN: divided by the number of unmasked tokens),
+ * D = s_2i - s_2i+1 and e = label_smoothing:
+ *     l_i = -(1-e) log sigma(beta D) - e log sigma(-beta D) ,
+ *     ISO_PREF_SQUARED:  l_i = (D - 1 / (2 beta))^2 ,
+ *     loss = (1 / pairs) sum_i l_i .
+ *   logp, ref_logp [tokens] f32 (ref_logp NULL: no reference, zeros).
+ *   beta > 0; label_smoothing in [0, 1/2] (0 with ISO_PREF_SQUARED).
+ *   loss      [1], written (0 when pairs is 0).  pair_loss [pairs] = l_i,
+ *             written.  reward [2 pairs] = beta s_q, written.
+ *   grad      [tokens], written, or NULL: grad_scale times the gradient of
+ *             loss with respect to logp.
+ *
+ * iso_policy_loss - the clipped policy loss.  Per token, with A its advantage,
+ * d = logp - old_logp, r = exp(d), u = ref_logp - logp:
+ *     pg = -min(r A, clip(r, 1 - clip_lo, 1 + clip_hi) A) ,
+ *     kl = exp(u) - u - 1      (0 without ref_logp) ,
+ *     loss = sum_t w_t (pg_t + kl_coef kl_t) ,
+ *   w_t = 1 / (unmasked tokens), or with ISO_POLICY_SEQ_MEAN
+ *   1 / (seqs * unmasked tokens of its sequence); a norm > 0 takes the place of
+ *   the count of tokens, or of seqs (for sums over several calls).
+ *   adv       [seqs] f32, or [tokens] with ISO_POLICY_ADV_TOKEN.
+ *   clip_lo in [0, 1], clip_hi >= 0 (may be infinite), kl_coef finite (0
+ *   without ref_logp).
+ *   loss      [3] f32, written: the loss, its part sum w pg, and sum w kl.
+ *   counts    [2] int32, written: unmasked tokens, and those the clip holds
+ *             (A > 0 and d > log(1 + clip_hi), or A < 0 and
+ *             d < log(1 - clip_lo)): their pg has gradient 0.
+ *   grad      [tokens], written, or NULL: grad_scale times the gradient of
+ *             loss with respect to logp.
+ *
+ * iso_policy_loss_logits - token_logp, the policy loss and the gradient of the
+ * logits in one call: rows of logits are the tokens, ignored rows (target < 0)
+ * the masked ones.  Arguments as above; logp [rows] f32 is written (0 on
+ * ignored rows), grad as in iso_token_logp_vjp (may be the logits; NULL for
+ * the loss alone).
+ */
+enum { ISO_PREF_MEAN = 1u, ISO_PREF_SQUARED = 2u };
+enum { ISO_POLICY_SEQ_MEAN = 1u, ISO_POLICY_ADV_TOKEN = 2u };
+size_t iso_pref_loss_workspace_bytes(int64_t tokens, int64_t pairs);
+int iso_pref_loss(const float* logp, const float* ref_logp, const uint8_t* mask,
+                  const int32_t* seq_off, int64_t pairs, int64_t tokens, double beta,
+                  double label_smoothing, float* loss, float* pair_loss, float* reward, float* grad,
+                  double grad_scale, void* workspace, size_t workspace_bytes, void* stream,
+                  uint32_t flags);
+size_t iso_policy_loss_workspace_bytes(int64_t tokens, int64_t seqs);
+int iso_policy_loss(const float* logp, const float* old_logp, const float* ref_logp,
+                    const float* adv, const uint8_t* mask, const int32_t* seq_off, int64_t seqs,
+                    int64_t tokens, double clip_lo, double clip_hi, double kl_coef, double norm,
+                    float* loss, int32_t* counts, float* grad, double grad_scale, void* workspace,
+                    size_t workspace_bytes, void* stream, uint32_t flags);
+size_t iso_policy_loss_logits_workspace_bytes(int64_t rows, int64_t vocab, int64_t seqs, int dtype);
+int iso_policy_loss_logits(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                           const int32_t* target, double temperature, const float* old_logp,
+                           const float* ref_logp, const float* adv, const int32_t* seq_off,
+                           int64_t seqs, double clip_lo, double clip_hi, double kl_coef, double norm,
+                           float* loss, int32_t* counts, float* logp, void* grad, int64_t ld_grad,
+                           double grad_scale, void* workspace, size_t workspace_bytes, void* stream,
+                           uint32_t flags);
+
 /* Bytes of device workspace iso_fit_ex needs for this shape and these flags
  * (weighted or not is part of the shape: pass ISO_F_WEIGHTED_HINT in flags
  * when w will be non-NULL).  Returns 0 for an empty or invalid shape. */

@@ -4,9 +4,11 @@ Every step of the fit runs in the library's gfx950 kernels; this module only
 passes pointers, sizes and the current torch stream.  It raises if the built
 library is missing: there is no fallback.
 
-Functions with the C names take raw device pointers (ints); ``fit`` is a
-convenience wrapper over torch CUDA tensors that allocates the output and the
-workspace with torch and calls ``iso_fit_ex``.
+Functions with the C names take raw device pointers (ints); ``fit``, ``vjp``,
+``calib_curve`` and the loss operators ``token_logp``, ``token_logp_vjp``,
+``pref_loss``, ``policy_loss`` and ``policy_loss_logits`` are convenience
+wrappers over torch CUDA tensors that allocate the outputs and the workspace
+with torch.
 """
 from __future__ import annotations
 
@@ -36,6 +38,15 @@ ISO_F_TREE_MERGES = 0x1000
 ISO_F_WEIGHTED_HINT = 0x100
 ISO_F_PHASE_STAMPS = 0x200
 
+ISO_DT_F32 = 0
+ISO_DT_F16 = 1
+ISO_DT_BF16 = 2
+
+ISO_PREF_MEAN = 1
+ISO_PREF_SQUARED = 2
+ISO_POLICY_SEQ_MEAN = 1
+ISO_POLICY_ADV_TOKEN = 2
+
 ISO_PHASE_NAMES = ("short_rows", "chunk_hulls", "merge", "expand", "copy_bridge", "copy_move",
                    "merge_top", "chunk_redo")
 
@@ -45,7 +56,10 @@ EXPORTS = ("iso_fit", "iso_fit_ex", "iso_fit_noalloc", "iso_workspace_bytes", "i
            "iso_release", "iso_chunk_size", "iso_short_row_max", "iso_timing_enable",
            "iso_timing_read", "iso_vjp", "iso_vjp_f64", "iso_vjp_workspace_bytes", "iso_fit_ex_f64",
            "iso_fit_f64", "iso_calib_fit", "iso_calib_apply", "iso_calib_workspace_bytes",
-           "iso_copy_probe")
+           "iso_copy_probe", "iso_token_logp", "iso_token_logp_vjp", "iso_token_logp_workspace_bytes",
+           "iso_pref_loss", "iso_pref_loss_workspace_bytes", "iso_policy_loss",
+           "iso_policy_loss_workspace_bytes", "iso_policy_loss_logits",
+           "iso_policy_loss_logits_workspace_bytes")
 
 _lib = None
 
@@ -89,6 +103,27 @@ def lib() -> ctypes.CDLL:
         L.iso_vjp_workspace_bytes.restype = sz
         L.iso_workspace_bytes.argtypes = [i64, i64, u32]
         L.iso_workspace_bytes.restype = sz
+        f64, i32 = ctypes.c_double, ctypes.c_int
+        L.iso_token_logp.argtypes = [p, i32, i64, i64, i64, p, f64, p, p, p, p, sz, p]
+        L.iso_token_logp.restype = ctypes.c_int
+        L.iso_token_logp_workspace_bytes.argtypes = [i64, i64, i32]
+        L.iso_token_logp_workspace_bytes.restype = sz
+        L.iso_token_logp_vjp.argtypes = [p, i32, i64, i64, i64, p, f64, p, p, p, p, p, i64, p]
+        L.iso_token_logp_vjp.restype = ctypes.c_int
+        L.iso_pref_loss.argtypes = [p, p, p, p, i64, i64, f64, f64, p, p, p, p, f64, p, sz, p, u32]
+        L.iso_pref_loss.restype = ctypes.c_int
+        L.iso_pref_loss_workspace_bytes.argtypes = [i64, i64]
+        L.iso_pref_loss_workspace_bytes.restype = sz
+        L.iso_policy_loss.argtypes = [p, p, p, p, p, p, i64, i64, f64, f64, f64, f64, p, p, p, f64, p,
+                                      sz, p, u32]
+        L.iso_policy_loss.restype = ctypes.c_int
+        L.iso_policy_loss_workspace_bytes.argtypes = [i64, i64]
+        L.iso_policy_loss_workspace_bytes.restype = sz
+        L.iso_policy_loss_logits.argtypes = [p, i32, i64, i64, i64, p, f64, p, p, p, p, i64, f64, f64,
+                                             f64, f64, p, p, p, p, i64, f64, p, sz, p, u32]
+        L.iso_policy_loss_logits.restype = ctypes.c_int
+        L.iso_policy_loss_logits_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        L.iso_policy_loss_logits_workspace_bytes.restype = sz
         L.iso_status_str.argtypes = [ctypes.c_int]
         L.iso_status_str.restype = ctypes.c_char_p
         L.iso_release.argtypes = []
@@ -161,6 +196,58 @@ def iso_vjp_f64(g_ptr, y_ptr, w_ptr, block_id_ptr, rows, n, grad_y_ptr, grad_w_p
 
 def iso_vjp_workspace_bytes(rows, n) -> int:
     return lib().iso_vjp_workspace_bytes(rows, n)
+
+
+def iso_token_logp(logits_ptr, dtype, rows, vocab, ld, target_ptr, temperature, logp_ptr, lse_ptr,
+                   entropy_ptr, ws_ptr, ws_bytes, stream) -> int:
+    return lib().iso_token_logp(logits_ptr, dtype, rows, vocab, ld, target_ptr, temperature, logp_ptr,
+                                lse_ptr, entropy_ptr, ws_ptr, ws_bytes, stream)
+
+
+def iso_token_logp_workspace_bytes(rows, vocab, dtype) -> int:
+    return lib().iso_token_logp_workspace_bytes(rows, vocab, dtype)
+
+
+def iso_token_logp_vjp(logits_ptr, dtype, rows, vocab, ld, target_ptr, temperature, lse_ptr,
+                       entropy_ptr, g_logp_ptr, g_entropy_ptr, grad_ptr, ld_grad, stream) -> int:
+    return lib().iso_token_logp_vjp(logits_ptr, dtype, rows, vocab, ld, target_ptr, temperature, lse_ptr,
+                                    entropy_ptr, g_logp_ptr, g_entropy_ptr, grad_ptr, ld_grad, stream)
+
+
+def iso_pref_loss(logp_ptr, ref_ptr, mask_ptr, off_ptr, pairs, tokens, beta, label_smoothing, loss_ptr,
+                  pair_loss_ptr, reward_ptr, grad_ptr, grad_scale, ws_ptr, ws_bytes, stream, flags) -> int:
+    return lib().iso_pref_loss(logp_ptr, ref_ptr, mask_ptr, off_ptr, pairs, tokens, beta, label_smoothing,
+                               loss_ptr, pair_loss_ptr, reward_ptr, grad_ptr, grad_scale, ws_ptr, ws_bytes,
+                               stream, flags)
+
+
+def iso_pref_loss_workspace_bytes(tokens, pairs) -> int:
+    return lib().iso_pref_loss_workspace_bytes(tokens, pairs)
+
+
+def iso_policy_loss(logp_ptr, old_ptr, ref_ptr, adv_ptr, mask_ptr, off_ptr, seqs, tokens, clip_lo, clip_hi,
+                    kl_coef, norm, loss_ptr, counts_ptr, grad_ptr, grad_scale, ws_ptr, ws_bytes, stream,
+                    flags) -> int:
+    return lib().iso_policy_loss(logp_ptr, old_ptr, ref_ptr, adv_ptr, mask_ptr, off_ptr, seqs, tokens,
+                                 clip_lo, clip_hi, kl_coef, norm, loss_ptr, counts_ptr, grad_ptr, grad_scale,
+                                 ws_ptr, ws_bytes, stream, flags)
+
+
+def iso_policy_loss_workspace_bytes(tokens, seqs) -> int:
+    return lib().iso_policy_loss_workspace_bytes(tokens, seqs)
+
+
+def iso_policy_loss_logits(logits_ptr, dtype, rows, vocab, ld, target_ptr, temperature, old_ptr, ref_ptr,
+                           adv_ptr, off_ptr, seqs, clip_lo, clip_hi, kl_coef, norm, loss_ptr, counts_ptr,
+                           logp_ptr, grad_ptr, ld_grad, grad_scale, ws_ptr, ws_bytes, stream, flags) -> int:
+    return lib().iso_policy_loss_logits(logits_ptr, dtype, rows, vocab, ld, target_ptr, temperature, old_ptr,
+                                        ref_ptr, adv_ptr, off_ptr, seqs, clip_lo, clip_hi, kl_coef, norm,
+                                        loss_ptr, counts_ptr, logp_ptr, grad_ptr, ld_grad, grad_scale, ws_ptr,
+                                        ws_bytes, stream, flags)
+
+
+def iso_policy_loss_logits_workspace_bytes(rows, vocab, seqs, dtype) -> int:
+    return lib().iso_policy_loss_logits_workspace_bytes(rows, vocab, seqs, dtype)
 
 
 def iso_workspace_bytes(rows, n, flags=0) -> int:
@@ -283,3 +370,215 @@ def calib_curve(scores, outcomes, segment=None, stream=None):
     if st < 0:
         raise IsoError(st)
     return xp[:k.value], fp[:k.value]
+
+
+class _Launch:
+    """One call of a loss operator over torch tensors: their checks, the stream
+    it runs on, and its outputs and workspace.  Outputs and workspace are
+    allocated on that stream, and every tensor the call is given is recorded on
+    it where it is not the current one, so that none is reused too early."""
+
+    def __init__(self, lead, stream):
+        import torch
+
+        self.torch, self.dev = torch, lead.device
+        if not lead.is_cuda:
+            raise TypeError("the tensors must be CUDA tensors")
+        current = torch.cuda.current_stream(self.dev)
+        if self.dev.index != torch.cuda.current_device():
+            raise ValueError("the tensors must be on the current device")
+        self.stream = current if stream is None else stream
+        self.other = self.stream if self.stream != current else None
+        self.handle = ctypes.c_void_p(self.stream.cuda_stream)
+
+    def use(self, t, name, shape, dtypes):
+        """The pointer of input t (None: NULL) after its checks."""
+        if t is None:
+            return None
+        if t.device != self.dev or t.dtype not in dtypes:
+            raise TypeError(f"{name} must be a tensor of {' or '.join(str(d) for d in dtypes)} on {self.dev}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have the shape {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if self.other is not None:
+            t.record_stream(self.other)
+        return t.data_ptr()
+
+    def new(self, shape, dtype):
+        if self.other is None:
+            return self.torch.empty(shape, dtype=dtype, device=self.dev)
+        with self.torch.cuda.stream(self.other):
+            return self.torch.empty(shape, dtype=dtype, device=self.dev)
+
+    def workspace(self, nbytes):
+        return self.new(max(nbytes, 1), self.torch.uint8)
+
+    def logits(self, t, name):
+        """(pointer, dtype code, rows, vocab, ld) of a matrix of logits: 2-D, its rows contiguous."""
+        codes = {self.torch.float32: ISO_DT_F32, self.torch.float16: ISO_DT_F16, self.torch.bfloat16: ISO_DT_BF16}
+        if t.device != self.dev or t.dtype not in codes:
+            raise TypeError(f"{name} must be a float32, float16 or bfloat16 CUDA tensor")
+        if t.dim() != 2 or t.shape[1] < 1:
+            raise ValueError(f"{name} must have the shape (rows, vocab)")
+        rows, vocab = t.shape
+        ld = t.stride(0) if rows > 1 else vocab
+        if (vocab > 1 and t.stride(1) != 1) or ld < vocab:
+            raise ValueError(f"{name}'s rows must be contiguous and not overlap")
+        if self.other is not None:
+            t.record_stream(self.other)
+        return t.data_ptr(), codes[t.dtype], rows, vocab, ld
+
+    def grad_of(self, logits, out):
+        """The gradient's tensor (a new one, or `out`) with its pointer and ld."""
+        if out is None:
+            out = self.new(logits.shape, logits.dtype)
+        elif out.shape != logits.shape or out.dtype != logits.dtype:
+            raise ValueError("out must have the logits' shape and dtype")
+        ptr, _, _, _, ld = self.logits(out, "out")
+        return out, ptr, ld
+
+
+def _sequences(launch, t, seq_off):
+    """(sequences, tokens, pointer of the offsets) of a packed 1-D tensor with
+    offsets, a padded 2-D (sequences, length) one, or one 1-D sequence."""
+    if t.dim() == 2 and seq_off is None:
+        return t.shape[0], t.numel(), None
+    if t.dim() != 1:
+        raise ValueError("tokens must be 1-D (packed) or, without seq_off, 2-D (sequences, length)")
+    if seq_off is None:
+        return 1, t.numel(), None
+    if seq_off.dim() != 1 or seq_off.numel() < 1:
+        raise ValueError("seq_off must have the shape (sequences + 1,)")
+    off = launch.use(seq_off, "seq_off", seq_off.shape, (launch.torch.int32,))
+    return seq_off.numel() - 1, t.numel(), off
+
+
+def _done(st):
+    if st < 0:
+        raise IsoError(st)
+
+
+def token_logp(logits, target, *, temperature: float = 1.0, entropy: bool = False, stream=None):
+    """Log-probabilities of the targets under softmax(logits / temperature), row
+    by row: (logp, lse), or (logp, lse, entropies) when entropy.  logits: 2-D
+    f32, f16 or bf16 CUDA tensor with contiguous rows; target: int32 (rows,),
+    negative for ignored rows (outputs 0)."""
+    c = _Launch(logits, stream)
+    t = c.torch
+    ptr, code, rows, vocab, ld = c.logits(logits, "logits")
+    tgt = c.use(target, "target", (rows,), (t.int32,))
+    logp, lse = c.new(rows, t.float32), c.new(rows, t.float32)
+    ent = c.new(rows, t.float32) if entropy else None
+    nb = iso_token_logp_workspace_bytes(rows, vocab, code)
+    ws = c.workspace(nb)
+    _done(iso_token_logp(ptr, code, rows, vocab, ld, tgt, temperature, logp.data_ptr(), lse.data_ptr(),
+                         None if ent is None else ent.data_ptr(), ws.data_ptr(), nb, c.handle))
+    return (logp, lse, ent) if entropy else (logp, lse)
+
+
+def token_logp_vjp(g_logp, logits, target, lse, *, temperature: float = 1.0, entropy=None, g_entropy=None,
+                   out=None, stream=None):
+    """Backward pass of token_logp: the logits' gradient for g_logp (and, with
+    the forward call's entropy, g_entropy).  out may be the logits themselves."""
+    c = _Launch(logits, stream)
+    f32 = (c.torch.float32,)
+    ptr, code, rows, vocab, ld = c.logits(logits, "logits")
+    if (entropy is None) != (g_entropy is None):
+        raise ValueError("entropy and g_entropy go together")
+    args = [c.use(x, name, (rows,), ty) for x, name, ty in (
+        (target, "target", (c.torch.int32,)), (lse, "lse", f32), (entropy, "entropy", f32),
+        (g_logp, "g_logp", f32), (g_entropy, "g_entropy", f32))]
+    grad, gptr, gld = c.grad_of(logits, out)
+    _done(iso_token_logp_vjp(ptr, code, rows, vocab, ld, args[0], temperature, args[1], args[2], args[3],
+                             args[4], gptr, gld, c.handle))
+    return grad
+
+
+def pref_loss(logp, ref_logp, seq_off=None, *, mask=None, beta: float = 0.1, label_smoothing: float = 0.0,
+              squared: bool = False, mean: bool = False, grad: bool = True, grad_scale: float = 1.0,
+              stream=None):
+    """Paired preference loss over token log-probabilities: (loss, pair losses,
+    rewards, gradient of logp or None).  Sequences alternate chosen, rejected:
+    1-D packed by seq_off (int32), or 2-D (2 pairs, length).  ref_logp may be
+    None; mask is a bool or uint8 tensor shaped like logp."""
+    c = _Launch(logp, stream)
+    t = c.torch
+    seqs, tokens, off = _sequences(c, logp, seq_off)
+    if seqs % 2:
+        raise ValueError("sequences must come in pairs")
+    lp = c.use(logp, "logp", logp.shape, (t.float32,))
+    ref = c.use(ref_logp, "ref_logp", logp.shape, (t.float32,))
+    mk = c.use(mask, "mask", logp.shape, (t.bool, t.uint8))
+    pairs = seqs // 2
+    loss, each, reward = c.new((), t.float32), c.new(pairs, t.float32), c.new(seqs, t.float32)
+    g = c.new(logp.shape, t.float32) if grad else None
+    nb = iso_pref_loss_workspace_bytes(tokens, pairs)
+    ws = c.workspace(nb)
+    _done(iso_pref_loss(lp, ref, mk, off, pairs, tokens, beta, label_smoothing, loss.data_ptr(),
+                        each.data_ptr(), reward.data_ptr(), None if g is None else g.data_ptr(), grad_scale,
+                        ws.data_ptr(), nb, c.handle,
+                        (ISO_PREF_SQUARED if squared else 0) | (ISO_PREF_MEAN if mean else 0)))
+    return loss, each, reward, g
+
+
+def _policy_flags(seq_mean, token_adv):
+    return (ISO_POLICY_SEQ_MEAN if seq_mean else 0) | (ISO_POLICY_ADV_TOKEN if token_adv else 0)
+
+
+def policy_loss(logp, old_logp, adv, *, ref_logp=None, mask=None, seq_off=None, clip_lo: float = 0.2,
+                clip_hi: float = 0.2, kl_coef: float = 0.0, seq_mean: bool = False, token_adv: bool = False,
+                norm: float = 0.0, grad: bool = True, grad_scale: float = 1.0, stream=None):
+    """Clipped policy loss over token log-probabilities: (loss (3,) = [loss,
+    policy part, KL], counts (2,) = [tokens, clipped tokens], gradient of logp
+    or None).  Tokens: 1-D packed by seq_off (int32), 2-D (sequences, length),
+    or one 1-D sequence.  adv: one value per sequence, or shaped like logp when
+    token_adv."""
+    c = _Launch(logp, stream)
+    t = c.torch
+    f32 = (t.float32,)
+    seqs, tokens, off = _sequences(c, logp, seq_off)
+    lp, old, ref = (c.use(x, name, logp.shape, f32) for x, name in (
+        (logp, "logp"), (old_logp, "old_logp"), (ref_logp, "ref_logp")))
+    mk = c.use(mask, "mask", logp.shape, (t.bool, t.uint8))
+    av = c.use(adv, "adv", logp.shape if token_adv else (seqs,), f32)
+    loss, counts = c.new(3, t.float32), c.new(2, t.int32)
+    g = c.new(logp.shape, t.float32) if grad else None
+    nb = iso_policy_loss_workspace_bytes(tokens, seqs)
+    ws = c.workspace(nb)
+    _done(iso_policy_loss(lp, old, ref, av, mk, off, seqs, tokens, clip_lo, clip_hi, kl_coef, norm,
+                          loss.data_ptr(), counts.data_ptr(), None if g is None else g.data_ptr(), grad_scale,
+                          ws.data_ptr(), nb, c.handle, _policy_flags(seq_mean, token_adv)))
+    return loss, counts, g
+
+
+def policy_loss_logits(logits, target, old_logp, adv, *, ref_logp=None, seq_off=None, seqs: int = 1,
+                       temperature: float = 1.0, clip_lo: float = 0.2, clip_hi: float = 0.2,
+                       kl_coef: float = 0.0, seq_mean: bool = False, token_adv: bool = False,
+                       norm: float = 0.0, grad: bool = True, grad_scale: float = 1.0, out=None, stream=None):
+    """Clipped policy loss taken from the logits: (loss (3,), counts (2,), logp,
+    gradient of the logits or None).  Rows of logits are tokens, packed by
+    seq_off or `seqs` sequences of one length; rows whose target is negative
+    take no part.  out may be the logits themselves."""
+    c = _Launch(logits, stream)
+    t = c.torch
+    f32 = (t.float32,)
+    ptr, code, rows, vocab, ld = c.logits(logits, "logits")
+    off = None
+    if seq_off is not None:
+        if seq_off.dim() != 1 or seq_off.numel() < 1:
+            raise ValueError("seq_off must have the shape (sequences + 1,)")
+        off = c.use(seq_off, "seq_off", seq_off.shape, (t.int32,))
+        seqs = seq_off.numel() - 1
+    tgt = c.use(target, "target", (rows,), (t.int32,))
+    old, ref = c.use(old_logp, "old_logp", (rows,), f32), c.use(ref_logp, "ref_logp", (rows,), f32)
+    av = c.use(adv, "adv", (rows if token_adv else seqs,), f32)
+    loss, counts, logp = c.new(3, t.float32), c.new(2, t.int32), c.new(rows, t.float32)
+    g, gptr, gld = c.grad_of(logits, out) if grad else (None, None, vocab)
+    nb = iso_policy_loss_logits_workspace_bytes(rows, vocab, seqs, code)
+    ws = c.workspace(nb)
+    _done(iso_policy_loss_logits(ptr, code, rows, vocab, ld, tgt, temperature, old, ref, av, off, seqs,
+                                 clip_lo, clip_hi, kl_coef, norm, loss.data_ptr(), counts.data_ptr(),
+                                 logp.data_ptr(), gptr, gld, grad_scale, ws.data_ptr(), nb, c.handle,
+                                 _policy_flags(seq_mean, token_adv)))
+    return loss, counts, logp, g
