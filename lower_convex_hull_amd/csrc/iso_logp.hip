@@ -8,141 +8,318 @@
 namespace iso {
 namespace {
 
-constexpr int kRowNT = 256;
 constexpr double kLog2e = 1.4426950408889634;
+constexpr double kLn2 = 0.6931471805599453;
 
-// Per-row statistics of x over some of its entries: the maximum m, s = sum
-// exp((x - m)/T) and h = sum exp((x - m)/T) (x - m)/T.
-struct Stat {
-    float m;
-    double s, h;
+// 16 bytes of logits at element alignment: rows of an odd length or stride
+// start anywhere, and global loads and stores need no wider alignment.
+template <typename T>
+struct Wide {
+    static constexpr int N = 16 / sizeof(T);
+    typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
 };
 
-// exp((x - m)/T) with c = log2(e)/T.  m is finite or +infinity (base_of).
-__device__ __forceinline__ float exp_of(float d, float c) { return __builtin_amdgcn_exp2f(d * c); }
+template <typename T>
+__device__ __forceinline__ typename Wide<T>::V load_wide(const T* p) {
+    return *reinterpret_cast<const typename Wide<T>::V*>(p);
+}
+
+// The same with elements at or past `avail` filled with -infinity (they add nothing).
+template <typename T>
+__device__ __forceinline__ typename Wide<T>::V load_part(const T* p, int64_t avail) {
+    typename Wide<T>::V v;
+#pragma unroll
+    for (int i = 0; i < Wide<T>::N; ++i) v[i] = i < avail ? p[i] : (T)-INFINITY;
+    return v;
+}
+
+// exp((x - m)/T) = exp2((x - m) c), c = log2(e)/T.  The difference to the
+// maximum m of what a sum covers comes first: it is exact, or nearly, where the
+// term counts, the largest term is exactly 1, and no finite logit overflows.
+struct Scale {
+    double inv_t, c;
+    float cf;  // c in f32
+};
 
 // The maximum that differences are taken to: 0 where everything so far is
 // -infinity, so that no -infinity minus -infinity arises.
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
-// A difference to the maximum as a factor of h: a masked entry's -infinity is
-// held finite, its product with exp(-infinity) = 0 is then 0.
-__device__ __forceinline__ float held(float d) { return fmaxf(d, -1e30f); }
+// An exponent as a factor of the entropy's sum: a masked entry's -infinity is
+// held finite, its product with exp2(-infinity) = 0 is then 0.
+__device__ __forceinline__ float held(float a) { return fmaxf(a, -1e30f); }
 
-// a and b of the same row joined.
+// Part of a row: its maximum m, the sum s of e = exp2((x - m) c) and the sum h
+// of e times its exponent.  m = -infinity: nothing but -infinity, sums 0.
+struct Stat {
+    double m, s, h;
+};
+
 template <bool ENT>
-__device__ __forceinline__ Stat join(const Stat& a, const Stat& b, double inv_t) {
+__device__ __forceinline__ Stat join(const Stat& a, const Stat& b, double c) {
+    // an infinite maximum's own sums are NaN, and stay
+    const double m = a.m > b.m ? a.m : b.m;
+    const double da = a.m == -INFINITY ? 0.0 : (a.m - m) * c, db = b.m == -INFINITY ? 0.0 : (b.m - m) * c;
+    const double fa = exp2(da), fb = exp2(db);
     Stat o;
-    o.m = fmaxf(a.m, b.m);
-    const float base = base_of(o.m);
-    // where one side holds nothing but -infinity, its sums are 0
-    const double da = (double)held(base_of(a.m) - base) * inv_t, db = (double)held(base_of(b.m) - base) * inv_t;
-    const double fa = a.m == -INFINITY ? 1.0 : exp(da), fb = b.m == -INFINITY ? 1.0 : exp(db);
+    o.m = m;
     o.s = a.s * fa + b.s * fb;
-    o.h = ENT ? (a.h + (a.m == -INFINITY ? 0.0 : a.s * da)) * fa + (b.h + (b.m == -INFINITY ? 0.0 : b.s * db)) * fb
-              : 0.0;
+    o.h = ENT ? (a.h + (da > -1e30 ? a.s * da : 0.0)) * fa + (b.h + (db > -1e30 ? b.s * db : 0.0)) * fb : 0.0;
+    return o;
+}
+
+template <bool ENT>
+__device__ __forceinline__ Stat lane_xor(const Stat& a, int d) {
+    return Stat{__shfl_xor(a.m, d), __shfl_xor(a.s, d), ENT ? __shfl_xor(a.h, d) : 0.0};
+}
+
+// The statistics of x[k0, k1) by a workgroup of NT threads; thread 0 has them.
+// Each thread takes U vectors at a time: their maximum first, then the sums in
+// f32 (U*8 terms at most), joined in f64 to the sums so far, which are scaled
+// when the maximum rises.
+template <typename T, bool ENT, int NT, int U>
+__device__ __forceinline__ Stat row_stat(const T* __restrict__ x, int64_t k0, int64_t k1, const Scale& sc,
+                                         Stat* part) {
+    constexpr int N = Wide<T>::N;
+    float m = -INFINITY;
+    double s = 0.0, h = 0.0;
+    for (int64_t k = k0; k < k1; k += (int64_t)NT * N * U) {
+        typename Wide<T>::V v[U];
+        const int64_t at = k + (int64_t)threadIdx.x * N;
+        if (k + (int64_t)NT * N * U <= k1) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = load_wide<T>(x + at + (int64_t)u * NT * N);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t p = at + (int64_t)u * NT * N;
+                if (p + N <= k1) v[u] = load_wide<T>(x + p);
+                else v[u] = load_part<T>(x + p, k1 - p);
+            }
+        }
+        float bm = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < N; ++i) bm = fmaxf(bm, (float)v[u][i]);
+        if (bm > m) {
+            if (m != -INFINITY) {
+                const float d = held((m - bm) * sc.cf), f = __builtin_amdgcn_exp2f(d);
+                if (ENT) h = (h + s * (double)d) * (double)f;
+                s *= (double)f;
+            }
+            m = bm;
+        }
+        const float base = base_of(m);
+        float fs = 0.0f, fh = 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float a = ((float)v[u][i] - base) * sc.cf;
+                const float e = __builtin_amdgcn_exp2f(a);
+                fs += e;
+                if (ENT) fh = fmaf(e, held(a), fh);
+            }
+        s += (double)fs;
+        if (ENT) h += (double)fh;
+    }
+    Stat a{(double)m, s, h};
+    for (int d = 32; d > 0; d >>= 1) a = join<ENT>(a, lane_xor<ENT>(a, d), sc.c);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int k = 1; k < NT / 64; ++k) a = join<ENT>(a, part[k], sc.c);
+    return a;
+}
+
+// Where the forward pass's results go: f32 outputs (lse, ent may be NULL), or
+// f64 for the loss from the logits (logp64, lse64, else NULL).
+struct LogpOut {
+    float *logp, *lse, *ent;
+    double *logp64, *lse64;
+};
+template <typename T>
+__device__ __forceinline__ void write_row(const LogpOut& o, int64_t r, const T* x, int32_t j, int64_t vocab,
+                                          double inv_t, const Stat& a) {
+    double l = 0.0, en = 0.0, lp = 0.0;
+    if (j >= 0) {
+        const double ls = log(a.s);
+        const bool none = a.m == -INFINITY;
+        l = none ? __builtin_nan("") : a.m * inv_t + ls;
+        en = none ? __builtin_nan("") : ls - kLn2 * (a.h / a.s);
+        lp = none || j >= vocab ? __builtin_nan("") : ((double)(float)x[j] - a.m) * inv_t - ls;
+    }
+    o.logp[r] = (float)lp;
+    if (o.lse) o.lse[r] = (float)l;
+    if (o.ent) o.ent[r] = (float)en;
+    if (o.logp64) o.logp64[r] = lp, o.lse64[r] = l;
+}
+
+// Items of a grid: `count` of them, each taken by one workgroup; the grid is
+// capped and its workgroups then take several.
+constexpr int64_t kMaxGrid = 1 << 20;
+inline dim3 grid_of(int64_t items) { return dim3((unsigned)(items < kMaxGrid ? items : kMaxGrid)); }
+
+// Item = (row, part of it).  With one part a row its outputs are written, else
+// the part's statistics.
+template <typename T, bool ENT, int NT>
+__global__ __launch_bounds__(NT) void k_token_logp(const T* __restrict__ logits, int64_t rows, int64_t vocab,
+                                                   int64_t ld, const int32_t* __restrict__ target, Scale sc,
+                                                   int splits, int64_t chunk, LogpOut o, Stat* __restrict__ parts) {
+    __shared__ Stat part[NT / 64];
+    for (int64_t item = blockIdx.x; item < rows * splits; item += gridDim.x) {
+        const int64_t r = item / splits;
+        const int32_t j = target[r];
+        const T* x = logits + r * ld;
+        Stat a{};
+        if (j >= 0) {
+            const int64_t k0 = (item - r * splits) * chunk, k1 = min(k0 + chunk, vocab);
+            a = row_stat<T, ENT, NT, 4>(x, k0, k1, sc, part);
+        }
+        if (threadIdx.x == 0) {
+            if (splits == 1) write_row(o, r, x, j, vocab, sc.inv_t, a);
+            else parts[item] = a;
+        }
+        __syncthreads();  // part is used again
+    }
+}
+
+// A wave a row: the parts' statistics joined (in a fixed order), the outputs written.
+constexpr int kJoinNT = 256;
+template <typename T, bool ENT>
+__global__ __launch_bounds__(kJoinNT) void k_token_logp_join(const T* __restrict__ logits, int64_t rows,
+                                                             int64_t vocab, int64_t ld,
+                                                             const int32_t* __restrict__ target, Scale sc,
+                                                             int splits, const Stat* __restrict__ parts, LogpOut o) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t r = (int64_t)blockIdx.x * (kJoinNT / 64) + (threadIdx.x >> 6); r < rows;
+         r += (int64_t)gridDim.x * (kJoinNT / 64)) {
+        Stat a{-INFINITY, 0.0, 0.0};
+        for (int k = lane; k < splits; k += 64) a = join<ENT>(a, parts[r * splits + k], sc.c);
+        for (int d = 32; d > 0; d >>= 1) a = join<ENT>(a, lane_xor<ENT>(a, d), sc.c);
+        if (lane == 0) write_row(o, r, logits + r * ld, target[r], vocab, sc.inv_t, a);
+    }
+}
+
+// What a row's gradient takes: p = exp(x/T - lse) as exp2((x - mh) c) times a
+// factor of the row, mh = lse T rounded to f32 (the factor is what that
+// rounding leaves off), folded into a, b: gradient p (a + b (x - mh)).
+struct RowGrad {
+    float mh, a, b, hot;
+};
+__device__ __forceinline__ RowGrad row_grad(double lse, double g, double ent, double g_ent, double inv_t,
+                                            double temperature) {
+    RowGrad o;
+    o.mh = (float)(lse * temperature);
+    const double off = (double)o.mh * inv_t - lse;  // x/T - lse = (x - mh)/T + off
+    const double f = (double)__builtin_amdgcn_exp2f((float)(off * kLog2e)) * inv_t;
+    o.a = (float)(-(g + g_ent * (ent + off)) * f);
+    o.b = (float)(-g_ent * inv_t * f);
+    o.hot = (float)(g * inv_t);
+    return o;
+}
+
+// N elements of a row's gradient from position k on; j: the target's position.
+template <typename T, bool ENT>
+__device__ __forceinline__ typename Wide<T>::V grad_wide(const typename Wide<T>::V& x, int64_t k, int64_t j,
+                                                         const RowGrad& q, float cf) {
+    constexpr int N = Wide<T>::N;
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float d = (float)x[i] - q.mh;
+        const float p = __builtin_amdgcn_exp2f(d * cf);
+        v[i] = ENT ? p * fmaf(q.b, held(d), q.a) : p * q.a;
+    }
+    if ((uint64_t)(j - k) < (uint64_t)N) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (j - k == i) v[i] += q.hot;
+    }
+    typename Wide<T>::V o;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = (T)v[i];
     return o;
 }
 
 template <typename T>
-__device__ __forceinline__ T nan_of() {
-    return (T)__builtin_nanf("");
+__device__ __forceinline__ void store_wide(T* p, const typename Wide<T>::V& v, int64_t avail) {
+    constexpr int N = Wide<T>::N;
+    if (avail >= N) {
+        *reinterpret_cast<typename Wide<T>::V*>(p) = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < avail) p[i] = v[i];
+    }
 }
 
-// A row's outputs from its statistics: lse and entropy.
-__device__ __forceinline__ void finish_row(const Stat& r, double inv_t, double& lse, double& ent) {
-    // nothing but -infinity: s = 0 against base 0
-    const bool none = r.m == -INFINITY;
-    const double ls = log(r.s);
-    lse = none ? __builtin_nan("") : (double)r.m * inv_t + ls;
-    ent = none ? __builtin_nan("") : ls - r.h / r.s;
-}
-
-// One workgroup a row.
-template <typename T, bool ENT>
-__global__ __launch_bounds__(kRowNT) void k_token_logp(const T* __restrict__ logits, int64_t vocab, int64_t ld,
-                                                       const int32_t* __restrict__ target, double inv_t, float c,
-                                                       float* __restrict__ logp, float* __restrict__ lse,
-                                                       float* __restrict__ ent, double* __restrict__ logp64,
-                                                       double* __restrict__ lse64) {
-    __shared__ Stat part[kRowNT / 64];
-    const int64_t r = blockIdx.x;
-    const int32_t j = target[r];
-    if (j < 0) {
-        if (threadIdx.x == 0) {
-            logp[r] = 0.0f;
-            if (lse) lse[r] = 0.0f;
-            if (ENT) ent[r] = 0.0f;
-            if (logp64) logp64[r] = 0.0, lse64[r] = 0.0;
+// The gradient of x[k0, k1) by NT threads, U vectors at a time.
+template <typename T, bool ENT, int NT, int U>
+__device__ __forceinline__ void row_grads(const T* x, T* o, int64_t k0, int64_t k1, int64_t j, const RowGrad& q,
+                                          float cf) {
+    constexpr int N = Wide<T>::N;
+    for (int64_t k = k0; k < k1; k += (int64_t)NT * N * U) {
+        const int64_t at = k + (int64_t)threadIdx.x * N;
+        typename Wide<T>::V v[U];
+        if (k + (int64_t)NT * N * U <= k1) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = load_wide<T>(x + at + (int64_t)u * NT * N);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t p = at + (int64_t)u * NT * N;
+                *reinterpret_cast<typename Wide<T>::V*>(o + p) = grad_wide<T, ENT>(v[u], p, j, q, cf);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t p = at + (int64_t)u * NT * N;
+                if (p + N <= k1) v[u] = load_wide<T>(x + p);
+                else v[u] = load_part<T>(x + p, k1 - p);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t p = at + (int64_t)u * NT * N;
+                store_wide<T>(o + p, grad_wide<T, ENT>(v[u], p, j, q, cf), k1 - p);
+            }
         }
-        return;
-    }
-    const T* x = logits + r * ld;
-    float m = -INFINITY;
-    bool bad = false;
-    for (int64_t k = threadIdx.x; k < vocab; k += kRowNT) {
-        const float v = (float)x[k];
-        m = fmaxf(m, v);
-        bad |= v != v;
-    }
-    const float base = base_of(m);
-    double s = 0.0, h = 0.0;
-    for (int64_t k = threadIdx.x; k < vocab; k += kRowNT) {
-        const float d = (float)x[k] - base;
-        const float e = exp_of(d, c);
-        s += (double)e;
-        if (ENT) h += (double)(e * held(d)) * inv_t;
-    }
-    Stat a{m, bad ? (double)__builtin_nanf("") : s, h};
-    for (int d = 32; d > 0; d >>= 1) {
-        const Stat b{__shfl_xor(a.m, d), __shfl_xor(a.s, d), __shfl_xor(a.h, d)};
-        a = join<ENT>(a, b, inv_t);
-    }
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int k = 1; k < kRowNT / 64; ++k) a = join<ENT>(a, part[k], inv_t);
-        double l, en;
-        finish_row(a, inv_t, l, en);
-        const double lp = j < vocab ? (double)(float)x[j] * inv_t - l : __builtin_nan("");
-        logp[r] = (float)lp;
-        if (lse) lse[r] = (float)l;
-        if (ENT) ent[r] = (float)en;
-        if (logp64) logp64[r] = lp, lse64[r] = l;
     }
 }
 
-// One workgroup a row of the gradient.  With z = x/T - lse: p = exp(z), taken
-// as exp((x - mh)/T) times a factor of the row, mh = lse T rounded to f32.
+// A row's gradient where it is one value: 0 (ignored) or NaN.
+template <typename T, int NT>
+__device__ __forceinline__ void fill_row(T* o, int64_t k0, int64_t k1, T v) {
+    constexpr int N = Wide<T>::N;
+    typename Wide<T>::V w;
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = v;
+    for (int64_t k = k0 + (int64_t)threadIdx.x * N; k < k1; k += (int64_t)NT * N) store_wide<T>(o + k, w, k1 - k);
+}
+
+constexpr int kVjpNT = 256;
+
+// Item = (row, chunk of it).
 template <typename T, bool ENT, typename LSE>
-__global__ __launch_bounds__(kRowNT) void k_logp_vjp(const T* logits, int64_t vocab, int64_t ld,
-                                                     const int32_t* __restrict__ target, double inv_t, float c,
+__global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t rows, int64_t vocab, int64_t ld,
+                                                     const int32_t* __restrict__ target, double inv_t,
+                                                     double temperature, float cf, int splits, int64_t chunk,
                                                      const LSE* __restrict__ lse, const float* __restrict__ ent,
                                                      const float* __restrict__ g_logp,
                                                      const float* __restrict__ g_ent, T* grad, int64_t ldg) {
-    const int64_t r = blockIdx.x;
-    const int32_t j = target[r];
-    const T* x = logits + r * ld;
-    T* o = grad + r * ldg;
-    if (j < 0 || j >= vocab) {
-        const T v = j < 0 ? (T)0.0f : nan_of<T>();
-        for (int64_t k = threadIdx.x; k < vocab; k += kRowNT) o[k] = v;
-        return;
-    }
-    const double l = (double)lse[r], g = (double)g_logp[r];
-    const float mh = (float)(l / inv_t);
-    const double off = (double)mh * inv_t - l;  // x/T - lse = (x - mh)/T + off
-    const double f = exp(off) * inv_t;
-    const double gh = ENT ? (double)g_ent[r] : 0.0;
-    const float a = (float)(-(g + (ENT ? gh * ((double)ent[r] + off) : 0.0)) * f);
-    const float b = ENT ? (float)(-gh * inv_t * f) : 0.0f;
-    const float hot = (float)(g * inv_t);
-    for (int64_t k = threadIdx.x; k < vocab; k += kRowNT) {
-        const float d = (float)x[k] - mh;
-        const float p = exp_of(d, c);
-        float v = ENT ? p * (a + b * held(d)) : p * a;
-        if (k == j) v += hot;
-        o[k] = (T)v;
+    for (int64_t item = blockIdx.x; item < rows * splits; item += gridDim.x) {
+        const int64_t r = item / splits;
+        const int64_t k0 = (item - r * splits) * chunk, k1 = min(k0 + chunk, vocab);
+        const int32_t j = target[r];
+        const T* x = logits + r * ld;
+        T* o = grad + r * ldg;
+        if (j < 0 || j >= vocab) {
+            fill_row<T, kVjpNT>(o, k0, k1, j < 0 ? (T)0.0f : (T)__builtin_nanf(""));
+            continue;
+        }
+        const RowGrad q = row_grad((double)lse[r], (double)g_logp[r], ENT ? (double)ent[r] : 0.0,
+                                   ENT ? (double)g_ent[r] : 0.0, inv_t, temperature);
+        row_grads<T, ENT, kVjpNT, 4>(x, o, k0, k1, j, q, cf);
     }
 }
 
@@ -170,37 +347,72 @@ bool grad_ok(const void* logits, void* grad, int dtype, int64_t rows, int64_t vo
     return !overlap({grad, matrix_bytes(dtype, rows, vocab, ldg)}, {logits, matrix_bytes(dtype, rows, vocab, ld)});
 }
 
+// How a row is split over workgroups: one takes a whole row where there are
+// enough rows, else parts of at least kMinPart bytes.
+struct LogpPlan {
+    int splits;
+    int64_t chunk;
+    size_t bytes;
+};
+constexpr int64_t kLogpGrid = 1024;     // workgroups wanted
+constexpr int64_t kMinPart = 64 << 10;  // bytes of a row
+LogpPlan logp_plan(int64_t rows, int64_t vocab, int dtype) {
+    const int64_t parts = (vocab * (int64_t)size_of(dtype) + kMinPart - 1) / kMinPart;
+    const int64_t want = rows ? (kLogpGrid + rows - 1) / rows : 1;
+    int64_t splits = parts < want ? parts : want;
+    if (splits < 1) splits = 1;
+    // parts of whole steps of a workgroup
+    const int64_t step = 8192;
+    const int64_t chunk = splits == 1 ? vocab : ((vocab + splits - 1) / splits + step - 1) / step * step;
+    splits = (vocab + chunk - 1) / chunk;
+    return LogpPlan{(int)splits, chunk, splits > 1 ? (size_t)rows * (size_t)splits * sizeof(Stat) : 0};
+}
+
+Scale scale_of(double temperature) {
+    const double c = kLog2e / temperature;
+    return Scale{1.0 / temperature, c, (float)c};
+}
+
+template <typename T, bool ENT>
+void start_logp_t(const T* x, int64_t rows, int64_t vocab, int64_t ld, const int32_t* target, double temperature,
+                  const LogpOut& o, const LogpPlan& pl, void* workspace, hipStream_t st) {
+    const Scale sc = scale_of(temperature);
+    Stat* parts = static_cast<Stat*>(workspace);
+    if (rows * pl.splits < kLogpGrid)
+        hipLaunchKernelGGL((k_token_logp<T, ENT, 1024>), grid_of(rows * pl.splits), dim3(1024), 0, st, x, rows, vocab,
+                           ld, target, sc, pl.splits, pl.chunk, o, parts);
+    else
+        hipLaunchKernelGGL((k_token_logp<T, ENT, 256>), grid_of(rows * pl.splits), dim3(256), 0, st, x, rows, vocab, ld,
+                           target, sc, pl.splits, pl.chunk, o, parts);
+    if (pl.splits > 1)
+        hipLaunchKernelGGL((k_token_logp_join<T, ENT>), grid_of((rows + kJoinNT / 64 - 1) / (kJoinNT / 64)),
+                           dim3(kJoinNT), 0, st, x, rows, vocab, ld, target, sc, pl.splits, parts, o);
+}
+
 template <typename T>
 void start_logp(const void* logits, int64_t rows, int64_t vocab, int64_t ld, const int32_t* target,
-                double temperature, float* logp, float* lse, float* ent, double* logp64, double* lse64,
-                hipStream_t st) {
-    const double inv_t = 1.0 / temperature;
-    const float c = (float)(kLog2e * inv_t);
+                double temperature, const LogpOut& o, const LogpPlan& pl, void* workspace, hipStream_t st) {
     const T* x = static_cast<const T*>(logits);
-    const dim3 grid((unsigned)rows), nt(kRowNT);
-    if (ent)
-        hipLaunchKernelGGL((k_token_logp<T, true>), grid, nt, 0, st, x, vocab, ld, target, inv_t, c, logp, lse, ent,
-                           logp64, lse64);
-    else
-        hipLaunchKernelGGL((k_token_logp<T, false>), grid, nt, 0, st, x, vocab, ld, target, inv_t, c, logp, lse, ent,
-                           logp64, lse64);
+    if (o.ent) start_logp_t<T, true>(x, rows, vocab, ld, target, temperature, o, pl, workspace, st);
+    else start_logp_t<T, false>(x, rows, vocab, ld, target, temperature, o, pl, workspace, st);
 }
 
 template <typename T, typename LSE>
 void start_vjp(const void* logits, int64_t rows, int64_t vocab, int64_t ld, const int32_t* target,
                double temperature, const LSE* lse, const float* ent, const float* g_logp, const float* g_ent,
                void* grad, int64_t ldg, hipStream_t st) {
-    const double inv_t = 1.0 / temperature;
-    const float c = (float)(kLog2e * inv_t);
+    const Scale sc = scale_of(temperature);
     const T* x = static_cast<const T*>(logits);
     T* o = static_cast<T*>(grad);
-    const dim3 grid((unsigned)rows), nt(kRowNT);
+    const int64_t chunk = 4 * 4 * kVjpNT * Wide<T>::N;
+    const int splits = (int)((vocab + chunk - 1) / chunk);
+    const dim3 grid = grid_of(rows * splits), nt(kVjpNT);
     if (g_ent)
-        hipLaunchKernelGGL((k_logp_vjp<T, true, LSE>), grid, nt, 0, st, x, vocab, ld, target, inv_t, c, lse, ent,
-                           g_logp, g_ent, o, ldg);
+        hipLaunchKernelGGL((k_logp_vjp<T, true, LSE>), grid, nt, 0, st, x, rows, vocab, ld, target, sc.inv_t, temperature,
+                           sc.cf, splits, chunk, lse, ent, g_logp, g_ent, o, ldg);
     else
-        hipLaunchKernelGGL((k_logp_vjp<T, false, LSE>), grid, nt, 0, st, x, vocab, ld, target, inv_t, c, lse, ent,
-                           g_logp, g_ent, o, ldg);
+        hipLaunchKernelGGL((k_logp_vjp<T, false, LSE>), grid, nt, 0, st, x, rows, vocab, ld, target, sc.inv_t,
+                           temperature, sc.cf, splits, chunk, lse, ent, g_logp, g_ent, o, ldg);
 }
 
 // f called with a value of the logits' type.
@@ -213,15 +425,18 @@ void by_dtype(int dtype, F f) {
 
 // Workspace of iso_policy_loss_logits.
 struct HeadPlan {
-    size_t off_lp, off_lse, off_g, off_policy, bytes;
+    LogpPlan logp;
+    size_t off_lp, off_lse, off_g, off_parts, off_policy, bytes;
 };
-HeadPlan head_plan(int64_t rows, int64_t seqs) {
+HeadPlan head_plan(int64_t rows, int64_t vocab, int64_t seqs, int dtype) {
     HeadPlan p;
+    p.logp = logp_plan(rows, vocab, dtype);
     const size_t n = (size_t)rows;
     p.off_lp = 0;
     p.off_lse = align_up(n * 8);
     p.off_g = p.off_lse + align_up(n * 8);
-    p.off_policy = p.off_g + align_up(n * 4);
+    p.off_parts = p.off_g + align_up(n * 4);
+    p.off_policy = p.off_parts + align_up(p.logp.bytes);
     p.bytes = p.off_policy + policy_workspace(rows, seqs);
     return p;
 }
@@ -232,10 +447,9 @@ HeadPlan head_plan(int64_t rows, int64_t seqs) {
 extern "C" {
 
 size_t iso_token_logp_workspace_bytes(int64_t rows, int64_t vocab, int dtype) {
-    (void)rows;
-    (void)vocab;
-    (void)dtype;
-    return 0;
+    if (rows < 0 || rows > 0x7fffffffLL || vocab < 1 || vocab > (1LL << 30) || dtype < ISO_DT_F32 || dtype > ISO_DT_BF16)
+        return 0;
+    return iso::logp_plan(rows, vocab, dtype).bytes;
 }
 
 int iso_token_logp(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld, const int32_t* target,
@@ -255,8 +469,8 @@ int iso_token_logp(const void* logits, int dtype, int64_t rows, int64_t vocab, i
     if (!aligned(workspace, 256)) return ISO_ERR_ARG;
     hipStream_t st = static_cast<hipStream_t>(stream);
     by_dtype(dtype, [&](auto v) {
-        start_logp<decltype(v)>(logits, rows, vocab, ld, target, temperature, logp, lse, entropy, nullptr, nullptr,
-                                st);
+        start_logp<decltype(v)>(logits, rows, vocab, ld, target, temperature, {logp, lse, entropy, nullptr, nullptr},
+                                logp_plan(rows, vocab, dtype), workspace, st);
     });
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
@@ -284,10 +498,10 @@ int iso_token_logp_vjp(const void* logits, int dtype, int64_t rows, int64_t voca
 }
 
 size_t iso_policy_loss_logits_workspace_bytes(int64_t rows, int64_t vocab, int64_t seqs, int dtype) {
-    (void)vocab;
-    (void)dtype;
-    if (rows < 0 || seqs < 0) return 0;
-    return iso::head_plan(rows, seqs).bytes;
+    if (rows < 0 || rows > 0x7fffffffLL || vocab < 1 || vocab > (1LL << 30) || seqs < 0 || seqs > 0x7fffffffLL ||
+        dtype < ISO_DT_F32 || dtype > ISO_DT_BF16)
+        return 0;
+    return iso::head_plan(rows, vocab, seqs, dtype).bytes;
 }
 
 int iso_policy_loss_logits(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
@@ -311,7 +525,7 @@ int iso_policy_loss_logits(const void* logits, int dtype, int64_t rows, int64_t 
     const Span lg{logits, matrix_bytes(dtype, rows, vocab, ld)};
     if (overlap(lg, out[0]) || overlap(lg, out[1]) || overlap(lg, out[2])) return ISO_ERR_ARG;
     if (!aligned(target, 4) || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(logp, 4)) return ISO_ERR_ARG;
-    const HeadPlan pl = head_plan(rows, seqs);
+    const HeadPlan pl = head_plan(rows, vocab, seqs, dtype);
     if (!workspace || workspace_bytes < pl.bytes) return ISO_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return ISO_ERR_ARG;
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -323,8 +537,8 @@ int iso_policy_loss_logits(const void* logits, int dtype, int64_t rows, int64_t 
     const Seqs sq{seq_off, seqs, rows, seqs ? rows / seqs : 0};
     if (rows)
         by_dtype(dtype, [&](auto v) {
-            start_logp<decltype(v)>(logits, rows, vocab, ld, target, temperature, logp, nullptr, nullptr, lp64, lse64,
-                                    st);
+            start_logp<decltype(v)>(logits, rows, vocab, ld, target, temperature,
+                                    {logp, nullptr, nullptr, lp64, lse64}, pl.logp, ws + pl.off_parts, st);
         });
     if (launch_policy<double>(p, lp64, nullptr, target, sq, loss, counts, grad ? g : nullptr, ws + pl.off_policy,
                               st) != hipSuccess)

@@ -31,7 +31,7 @@ def token_logp(x, target, temperature=1.0):
             lse = m + np.log(s)
             p = e / s
             zd = np.where(p > 0, d, 0.0)
-            out[0, r] = z[t] - lse if t < vocab else np.nan
+            out[0, r] = d[t] - np.log(s) if t < vocab else np.nan
             out[1, r] = lse
             out[2, r] = np.log(s) - (p * zd).sum()
             out[3, r] = (p * (3 * np.abs(zd) + 2)).sum() + 32
