@@ -55,22 +55,28 @@ struct Stat {
     double m, s, h;
 };
 
+// a brought to the maximum m of more: its sums scaled.
 template <bool ENT>
-__device__ __forceinline__ Stat join(const Stat& a, const Stat& b, double c) {
-    // an infinite maximum's own sums are NaN, and stay
-    const double m = a.m > b.m ? a.m : b.m;
-    const double da = a.m == -INFINITY ? 0.0 : (a.m - m) * c, db = b.m == -INFINITY ? 0.0 : (b.m - m) * c;
-    const double fa = exp2(da), fb = exp2(db);
-    Stat o;
-    o.m = m;
-    o.s = a.s * fa + b.s * fb;
-    o.h = ENT ? (a.h + (da > -1e30 ? a.s * da : 0.0)) * fa + (b.h + (db > -1e30 ? b.s * db : 0.0)) * fb : 0.0;
-    return o;
+__device__ __forceinline__ void rebase(Stat& a, double m, const Scale& sc) {
+    // an infinite or NaN maximum's sums are NaN, and stay
+    const float d = a.m == -INFINITY ? 0.0f : held((float)((a.m - m) * sc.c));
+    const double f = (double)__builtin_amdgcn_exp2f(d);
+    if (ENT) a.h = (a.h + a.s * (double)d) * f;
+    a.s *= f;
+    a.m = m;
 }
 
+// Every lane's statistics joined (the same in every lane): the maximum first,
+// then one scaling each, then plain sums.
 template <bool ENT>
-__device__ __forceinline__ Stat lane_xor(const Stat& a, int d) {
-    return Stat{__shfl_xor(a.m, d), __shfl_xor(a.s, d), ENT ? __shfl_xor(a.h, d) : 0.0};
+__device__ __forceinline__ Stat wave_join(Stat a, const Scale& sc) {
+    float m = (float)a.m;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    rebase<ENT>(a, (double)m, sc);
+    a.s = wave_sum(a.s);
+    if (ENT) a.h = wave_sum(a.h);
+    return a;
 }
 
 // The statistics of x[k0, k1) by a workgroup of NT threads; thread 0 has them.
@@ -124,12 +130,12 @@ __device__ __forceinline__ Stat row_stat(const T* __restrict__ x, int64_t k0, in
         s += (double)fs;
         if (ENT) h += (double)fh;
     }
-    Stat a{(double)m, s, h};
-    for (int d = 32; d > 0; d >>= 1) a = join<ENT>(a, lane_xor<ENT>(a, d), sc.c);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
+    Stat a = wave_join<ENT>(Stat{(double)m, s, h}, sc);
+    if (NT == 64) return a;
+    const int lane = threadIdx.x & 63;
+    if (lane == 0) part[threadIdx.x >> 6] = a;
     __syncthreads();
-    if (threadIdx.x == 0)
-        for (int k = 1; k < NT / 64; ++k) a = join<ENT>(a, part[k], sc.c);
+    if (threadIdx.x < 64) a = wave_join<ENT>(lane < NT / 64 ? part[lane] : Stat{-INFINITY, 0.0, 0.0}, sc);
     return a;
 }
 
@@ -196,8 +202,15 @@ __global__ __launch_bounds__(kJoinNT) void k_token_logp_join(const T* __restrict
     for (int64_t r = (int64_t)blockIdx.x * (kJoinNT / 64) + (threadIdx.x >> 6); r < rows;
          r += (int64_t)gridDim.x * (kJoinNT / 64)) {
         Stat a{-INFINITY, 0.0, 0.0};
-        for (int k = lane; k < splits; k += 64) a = join<ENT>(a, parts[r * splits + k], sc.c);
-        for (int d = 32; d > 0; d >>= 1) a = join<ENT>(a, lane_xor<ENT>(a, d), sc.c);
+        for (int k = lane; k < splits; k += 64) {
+            Stat b = parts[r * splits + k];
+            const double m = a.m > b.m ? a.m : b.m;
+            rebase<ENT>(a, m, sc);
+            rebase<ENT>(b, m, sc);
+            a.s += b.s;
+            if (ENT) a.h += b.h;
+        }
+        a = wave_join<ENT>(a, sc);
         if (lane == 0) write_row(o, r, logits + r * ld, target[r], vocab, sc.inv_t, a);
     }
 }

@@ -65,8 +65,8 @@ struct PolicyTerm {
     double pg, kl, slope;  // slope: derivative of pg + kl_coef kl in logp
     bool over;             // held by the clip
 };
-__device__ __forceinline__ PolicyTerm policy_term(const Policy& p, double lp, int64_t t, double a) {
-    const double d = lp - (double)p.old_logp[t];
+__device__ __forceinline__ PolicyTerm policy_term(const Policy& p, double lp, double old, double ref, double a) {
+    const double d = lp - old;
     PolicyTerm o;
     o.over = a > 0.0 ? d > p.up : a < 0.0 ? d < p.low : false;
     const double ra = exp(d) * a;
@@ -74,7 +74,7 @@ __device__ __forceinline__ PolicyTerm policy_term(const Policy& p, double lp, in
     o.slope = o.over ? 0.0 : -ra;
     o.kl = 0.0;
     if (p.ref_logp) {
-        const double u = (double)p.ref_logp[t] - lp;
+        const double u = ref - lp;
         const double em = expm1(u);
         o.kl = em - u;
         o.slope -= p.kl_coef * em;
