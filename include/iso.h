@@ -353,7 +353,8 @@ int iso_token_logp_vjp(const void* logits, int dtype, int64_t rows, int64_t voca
  * [0, tokens]: nothing outside the arrays is touched, the outputs are then
  * unspecified.  mask [tokens] bytes, device, or NULL: a token with mask 0
  * takes no part, whatever its values (NaN included), and its gradient is 0.
- * A sequence may be empty or wholly masked.  tokens is at most 2^31 - 1.
+ * A sequence may be empty or wholly masked.  Tokens without a sequence are an
+ * error.  tokens is at most 2^31 - 1.
  *
  * iso_pref_loss - the paired preference loss.  Sequence 2i is pair i's chosen
  * answer, 2i+1 its rejected one.  With s_q the sum over q's tokens of

@@ -529,8 +529,8 @@ PolicyPlan policy_plan(int64_t tokens, int64_t seqs) {
 bool seqs_ok(const int32_t* off, int64_t seqs, int64_t tokens) {
     if (seqs < 0 || tokens < 0 || tokens > 0x7fffffffLL || seqs > 0x7fffffffLL) return false;
     if (!aligned(off, 4)) return false;
-    if (!off && (seqs ? tokens % seqs != 0 : tokens != 0)) return false;
-    return true;
+    if (seqs == 0) return tokens == 0;  // tokens have to belong to a sequence
+    return off || tokens % seqs == 0;
 }
 
 }  // namespace

@@ -155,6 +155,13 @@ def test_policy_logits_refuses_places(mem):
     assert iso.iso_policy_loss_logits(*head_args(mem, ws=None)) == WS
 
 
+def test_tokens_without_sequences_are_refused(mem):
+    """Offsets of no sequence hold no token."""
+    assert iso.iso_pref_loss(*pref_args(mem, pairs=0)) == ARG
+    assert iso.iso_policy_loss(*policy_args(mem, seqs=0)) == ARG
+    assert iso.iso_policy_loss_logits(*head_args(mem, seqs=0)) == ARG
+
+
 def test_binding_refuses_cpu_tensors():
     import torch
 
