@@ -139,27 +139,32 @@ __device__ __forceinline__ Stat row_stat(const T* __restrict__ x, int64_t k0, in
     return a;
 }
 
-// Where the forward pass's results go: f32 outputs (lse, ent may be NULL), or
-// f64 for the loss from the logits (logp64, lse64, else NULL).
+// A row's log-sum and its target's log-probability from its statistics and the
+// target's logit; NaN where nothing but -infinity is in the row, or (logp) the
+// target is outside it.
+struct RowLogp {
+    double lse, logp, entropy;
+};
+template <typename T>
+__device__ __forceinline__ RowLogp row_logp(const T* x, int32_t j, int64_t vocab, double inv_t, const Stat& a) {
+    const double ls = log(a.s);
+    const bool none = a.m == -INFINITY;
+    return RowLogp{none ? __builtin_nan("") : a.m * inv_t + ls,
+                   none || j >= vocab ? __builtin_nan("") : ((double)(float)x[j] - a.m) * inv_t - ls,
+                   none ? __builtin_nan("") : ls - kLn2 * (a.h / a.s)};
+}
+
+// Where the forward pass's results go (ent may be NULL).
 struct LogpOut {
     float *logp, *lse, *ent;
-    double *logp64, *lse64;
 };
 template <typename T>
 __device__ __forceinline__ void write_row(const LogpOut& o, int64_t r, const T* x, int32_t j, int64_t vocab,
                                           double inv_t, const Stat& a) {
-    double l = 0.0, en = 0.0, lp = 0.0;
-    if (j >= 0) {
-        const double ls = log(a.s);
-        const bool none = a.m == -INFINITY;
-        l = none ? __builtin_nan("") : a.m * inv_t + ls;
-        en = none ? __builtin_nan("") : ls - kLn2 * (a.h / a.s);
-        lp = none || j >= vocab ? __builtin_nan("") : ((double)(float)x[j] - a.m) * inv_t - ls;
-    }
-    o.logp[r] = (float)lp;
-    if (o.lse) o.lse[r] = (float)l;
-    if (o.ent) o.ent[r] = (float)en;
-    if (o.logp64) o.logp64[r] = lp, o.lse64[r] = l;
+    const RowLogp v = j >= 0 ? row_logp(x, j, vocab, inv_t, a) : RowLogp{0.0, 0.0, 0.0};
+    o.logp[r] = (float)v.logp;
+    o.lse[r] = (float)v.lse;
+    if (o.ent) o.ent[r] = (float)v.entropy;
 }
 
 // Items of a grid: `count` of them, each taken by one workgroup; the grid is
@@ -313,11 +318,11 @@ __device__ __forceinline__ void fill_row(T* o, int64_t k0, int64_t k1, T v) {
 constexpr int kVjpNT = 256;
 
 // Item = (row, chunk of it).
-template <typename T, bool ENT, typename LSE>
+template <typename T, bool ENT>
 __global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t rows, int64_t vocab, int64_t ld,
                                                      const int32_t* __restrict__ target, double inv_t,
                                                      double temperature, float cf, int splits, int64_t chunk,
-                                                     const LSE* __restrict__ lse, const float* __restrict__ ent,
+                                                     const float* __restrict__ lse, const float* __restrict__ ent,
                                                      const float* __restrict__ g_logp,
                                                      const float* __restrict__ g_ent, T* grad, int64_t ldg) {
     for (int64_t item = blockIdx.x; item < rows * splits; item += gridDim.x) {
@@ -334,6 +339,57 @@ __global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t ro
                                    ENT ? (double)g_ent[r] : 0.0, inv_t, temperature);
         row_grads<T, ENT, kVjpNT, 4>(x, o, k0, k1, j, q, cf);
     }
+}
+
+// The policy loss from the logits, a row of a workgroup at a time: its
+// statistics, its token's terms, and its gradient, for which the row is read
+// again while the last-level cache may still have it.  Every row's weight and
+// advantage are known before (they depend on the targets alone).
+template <typename T, int NT, int U>
+__global__ __launch_bounds__(NT, 8) void k_policy_rows(const T* logits, int64_t rows, int64_t vocab, int64_t ld,
+                                                       const int32_t* __restrict__ target, Scale sc,
+                                                       double temperature, Policy p,
+                                                       const RowTerm* __restrict__ terms, float* __restrict__ logp,
+                                                       T* grad, int64_t ldg, PolicySums* __restrict__ sums) {
+    __shared__ Stat part[NT / 64];
+    __shared__ double of_row[2];  // log-sum, gradient of the token's logp
+    __shared__ PolicySums total;  // thread 0's
+    if (threadIdx.x == 0) total = PolicySums{0.0, 0.0, 0, 0};
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const int32_t j = target[r];
+        const T* x = logits + r * ld;
+        T* o = grad + r * ldg;
+        if (j < 0) {
+            if (threadIdx.x == 0) logp[r] = 0.0f;
+            if (grad) fill_row<T, NT>(o, 0, vocab, (T)0.0f);
+            continue;
+        }
+        const Stat a = row_stat<T, false, NT, U>(x, 0, vocab, sc, part);
+        if (threadIdx.x == 0) {
+            const RowLogp v = row_logp(x, j, vocab, sc.inv_t, a);
+            const RowTerm t = terms[r];
+            const PolicyTerm k = policy_term(p, v.logp, (double)p.old_logp[r], p.ref_logp ? (double)p.ref_logp[r] : 0.0,
+                                             (double)t.adv);
+            logp[r] = (float)v.logp;
+            total.pg += t.w * k.pg;
+            total.kl += t.w * k.kl;
+            total.live += 1;
+            total.over += k.over ? 1 : 0;
+            of_row[0] = v.lse;
+            of_row[1] = k.slope * (t.w * p.grad_scale);
+        }
+        __syncthreads();
+        if (grad) {
+            if (j >= vocab) {
+                fill_row<T, NT>(o, 0, vocab, (T)__builtin_nanf(""));
+            } else {
+                const RowGrad q = row_grad(of_row[0], of_row[1], 0.0, 0.0, sc.inv_t, temperature);
+                row_grads<T, false, NT, U>(x, o, 0, vocab, j, q, sc.cf);
+            }
+        }
+        __syncthreads();  // part and of_row are used again
+    }
+    if (threadIdx.x == 0) sums[blockIdx.x] = total;
 }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -410,9 +466,9 @@ void start_logp(const void* logits, int64_t rows, int64_t vocab, int64_t ld, con
     else start_logp_t<T, false>(x, rows, vocab, ld, target, temperature, o, pl, workspace, st);
 }
 
-template <typename T, typename LSE>
+template <typename T>
 void start_vjp(const void* logits, int64_t rows, int64_t vocab, int64_t ld, const int32_t* target,
-               double temperature, const LSE* lse, const float* ent, const float* g_logp, const float* g_ent,
+               double temperature, const float* lse, const float* ent, const float* g_logp, const float* g_ent,
                void* grad, int64_t ldg, hipStream_t st) {
     const Scale sc = scale_of(temperature);
     const T* x = static_cast<const T*>(logits);
@@ -421,10 +477,10 @@ void start_vjp(const void* logits, int64_t rows, int64_t vocab, int64_t ld, cons
     const int splits = (int)((vocab + chunk - 1) / chunk);
     const dim3 grid = grid_of(rows * splits), nt(kVjpNT);
     if (g_ent)
-        hipLaunchKernelGGL((k_logp_vjp<T, true, LSE>), grid, nt, 0, st, x, rows, vocab, ld, target, sc.inv_t, temperature,
+        hipLaunchKernelGGL((k_logp_vjp<T, true>), grid, nt, 0, st, x, rows, vocab, ld, target, sc.inv_t, temperature,
                            sc.cf, splits, chunk, lse, ent, g_logp, g_ent, o, ldg);
     else
-        hipLaunchKernelGGL((k_logp_vjp<T, false, LSE>), grid, nt, 0, st, x, rows, vocab, ld, target, sc.inv_t,
+        hipLaunchKernelGGL((k_logp_vjp<T, false>), grid, nt, 0, st, x, rows, vocab, ld, target, sc.inv_t,
                            temperature, sc.cf, splits, chunk, lse, ent, g_logp, g_ent, o, ldg);
 }
 
@@ -436,22 +492,35 @@ void by_dtype(int dtype, F f) {
     else f(__bf16{});
 }
 
-// Workspace of iso_policy_loss_logits.
+// Workspace and grid of iso_policy_loss_logits.
+constexpr int64_t kHeadGrid = 2048;
 struct HeadPlan {
-    LogpPlan logp;
-    size_t off_lp, off_lse, off_g, off_parts, off_policy, bytes;
+    int grid;
+    size_t off_terms, off_sums, off_weights, bytes;
 };
-HeadPlan head_plan(int64_t rows, int64_t vocab, int64_t seqs, int dtype) {
+HeadPlan head_plan(int64_t rows, int64_t seqs) {
     HeadPlan p;
-    p.logp = logp_plan(rows, vocab, dtype);
-    const size_t n = (size_t)rows;
-    p.off_lp = 0;
-    p.off_lse = align_up(n * 8);
-    p.off_g = p.off_lse + align_up(n * 8);
-    p.off_parts = p.off_g + align_up(n * 4);
-    p.off_policy = p.off_parts + align_up(p.logp.bytes);
-    p.bytes = p.off_policy + policy_workspace(rows, seqs);
+    p.grid = (int)(rows < kHeadGrid ? rows : kHeadGrid);
+    p.off_terms = 0;
+    p.off_sums = align_up((size_t)rows * sizeof(RowTerm));
+    p.off_weights = p.off_sums + align_up((size_t)p.grid * sizeof(PolicySums));
+    p.bytes = p.off_weights + row_terms_workspace(rows, seqs);
     return p;
+}
+
+template <typename T>
+void start_rows(const void* logits, int64_t rows, int64_t vocab, int64_t ld, const int32_t* target,
+                double temperature, const Policy& p, const RowTerm* terms, float* logp, void* grad, int64_t ldg,
+                PolicySums* sums, int grid, hipStream_t st) {
+    const T* x = static_cast<const T*>(logits);
+    T* o = static_cast<T*>(grad);
+    const Scale sc = scale_of(temperature);
+    if (vocab * (int64_t)sizeof(T) >= 32 << 10)
+        hipLaunchKernelGGL((k_policy_rows<T, 1024, 4>), dim3(grid), dim3(1024), 0, st, x, rows, vocab, ld, target, sc,
+                           temperature, p, terms, logp, o, ldg, sums);
+    else
+        hipLaunchKernelGGL((k_policy_rows<T, 256, 4>), dim3(grid), dim3(256), 0, st, x, rows, vocab, ld, target, sc,
+                           temperature, p, terms, logp, o, ldg, sums);
 }
 
 }  // namespace
@@ -482,7 +551,7 @@ int iso_token_logp(const void* logits, int dtype, int64_t rows, int64_t vocab, i
     if (!aligned(workspace, 256)) return ISO_ERR_ARG;
     hipStream_t st = static_cast<hipStream_t>(stream);
     by_dtype(dtype, [&](auto v) {
-        start_logp<decltype(v)>(logits, rows, vocab, ld, target, temperature, {logp, lse, entropy, nullptr, nullptr},
+        start_logp<decltype(v)>(logits, rows, vocab, ld, target, temperature, {logp, lse, entropy},
                                 logp_plan(rows, vocab, dtype), workspace, st);
     });
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
@@ -514,7 +583,7 @@ size_t iso_policy_loss_logits_workspace_bytes(int64_t rows, int64_t vocab, int64
     if (rows < 0 || rows > 0x7fffffffLL || vocab < 1 || vocab > (1LL << 30) || seqs < 0 || seqs > 0x7fffffffLL ||
         dtype < ISO_DT_F32 || dtype > ISO_DT_BF16)
         return 0;
-    return iso::head_plan(rows, vocab, seqs, dtype).bytes;
+    return iso::head_plan(rows, seqs).bytes;
 }
 
 int iso_policy_loss_logits(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
@@ -538,30 +607,23 @@ int iso_policy_loss_logits(const void* logits, int dtype, int64_t rows, int64_t 
     const Span lg{logits, matrix_bytes(dtype, rows, vocab, ld)};
     if (overlap(lg, out[0]) || overlap(lg, out[1]) || overlap(lg, out[2])) return ISO_ERR_ARG;
     if (!aligned(target, 4) || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(logp, 4)) return ISO_ERR_ARG;
-    const HeadPlan pl = head_plan(rows, vocab, seqs, dtype);
+    const HeadPlan pl = head_plan(rows, seqs);
     if (!workspace || workspace_bytes < pl.bytes) return ISO_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return ISO_ERR_ARG;
     hipStream_t st = static_cast<hipStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
-    double* lp64 = reinterpret_cast<double*>(ws + pl.off_lp);
-    double* lse64 = reinterpret_cast<double*>(ws + pl.off_lse);
-    float* g = reinterpret_cast<float*>(ws + pl.off_g);
+    RowTerm* terms = reinterpret_cast<RowTerm*>(ws + pl.off_terms);
+    PolicySums* sums = reinterpret_cast<PolicySums*>(ws + pl.off_sums);
     const Policy p = make_policy(old_logp, ref_logp, adv, clip_lo, clip_hi, kl_coef, norm, grad_scale, flags);
-    const Seqs sq{seq_off, seqs, rows, seqs ? rows / seqs : 0};
-    if (rows)
+    if (rows) {
+        if (launch_row_terms(p, target, make_seqs(seq_off, seqs, rows), terms, ws + pl.off_weights, st) != hipSuccess)
+            return ISO_ERR_HIP;
         by_dtype(dtype, [&](auto v) {
-            start_logp<decltype(v)>(logits, rows, vocab, ld, target, temperature,
-                                    {logp, nullptr, nullptr, lp64, lse64}, pl.logp, ws + pl.off_parts, st);
+            start_rows<decltype(v)>(logits, rows, vocab, ld, target, temperature, p, terms, logp, grad, ld_grad, sums,
+                                    pl.grid, st);
         });
-    if (launch_policy<double>(p, lp64, nullptr, target, sq, loss, counts, grad ? g : nullptr, ws + pl.off_policy,
-                              st) != hipSuccess)
-        return ISO_ERR_HIP;
-    if (rows && grad)
-        by_dtype(dtype, [&](auto v) {
-            start_vjp<decltype(v)>(logits, rows, vocab, ld, target, temperature, lse64, nullptr, g, nullptr, grad,
-                                   ld_grad, st);
-        });
-    return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
+    }
+    return launch_policy_out(p, sums, pl.grid, loss, counts, st) == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 
 }  // extern "C"

@@ -1,61 +1,55 @@
 // Losses over tokens' log-probabilities, with their gradients: the paired
 // preference loss and the clipped policy loss with a KL term (formulas in
 // iso.h).  Both are sums over sequences of tokens followed by one value per
-// token; every sum is f64, without atomics.
+// token; every sum of values is f64, in a fixed order, without atomics.
 #include "../../include/iso.h"
 #include "iso_losses.hpp"
 
 namespace iso {
 namespace {
 
-constexpr int kLossNT = 256;       // threads of a workgroup over many tokens: four waves, a span each
-constexpr int kSpan = 1024;        // tokens of a wave at a time: 16 a lane, in four groups of four
-constexpr int kOneNT = 1024;       // the one workgroup of a small call
+constexpr int kLossNT = 256;        // threads of a workgroup over many tokens: four waves, a span each
+constexpr int kSpanG = 4;           // a wave's span: 4 groups of 256 tokens, 4 a lane in each
+constexpr int kTermG = 2;           // the same where the policy's terms are computed, which take more registers
+constexpr int kOneNT = 1024;        // the one workgroup of a small call, whose spans are one group
 constexpr int64_t kOneMax = 16384;  // tokens (and sequences) up to which one workgroup takes the whole call
 
-// A lane's 16 tokens of a span: group g holds tokens at(g) .. at(g)+3.
+// A span of G groups and a lane's tokens of it: group g holds tokens at(g) .. at(g)+3.
+template <int G>
 struct Place {
-    int64_t p0, p1;  // the span's tokens
+    uint32_t p0, p1;  // the span's tokens
     int lane;
-    __device__ __forceinline__ Place(int64_t span, int64_t tokens) {
+    __device__ __forceinline__ Place(uint32_t span, uint32_t tokens) {
         lane = threadIdx.x & 63;
-        p0 = span * kSpan;
-        p1 = min(p0 + kSpan, tokens);
+        p0 = span * (256u * G);
+        p1 = min(p0 + 256u * G, tokens);
     }
-    __device__ __forceinline__ int64_t at(int g) const { return p0 + g * 256 + lane * 4; }
+    __device__ __forceinline__ uint32_t at(int g) const { return p0 + g * 256u + lane * 4u; }
 };
 
 typedef float Float4 __attribute__((ext_vector_type(4), aligned(4)));
 
-__device__ __forceinline__ void load16(const float* __restrict__ p, const Place& w, float (&v)[16]) {
+// The four values from t on, those at or past `end` 0.
+__device__ __forceinline__ void load4(const float* __restrict__ p, uint32_t t, uint32_t end, float* v) {
+    if (t + 4 <= end) {
+        const Float4 x = *reinterpret_cast<const Float4*>(p + t);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int64_t t = w.at(g);
-        if (t + 4 <= w.p1) {
-            const Float4 x = *reinterpret_cast<const Float4*>(p + t);
+        for (int i = 0; i < 4; ++i) v[i] = x[i];
+    } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[4 * g + i] = x[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[4 * g + i] = t + i < w.p1 ? p[t + i] : 0.0f;
-        }
+        for (int i = 0; i < 4; ++i) v[i] = t + i < end ? p[t + i] : 0.0f;
     }
 }
-
-__device__ __forceinline__ void store16(float* __restrict__ p, const Place& w, const float (&v)[16]) {
+__device__ __forceinline__ void store4(float* __restrict__ p, uint32_t t, uint32_t end, const float* v) {
+    if (t + 4 <= end) {
+        Float4 x;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int64_t t = w.at(g);
-        if (t + 4 <= w.p1) {
-            Float4 x;
+        for (int i = 0; i < 4; ++i) x[i] = v[i];
+        *reinterpret_cast<Float4*>(p + t) = x;
+    } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = v[4 * g + i];
-            *reinterpret_cast<Float4*>(p + t) = x;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (t + i < w.p1) p[t + i] = v[4 * g + i];
-        }
+        for (int i = 0; i < 4; ++i)
+            if (t + i < end) p[t + i] = v[i];
     }
 }
 
@@ -63,122 +57,273 @@ __device__ __forceinline__ void store16(float* __restrict__ p, const Place& w, c
 struct Live {
     const uint8_t* mask;
     const int32_t* target;
-    __device__ __forceinline__ bool all() const { return !mask && !target; }
-    // bit k: the lane's token k takes part
-    __device__ __forceinline__ uint32_t bits(const Place& w) const {
+    __host__ __device__ __forceinline__ bool all() const { return !mask && !target; }
+    // bit i: token t + i takes part
+    __device__ __forceinline__ uint32_t bits4(uint32_t t, uint32_t end) const {
         uint32_t b = 0;
+        if (t + 4 <= end) {
+            if (all()) return 15u;
+            if (mask) {
+                uint32_t x;
+                __builtin_memcpy(&x, mask + t, 4);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int64_t t = w.at(g);
-            if (t + 4 <= w.p1) {
-                if (mask) {
-                    uint32_t x;
-                    __builtin_memcpy(&x, mask + t, 4);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) b |= ((x >> (8 * i)) & 255u) ? 1u << (4 * g + i) : 0u;
-                } else if (target) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) b |= target[t + i] >= 0 ? 1u << (4 * g + i) : 0u;
-                } else {
-                    b |= 15u << (4 * g);
-                }
+                for (int i = 0; i < 4; ++i) b |= ((x >> (8 * i)) & 255u) ? 1u << i : 0u;
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (t + i < w.p1 && (!mask || mask[t + i]) && (!target || target[t + i] >= 0))
-                        b |= 1u << (4 * g + i);
+                for (int i = 0; i < 4; ++i) b |= target[t + i] >= 0 ? 1u << i : 0u;
             }
+            return b;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (t + i < end && (!mask || mask[t + i]) && (!target || target[t + i] >= 0)) b |= 1u << i;
+        return b;
+    }
+    // bit 4g + i: the lane's token i of group g
+    template <int G>
+    __device__ __forceinline__ uint32_t bits(const Place<G>& w) const {
+        uint32_t b = 0;
+#pragma unroll
+        for (int g = 0; g < G; ++g) b |= bits4(w.at(g), w.p1) << (4 * g);
         return b;
     }
 };
 
-// The bits of a lane's tokens in [a, b).
-__device__ __forceinline__ uint32_t inside(const Place& w, int64_t a, int64_t b) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int lo = (int)max((int64_t)0, min((int64_t)4, a - w.at(g)));
-        const int hi = (int)max((int64_t)0, min((int64_t)4, b - w.at(g)));
-        m |= (((1u << hi) - 1u) & ~((1u << lo) - 1u)) << (4 * g);
-    }
-    return m;
-}
-
 // The sequence that holds token p: the last one that begins at or before it.
 // All lanes of a wave together: 64 places are looked at in each round.
-__device__ __forceinline__ int64_t find_seq(const Seqs& sq, int64_t p) {
+__device__ __forceinline__ uint32_t find_seq(const Seqs& sq, uint32_t p) {
     if (!sq.off) return p / sq.len;
-    const int lane = threadIdx.x & 63;
-    int64_t lo = 0, hi = sq.n;
+    const uint32_t lane = threadIdx.x & 63;
+    uint32_t lo = 0, hi = sq.n;
     while (hi - lo > 1) {
-        const int64_t step = (hi - lo + 63) / 64;
-        const int64_t k = lo + (lane + 1) * step;
-        const int c = __popcll(__ballot(k < hi && sq.begin(k) <= p));
+        const uint32_t step = (hi - lo + 63) / 64;
+        const uint32_t k = lo + (lane + 1) * step;
+        const uint32_t c = (uint32_t)__popcll(__ballot(k < hi && sq.begin(k) <= p));
         lo += c * step;
         hi = min(lo + step, hi);
     }
     return lo;
 }
 
-// f(q, a, b) for each piece [a, b) of a span that lies in one sequence q, in
-// order.  Offsets that are not non-decreasing end a piece at the span's end.
-template <typename F>
-__device__ __forceinline__ void each_piece(const Seqs& sq, const Place& w, F f) {
-    int64_t p = w.p0;
-    int64_t q = p < w.p1 ? find_seq(sq, p) : 0;
-    while (p < w.p1) {
-        int64_t e = sq.end(q);
-        if (e <= p || e > w.p1) e = w.p1;
-        f(q, p, e);
-        p = e;
-        if (p < w.p1) {
-            ++q;
-            if (q >= sq.n || sq.begin(q) > p || sq.end(q) <= p) q = find_seq(sq, p);
-        }
-    }
+// A wave's LDS writes before its LDS reads: one wave's are in order, the
+// compiler has to leave them so.
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
-// Sums by sequence of what spans hold.  A span's piece that holds its first
-// token goes to head, one that holds its last token (and not the first) to
-// tail, one between is a whole sequence's sum and goes to whole.
-struct PartSums {
-    double2 *head, *tail, *whole;
-    __device__ __forceinline__ void put(const Place& w, int64_t span, int64_t q, int64_t a, int64_t b, double2 v) const {
-        if (w.lane == 0) (a == w.p0 ? head[span] : b == w.p1 ? tail[span] : whole[q]) = v;
+// The sequence of each of a lane's tokens, as a distance id >= 0 to the
+// sequence q0 of the span's first token; the ids never fall along the span.
+template <int G>
+struct Ids {
+    uint32_t q0;
+    bool one;  // all tokens in q0
+    int id[4 * G];
+};
+struct MaxStep {
+    int v;
+    template <int CTRL, int RM>
+    __device__ __forceinline__ void step() { v = max(v, dpp<CTRL, RM>(0, v)); }
+};
+// Each sequence that begins inside the span marks its first token in `map`
+// (G * 256 words of the wave's own in LDS; the last one where some are empty);
+// a running maximum then tells every token's.  The cost does not depend on how
+// many sequences there are, and offsets that are not non-decreasing give some
+// ids below n - q0.
+template <int G>
+__device__ __forceinline__ Ids<G> seq_ids(const Seqs& sq, const Place<G>& w, int* map) {
+    Ids<G> s;
+    s.q0 = w.p0 < w.p1 ? (uint32_t)__builtin_amdgcn_readfirstlane((int)find_seq(sq, w.p0)) : 0u;
+#pragma unroll
+    for (int k = 0; k < 4 * G; ++k) s.id[k] = 0;
+    s.one = w.p0 >= w.p1 || s.q0 + 1 >= sq.n || sq.begin(s.q0 + 1) >= w.p1;
+    if (s.one) return s;
+    int4* m = reinterpret_cast<int4*>(map);
+#pragma unroll
+    for (int g = 0; g < G; ++g) m[g * 64 + w.lane] = make_int4(0, 0, 0, 0);
+    wave_order();
+    for (uint32_t k = s.q0 + 1 + w.lane;; k += 64) {
+        const uint32_t b = k < sq.n ? sq.begin(k) : 0xffffffffu;
+        if (b > w.p0 && b < w.p1) atomicMax(map + (b - w.p0), (int)(k - s.q0));
+        if (!__all(b < w.p1)) break;
     }
-    // The sum of sequence q; all lanes of a wave together.
-    __device__ __forceinline__ double2 get(const Seqs& sq, int64_t q) const {
-        const int64_t b = sq.begin(q), e = sq.end(q);
-        double2 v = make_double2(0.0, 0.0);
+    wave_order();
+    int before = 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int4 v = m[g * 64 + w.lane];
+        int* id = s.id + 4 * g;
+        id[0] = v.x;
+        id[1] = max(id[0], v.y);
+        id[2] = max(id[1], v.z);
+        id[3] = max(id[2], v.w);
+        MaxStep x{id[3]};
+        wave_scan(x);
+        const int low = max(before, dpp<kShr1, 0xf>(0, x.v));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) id[i] = max(id[i], low);
+        before = max(before, lane_value(x.v, 63));
+    }
+    return s;
+}
+
+// A sequence's sum (or a part of it): of values, and of tokens that take part.
+struct Part {
+    double sum, count;
+};
+
+// Sums by sequence of what spans hold.  The first sequence of a span puts its
+// part into head, one that holds the span's last token (and not its first)
+// into tail, one between is whole.
+struct PartSums {
+    Part *head, *tail, *whole;
+    // The sum of sequence q over spans of `size` tokens; all lanes of a wave together.
+    __device__ __forceinline__ Part get(const Seqs& sq, uint32_t q, uint32_t size) const {
+        const uint32_t b = sq.begin(q), e = sq.end(q);
+        Part v{0.0, 0.0};
         if (e <= b) return v;
-        const int64_t s0 = b / kSpan, s1 = (e - 1) / kSpan;
-        for (int64_t s = s0 + (threadIdx.x & 63); s <= s1; s += 64) {
-            const double2 x = b <= s * kSpan                                   ? head[s]
-                              : e >= min((s + 1) * (int64_t)kSpan, sq.tokens) ? tail[s]
-                                                                               : whole[q];
-            v.x += x.x;
-            v.y += x.y;
+        const uint32_t s0 = b / size, s1 = (e - 1) / size;
+        for (uint32_t s = s0 + (threadIdx.x & 63); s <= s1; s += 64) {
+            const Part x = b <= s * size ? head[s] : e >= min((s + 1) * size, sq.tokens) ? tail[s] : whole[q];
+            v.sum += x.sum;
+            v.count += x.count;
         }
-        return make_double2(wave_sum(v.x), wave_sum(v.y));
+        return Part{wave_sum(v.sum), wave_sum(v.count)};
     }
 };
 
-int64_t spans_of(int64_t tokens) { return (tokens + kSpan - 1) / kSpan; }
+// A step of the scan by sequence: the lane's running sum takes another's where
+// that one ends in the same sequence (ids do not fall, so nothing between differs).
+template <bool VALUE>
+struct SeqStep {
+    double x;
+    int n, key;
+    template <int CTRL, int RM>
+    __device__ __forceinline__ void step() {
+        const int k = dpp<CTRL, RM>(-1, key), m = dpp<CTRL, RM>(0, n);
+        const double y = VALUE ? dpp<CTRL, RM>(x) : 0.0;
+        if (k == key) {
+            n += m;
+            if (VALUE) x += y;
+        }
+    }
+};
 
-// Workgroups for `waves` waves' work, at most 65536 (each then takes more).
-dim3 wave_grid(int64_t waves) {
+// A span's sums by sequence: of v (VALUE; 0 at tokens that take no part) and of
+// live's bits.  A NaN or infinity stays in its own sequence.
+template <int G, bool VALUE>
+__device__ __forceinline__ void sum_span(const Place<G>& w, uint32_t span, const Ids<G>& s, const double* v,
+                                         uint32_t live, const PartSums& out) {
+    if (s.one) {
+        double x = 0.0;
+        if (VALUE) {
+#pragma unroll
+            for (int k = 0; k < 4 * G; ++k) x += v[k];
+            x = wave_sum(x);
+        }
+        const int n = wave_sum((int)__popc(live));
+        if (w.lane == 0) out.head[span] = Part{x, (double)n};
+        return;
+    }
+    double cx = 0.0;  // the sum that the group before left open, and its sequence
+    int cn = 0, ckey = -1;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int* id = s.id + 4 * g;
+        double x[4];
+        int n[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = VALUE ? v[4 * g + i] : 0.0;
+            n[i] = (int)((live >> (4 * g + i)) & 1u);
+            if (i == 0 ? w.lane == 0 && id[0] == ckey : id[i] == id[i > 0 ? i - 1 : 0]) {
+                if (VALUE) x[i] += i == 0 ? cx : x[i > 0 ? i - 1 : 0];
+                n[i] += i == 0 ? cn : n[i > 0 ? i - 1 : 0];
+            }
+        }
+        SeqStep<VALUE> t{x[3], n[3], id[3]};
+        wave_scan(t);
+        const int pk = dpp<kShr1, 0xf>(-1, t.key), pn = dpp<kShr1, 0xf>(0, t.n);
+        const double px = VALUE ? dpp<kShr1, 0xf>(t.x) : 0.0;
+        // the sequence of the token after the lane's last one
+        int next = dpp<kShl1, 0xf>(-1, id[0]);
+        if (g + 1 < G) {
+            const int first = lane_value(s.id[4 * (g + 1 < G ? g + 1 : g)], 0);
+            if (w.lane == 63) next = first;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (pk == id[i]) {
+                if (VALUE) x[i] += px;
+                n[i] += pn;
+            }
+            const uint32_t at = w.at(g) + i;
+            const bool last = at + 1 == w.p1;
+            if (at < w.p1 && (last || id[i] != (i < 3 ? id[i < 3 ? i + 1 : 3] : next)))
+                (id[i] == 0 ? out.head[span] : last ? out.tail[span] : out.whole[s.q0 + id[i]]) = Part{x[i], (double)n[i]};
+        }
+        cx = VALUE ? lane_value(t.x, 63) : 0.0;
+        cn = lane_value(t.n, 63);
+        ckey = lane_value(t.key, 63);
+    }
+}
+
+// f(t's sequence) for each of a lane's tokens of group g, called once where
+// neighbours share a sequence.
+template <int G, typename V, typename F>
+__device__ __forceinline__ void by_token(const Ids<G>& s, int g, V* v, F f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i > 0 && s.id[4 * g + i] == s.id[4 * g + (i > 0 ? i - 1 : 0)]) v[i] = v[i > 0 ? i - 1 : 0];
+        else v[i] = f(s.q0 + (uint32_t)s.id[4 * g + i]);
+    }
+}
+
+uint32_t spans_of(int64_t tokens, int g) { return (uint32_t)((tokens + 256 * g - 1) / (256 * g)); }
+
+// Workgroups for `waves` waves' work, at most `most` (each then takes more).
+dim3 wave_grid(int64_t waves, int64_t most = 65536) {
     const int64_t g = (waves + kLossNT / 64 - 1) / (kLossNT / 64);
-    return dim3((unsigned)(g < 1 ? 1 : g > 65536 ? 65536 : g));
+    return dim3((unsigned)(g < 1 ? 1 : g > most ? most : g));
 }
 
 // A wave's number among all of a launch, and their number.
 struct Wave {
-    int64_t id, count;
+    uint32_t id, count;
     __device__ __forceinline__ Wave() {
-        const int nw = blockDim.x >> 6;
-        id = (int64_t)blockIdx.x * nw + (threadIdx.x >> 6);
-        count = (int64_t)gridDim.x * nw;
+        const uint32_t nw = blockDim.x >> 6;
+        id = blockIdx.x * nw + (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+        count = gridDim.x * nw;
+    }
+};
+
+// A wave's own map for the sequences of its tokens.
+template <int NT, int G>
+struct Maps {
+    int word[NT / 64][256 * G];
+    __device__ __forceinline__ int* mine() { return word[__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6))]; }
+};
+
+struct Taker {  // places in a workspace, 256-byte aligned
+    size_t at = 0;
+    size_t take(int64_t n, size_t size) {
+        const size_t o = at;
+        at += ((size_t)n * size + 255) / 256 * 256;
+        return o;
+    }
+};
+// Span sums take as many places as the smaller spans need.
+struct SumsPlan {
+    size_t head, tail, whole;
+    SumsPlan(Taker& t, int64_t tokens, int64_t seqs) {
+        const int g = tokens <= kOneMax ? 1 : kSpanG;
+        head = t.take(spans_of(tokens, g), sizeof(Part));
+        tail = t.take(spans_of(tokens, g), sizeof(Part));
+        whole = t.take(seqs, sizeof(Part));
+    }
+    PartSums at(char* ws) const {
+        return PartSums{reinterpret_cast<Part*>(ws + head), reinterpret_cast<Part*>(ws + tail),
+                        reinterpret_cast<Part*>(ws + whole)};
     }
 };
 
@@ -189,7 +334,7 @@ struct Pref {
     const float* ref;  // or NULL
     Live live;
     Seqs sq;
-    int64_t pairs;
+    uint32_t pairs;
     double beta, smooth;
     int mean, squared;
     double grad_scale;
@@ -202,27 +347,33 @@ struct Pref {
 // -log sigma(h), without overflow for either sign.
 __device__ __forceinline__ double softplus_neg(double h) { return fmax(-h, 0.0) + log1p(exp(-fabs(h))); }
 
-__device__ __forceinline__ void pref_sums(const Pref& p, int64_t span) {
-    const Place w(span, p.sq.tokens);
-    float x[16], y[16];
-    load16(p.logp, w, x);
-    if (p.ref) load16(p.ref, w, y);
+template <int G>
+__device__ __forceinline__ void pref_sums(const Pref& p, uint32_t span, int* map) {
+    const Place<G> w(span, p.sq.tokens);
+    float x[4 * G], y[4 * G];
+    double v[4 * G];
     const uint32_t live = p.live.bits(w);
-    each_piece(p.sq, w, [&](int64_t q, int64_t a, int64_t b) {
-        const uint32_t m = live & inside(w, a, b);
-        double v = 0.0;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v += (m >> k) & 1u ? (double)x[k] - (p.ref ? (double)y[k] : 0.0) : 0.0;
-        p.sums.put(w, span, q, a, b, make_double2(wave_sum(v), wave_sum((double)__popc(m))));
-    });
+    for (int g = 0; g < G; ++g) load4(p.logp, w.at(g), w.p1, x + 4 * g);
+    if (p.ref) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) load4(p.ref, w.at(g), w.p1, y + 4 * g);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4 * G; ++k) y[k] = 0.0f;
+    }
+    const Ids<G> s = seq_ids(p.sq, w, map);
+#pragma unroll
+    for (int k = 0; k < 4 * G; ++k) v[k] = (live >> k) & 1u ? (double)x[k] - (double)y[k] : 0.0;
+    sum_span<G, true>(w, span, s, v, live, p.sums);
 }
 
-__device__ __forceinline__ void pref_pair(const Pref& p, int64_t i) {
-    double2 c = p.sums.get(p.sq, 2 * i), r = p.sums.get(p.sq, 2 * i + 1);
-    const double fc = p.mean ? 1.0 / fmax(c.y, 1.0) : 1.0, fr = p.mean ? 1.0 / fmax(r.y, 1.0) : 1.0;
-    c.x *= fc;
-    r.x *= fr;
-    const double delta = c.x - r.x;
+__device__ __forceinline__ void pref_pair(const Pref& p, uint32_t i, uint32_t size) {
+    Part c = p.sums.get(p.sq, 2 * i, size), r = p.sums.get(p.sq, 2 * i + 1, size);
+    const double fc = p.mean ? 1.0 / fmax(c.count, 1.0) : 1.0, fr = p.mean ? 1.0 / fmax(r.count, 1.0) : 1.0;
+    c.sum *= fc;
+    r.sum *= fr;
+    const double delta = c.sum - r.sum;
     double loss, slope;
     if (p.squared) {
         const double z = delta - 0.5 / p.beta;
@@ -239,292 +390,354 @@ __device__ __forceinline__ void pref_pair(const Pref& p, int64_t i) {
     p.coef[2 * i] = (float)(slope * fc);
     p.coef[2 * i + 1] = (float)(-slope * fr);
     p.pair_loss[i] = (float)loss;
-    p.reward[2 * i] = (float)(p.beta * c.x);
-    p.reward[2 * i + 1] = (float)(p.beta * r.x);
+    p.reward[2 * i] = (float)(p.beta * c.sum);
+    p.reward[2 * i + 1] = (float)(p.beta * r.sum);
 }
 
-__device__ __forceinline__ void pref_grad(const Pref& p, int64_t span) {
-    const Place w(span, p.sq.tokens);
-    float g[16] = {};
+template <int G>
+__device__ __forceinline__ void pref_grad(const Pref& p, uint32_t span, int* map) {
+    const Place<G> w(span, p.sq.tokens);
     const uint32_t live = p.live.bits(w);
-    each_piece(p.sq, w, [&](int64_t q, int64_t a, int64_t b) {
-        const uint32_t m = live & inside(w, a, b);
-        const float c = p.coef[q];
+    const Ids<G> s = seq_ids(p.sq, w, map);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) g[k] = (m >> k) & 1u ? c : g[k];
-    });
-    store16(p.grad, w, g);
+    for (int g = 0; g < G; ++g) {
+        float c[4];
+        by_token(s, g, c, [&](uint32_t q) { return p.coef[q]; });
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = (live >> (4 * g + i)) & 1u ? c[i] : 0.0f;
+        store4(p.grad, w.at(g), w.p1, c);
+    }
 }
 
 template <int NT>
 __device__ __forceinline__ void pref_mean(const Pref& p) {
     __shared__ double red[NT / 64];
     double v = 0.0;
-    for (int64_t i = threadIdx.x; i < p.pairs; i += NT) v += p.each[i];
+    for (uint32_t i = threadIdx.x; i < p.pairs; i += NT) v += p.each[i];
     v = wg_sum<NT>(v, red);
     if (threadIdx.x == 0) *p.loss = p.pairs ? (float)(v / (double)p.pairs) : 0.0f;
 }
 
-__global__ __launch_bounds__(kLossNT) void k_pref_sums(Pref p, int64_t spans) {
+__global__ __launch_bounds__(kLossNT) void k_pref_sums(Pref p, uint32_t spans) {
+    __shared__ Maps<kLossNT, kSpanG> maps;
     const Wave w;
-    for (int64_t s = w.id; s < spans; s += w.count) pref_sums(p, s);
+    for (uint32_t s = w.id; s < spans; s += w.count) pref_sums<kSpanG>(p, s, maps.mine());
 }
 __global__ __launch_bounds__(kLossNT) void k_pref_pairs(Pref p) {
     const Wave w;
-    for (int64_t i = w.id; i < p.pairs; i += w.count) pref_pair(p, i);
+    for (uint32_t i = w.id; i < p.pairs; i += w.count) pref_pair(p, i, 256 * kSpanG);
 }
 // The first workgroup takes the mean of the pair losses, the others the tokens.
-__global__ __launch_bounds__(kLossNT) void k_pref_grad(Pref p, int64_t spans) {
+__global__ __launch_bounds__(kLossNT) void k_pref_grad(Pref p, uint32_t spans) {
+    __shared__ Maps<kLossNT, kSpanG> maps;
     if (blockIdx.x == 0) {
         pref_mean<kLossNT>(p);
         return;
     }
     const Wave w;
-    const int64_t first = kLossNT / 64;
-    for (int64_t s = w.id - first; s < spans; s += w.count - first) pref_grad(p, s);
+    const uint32_t first = kLossNT / 64;
+    for (uint32_t s = w.id - first; s < spans; s += w.count - first) pref_grad<kSpanG>(p, s, maps.mine());
 }
 // A small call whole: the three steps by one workgroup.
-__global__ __launch_bounds__(kOneNT) void k_pref_one(Pref p, int64_t spans) {
+__global__ __launch_bounds__(kOneNT) void k_pref_one(Pref p, uint32_t spans) {
+    __shared__ Maps<kOneNT, 1> maps;
     const Wave w;
-    for (int64_t s = w.id; s < spans; s += w.count) pref_sums(p, s);
+    for (uint32_t s = w.id; s < spans; s += w.count) pref_sums<1>(p, s, maps.mine());
     __syncthreads();
-    for (int64_t i = w.id; i < p.pairs; i += w.count) pref_pair(p, i);
+    for (uint32_t i = w.id; i < p.pairs; i += w.count) pref_pair(p, i, 256);
     __syncthreads();
     if (p.grad)
-        for (int64_t s = w.id; s < spans; s += w.count) pref_grad(p, s);
+        for (uint32_t s = w.id; s < spans; s += w.count) pref_grad<1>(p, s, maps.mine());
     pref_mean<kOneNT>(p);
 }
 
 struct PrefPlan {
-    size_t off_head, off_tail, off_whole, off_each, off_coef, bytes;
+    Taker t;
+    SumsPlan sums;
+    size_t off_each, off_coef, bytes;
+    PrefPlan(int64_t tokens, int64_t pairs) : sums(t, tokens, 2 * pairs) {
+        off_each = t.take(pairs, sizeof(double));
+        off_coef = t.take(2 * pairs, sizeof(float));
+        bytes = t.at;
+    }
 };
-PrefPlan pref_plan(int64_t tokens, int64_t pairs) {
-    PrefPlan p;
-    size_t at = 0;
-    auto take = [&](int64_t n, size_t size) {
-        const size_t o = at;
-        at += ((size_t)n * size + 255) / 256 * 256;
-        return o;
-    };
-    p.off_head = take(spans_of(tokens), sizeof(double2));
-    p.off_tail = take(spans_of(tokens), sizeof(double2));
-    p.off_whole = take(2 * pairs, sizeof(double2));
-    p.off_each = take(pairs, sizeof(double));
-    p.off_coef = take(2 * pairs, sizeof(float));
-    p.bytes = at;
-    return p;
-}
 
 // ---- policy loss ----
 
-template <typename LP>
-struct PolicyCall {
+// Weights of tokens: what the loss, and the rows' terms, take of a policy call.
+struct Weights {
     Policy p;
-    const LP* logp;
     Live live;
     Seqs sq;
-    float* loss;
-    int32_t* counts;
-    float* grad;      // or NULL
-    PartSums sums;    // (tokens that take part, 0)
+    PartSums sums;    // (0, tokens that take part)
     double* weight;   // a sequence's w_t (ISO_POLICY_SEQ_MEAN)
-    double* part;     // a wave's sums of w pg, w kl; tokens, clipped
-    double2* total;   // tokens that take part in all, w_t
+    int* counted;     // a workgroup's tokens that take part (else)
+    uint32_t parts;   // how many of them
+    __device__ __forceinline__ bool by_seq() const { return p.seq_mean != 0; }
+    // a sequence's w_t, from the tokens that take part in it
+    __device__ __forceinline__ double seq_weight(double count) const {
+        return 1.0 / ((p.norm > 0.0 ? p.norm : (double)sq.n) * fmax(count, 1.0));
+    }
+    // every token's w_t where they are alike
+    __device__ __forceinline__ double token_weight(int count) const {
+        return 1.0 / (p.norm > 0.0 ? p.norm : fmax((double)count, 1.0));
+    }
+    __device__ __forceinline__ double weight_of(uint32_t q) const {
+        return live.all() ? seq_weight((double)(sq.end(q) - sq.begin(q))) : weight[q];
+    }
 };
 
 // Tokens that take part, by sequence.
-template <typename LP>
-__device__ __forceinline__ void policy_count(const PolicyCall<LP>& c, int64_t span) {
-    const Place w(span, c.sq.tokens);
+template <int G>
+__device__ __forceinline__ void count_by_seq(const Weights& c, uint32_t span, int* map) {
+    const Place<G> w(span, c.sq.tokens);
     const uint32_t live = c.live.bits(w);
-    if (!c.p.seq_mean) {
-        const double n = wave_sum((double)__popc(live));
-        if (w.lane == 0) c.sums.head[span] = make_double2(n, 0.0);
-        return;
+    const Ids<G> s = seq_ids(c.sq, w, map);
+    sum_span<G, false>(w, span, s, nullptr, live, c.sums);
+}
+__device__ __forceinline__ void weigh_seq(const Weights& c, uint32_t q, uint32_t size) {
+    const double n = c.sums.get(c.sq, q, size).count;
+    if ((threadIdx.x & 63) == 0) c.weight[q] = c.seq_weight(n);
+}
+
+// The weight that all tokens share, for every thread of a workgroup: from the
+// workgroups' counts.
+template <int NT>
+__device__ __forceinline__ double shared_weight(const Weights& c) {
+    __shared__ int red[NT / 64];
+    if (c.by_seq()) return 0.0;
+    if (c.live.all()) return c.token_weight((int)c.sq.tokens);
+    int n = 0;
+    for (uint32_t k = threadIdx.x; k < c.parts; k += NT) n += c.counted[k];
+    return c.token_weight(wg_sum<NT>(n, red));
+}
+// The weights of a small call, by one workgroup: every token's if they are alike.
+template <int NT>
+__device__ __forceinline__ double small_weights(const Weights& c, uint32_t spans, int* map) {
+    __shared__ int red[NT / 64];
+    const Wave w;
+    if (c.live.all()) return shared_weight<NT>(c);
+    if (c.by_seq()) {
+        for (uint32_t s = w.id; s < spans; s += w.count) count_by_seq<1>(c, s, map);
+        __syncthreads();
+        for (uint32_t q = w.id; q < c.sq.n; q += w.count) weigh_seq(c, q, 256);
+        __syncthreads();
+        return 0.0;
     }
-    each_piece(c.sq, w, [&](int64_t q, int64_t a, int64_t b) {
-        c.sums.put(w, span, q, a, b, make_double2(wave_sum((double)__popc(live & inside(w, a, b))), 0.0));
-    });
+    int n = 0;
+    for (uint32_t s = w.id; s < spans; s += w.count) n += (int)__popc(c.live.bits(Place<1>(s, c.sq.tokens)));
+    return c.token_weight(wg_sum<NT>(n, red));
 }
 
-// A sequence's weight, from its count.
-template <typename LP>
-__device__ __forceinline__ void policy_weight(const PolicyCall<LP>& c, int64_t q) {
-    const double n = c.sums.get(c.sq, q).x;
-    if ((threadIdx.x & 63) == 0) c.weight[q] = 1.0 / ((c.p.norm > 0.0 ? c.p.norm : (double)c.sq.n) * fmax(n, 1.0));
+__global__ __launch_bounds__(kLossNT) void k_count_by_seq(Weights c, uint32_t spans) {
+    __shared__ Maps<kLossNT, kSpanG> maps;
+    const Wave w;
+    for (uint32_t s = w.id; s < spans; s += w.count) count_by_seq<kSpanG>(c, s, maps.mine());
+}
+__global__ __launch_bounds__(kLossNT) void k_weigh_seqs(Weights c) {
+    const Wave w;
+    for (uint32_t q = w.id; q < c.sq.n; q += w.count) weigh_seq(c, q, 256 * kSpanG);
+}
+__global__ __launch_bounds__(kLossNT) void k_count(Weights c, uint32_t spans) {
+    __shared__ int red[kLossNT / 64];
+    const Wave w;
+    int n = 0;
+    for (uint32_t s = w.id; s < spans; s += w.count) n += (int)__popc(c.live.bits(Place<kSpanG>(s, c.sq.tokens)));
+    n = wg_sum<kLossNT>(n, red);
+    if (threadIdx.x == 0) c.counted[blockIdx.x] = n;
 }
 
-// Every token's weight where they are alike, by one workgroup.
-template <typename LP, int NT>
-__device__ __forceinline__ void policy_total(const PolicyCall<LP>& c, int64_t spans) {
-    __shared__ double red[NT / 64];
-    double n = 0.0;
-    for (int64_t s = threadIdx.x; s < spans; s += NT) n += c.sums.head[s].x;
-    n = wg_sum<NT>(n, red);
-    if (threadIdx.x == 0) *c.total = make_double2(n, 1.0 / (c.p.norm > 0.0 ? c.p.norm : fmax(n, 1.0)));
-}
-
-struct Four {
-    double pg, kl, live, over;
+struct PolicyCall {
+    Weights c;
+    const float* logp;
+    float* loss;
+    int32_t* counts;
+    float* grad;       // or NULL
+    PolicySums* part;  // a workgroup's sums
 };
 
 // The terms of a span's tokens, summed into s by lane; their gradient is written.
-template <typename LP>
-__device__ __forceinline__ void policy_span(const PolicyCall<LP>& c, int64_t span, Four& s) {
-    const Place w(span, c.sq.tokens);
+template <int G>
+__device__ __forceinline__ void policy_span(const PolicyCall& f, uint32_t span, double all, PolicySums& s, int* map) {
+    const Weights& c = f.c;
     const Policy& p = c.p;
-    float old[16], ref[16], adv[16], f[16];
-    double lp[16];
-    if constexpr (sizeof(LP) == 4) {
-        load16(c.logp, w, f);
+    const Place<G> w(span, c.sq.tokens);
+    float lp[4 * G], old[4 * G], ref[4 * G], adv[4 * G];
+    const uint32_t live = c.live.bits(w);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        load4(f.logp, w.at(g), w.p1, lp + 4 * g);
+        load4(p.old_logp, w.at(g), w.p1, old + 4 * g);
+    }
+    if (p.ref_logp) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) load4(p.ref_logp, w.at(g), w.p1, ref + 4 * g);
     } else {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const int64_t t = w.at(k / 4) + k % 4;
-            lp[k] = t < w.p1 ? c.logp[t] : 0.0;
-        }
+        for (int k = 0; k < 4 * G; ++k) ref[k] = 0.0f;
     }
-    load16(p.old_logp, w, old);
-    if (p.ref_logp) load16(p.ref_logp, w, ref);
-    const uint32_t live = c.live.bits(w);
-    double wt[16];
-    if (p.token_adv) load16(p.adv, w, adv);
-    if (!p.token_adv || p.seq_mean) {
+    if (p.token_adv) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) wt[k] = 0.0;
-        each_piece(c.sq, w, [&](int64_t q, int64_t a, int64_t b) {
-            const uint32_t m = inside(w, a, b);
-            const float av = p.token_adv ? 0.0f : p.adv[q];
-            const double wq = p.seq_mean ? c.weight[q] : 0.0;
+        for (int g = 0; g < G; ++g) load4(p.adv, w.at(g), w.p1, adv + 4 * g);
+    }
+    Ids<G> ids;
+    if (!p.token_adv || c.by_seq()) ids = seq_ids(c.sq, w, map);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                if (!p.token_adv) adv[k] = (m >> k) & 1u ? av : adv[k];
-                wt[k] = (m >> k) & 1u ? wq : wt[k];
+    for (int g = 0; g < G; ++g) {
+        double wt[4] = {all, all, all, all};
+        if (!p.token_adv) by_token(ids, g, adv + 4 * g, [&](uint32_t q) { return p.adv[q]; });
+        if (c.by_seq()) by_token(ids, g, wt, [&](uint32_t q) { return c.weight_of(q); });
+        float o4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = 4 * g + i;
+            o4[i] = 0.0f;
+            if ((live >> k) & 1u) {
+                const PolicyTerm o = policy_term(p, (double)lp[k], (double)old[k], (double)ref[k], (double)adv[k]);
+                s.pg += wt[i] * o.pg;
+                s.kl += wt[i] * o.kl;
+                s.over += o.over ? 1 : 0;
+                s.live += 1;
+                o4[i] = (float)(o.slope * (wt[i] * p.grad_scale));
             }
-        });
-    }
-    const double all = p.seq_mean ? 0.0 : c.total->y;
-    float g[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        g[k] = 0.0f;
-        if ((live >> k) & 1u) {
-            const double x = sizeof(LP) == 4 ? (double)f[k] : lp[k];
-            const PolicyTerm o = policy_term(p, x, (double)old[k], p.ref_logp ? (double)ref[k] : 0.0, (double)adv[k]);
-            const double wk = p.seq_mean ? wt[k] : all;
-            s.pg += wk * o.pg;
-            s.kl += wk * o.kl;
-            s.over += o.over ? 1.0 : 0.0;
-            s.live += 1.0;
-            g[k] = (float)(o.slope * (wk * p.grad_scale));
         }
+        if (f.grad) store4(f.grad, w.at(g), w.p1, o4);
     }
-    if (c.grad) store16(c.grad, w, g);
 }
 
-// A workgroup's sums into its part; or, from the parts, the outputs.
-template <typename LP, int NT>
-__device__ __forceinline__ void policy_part(const PolicyCall<LP>& c, const Four& s) {
-    __shared__ double red[NT / 64];
-    const double pg = wg_sum<NT>(s.pg, red), kl = wg_sum<NT>(s.kl, red);
-    const double live = wg_sum<NT>(s.live, red), over = wg_sum<NT>(s.over, red);
-    if (threadIdx.x == 0) {
-        double* o = c.part + 4 * (int64_t)blockIdx.x;
-        o[0] = pg;
-        o[1] = kl;
-        o[2] = live;
-        o[3] = over;
-    }
+// The workgroup's sums, in thread 0.
+template <int NT>
+__device__ __forceinline__ PolicySums wg_policy(const PolicySums& s) {
+    __shared__ PolicySums red[NT / 64];
+    PolicySums o{wave_sum(s.pg), wave_sum(s.kl), wave_sum(s.live), wave_sum(s.over)};
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = o;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int k = 1; k < NT / 64; ++k) {
+            o.pg += red[k].pg;
+            o.kl += red[k].kl;
+            o.live += red[k].live;
+            o.over += red[k].over;
+        }
+    return o;
 }
-template <typename LP>
-__device__ __forceinline__ void policy_out(const PolicyCall<LP>& c, const Four& s) {
-    if (threadIdx.x != 0) return;
-    c.loss[0] = (float)(c.p.kl_coef != 0.0 ? s.pg + c.p.kl_coef * s.kl : s.pg);
-    c.loss[1] = (float)s.pg;
-    c.loss[2] = (float)s.kl;
-    c.counts[0] = (int32_t)s.live;
-    c.counts[1] = (int32_t)s.over;
+__device__ __forceinline__ void policy_out(double kl_coef, const PolicySums& s, float* loss, int32_t* counts) {
+    loss[0] = (float)(kl_coef != 0.0 ? s.pg + kl_coef * s.kl : s.pg);
+    loss[1] = (float)s.pg;
+    loss[2] = (float)s.kl;
+    counts[0] = s.live;
+    counts[1] = s.over;
 }
 
-template <typename LP>
-__global__ __launch_bounds__(kLossNT) void k_policy_count(PolicyCall<LP> c, int64_t spans) {
+__global__ __launch_bounds__(kLossNT) void k_policy_tokens(PolicyCall f, uint32_t spans) {
+    __shared__ Maps<kLossNT, kTermG> maps;
+    const double all = shared_weight<kLossNT>(f.c);
     const Wave w;
-    for (int64_t s = w.id; s < spans; s += w.count) policy_count(c, s);
+    PolicySums s{};
+    for (uint32_t k = w.id; k < spans; k += w.count) policy_span<kTermG>(f, k, all, s, maps.mine());
+    s = wg_policy<kLossNT>(s);
+    if (threadIdx.x == 0) f.part[blockIdx.x] = s;
 }
-template <typename LP>
-__global__ __launch_bounds__(kLossNT) void k_policy_weights(PolicyCall<LP> c, int64_t spans) {
-    if (!c.p.seq_mean) {  // one workgroup
-        policy_total<LP, kLossNT>(c, spans);
-        return;
+__global__ __launch_bounds__(kOneNT) void k_policy_out(double kl_coef, const PolicySums* __restrict__ part, int parts,
+                                                       float* loss, int32_t* counts) {
+    PolicySums s{};
+    for (int k = threadIdx.x; k < parts; k += kOneNT) {
+        const PolicySums o = part[k];
+        s.pg += o.pg;
+        s.kl += o.kl;
+        s.live += o.live;
+        s.over += o.over;
     }
-    const Wave w;
-    for (int64_t q = w.id; q < c.sq.n; q += w.count) policy_weight(c, q);
-}
-template <typename LP>
-__global__ __launch_bounds__(kLossNT) void k_policy_tokens(PolicyCall<LP> c, int64_t spans) {
-    const Wave w;
-    Four s{};
-    for (int64_t k = w.id; k < spans; k += w.count) policy_span(c, k, s);
-    policy_part<LP, kLossNT>(c, s);
-}
-template <typename LP>
-__global__ __launch_bounds__(kOneNT) void k_policy_sum(PolicyCall<LP> c, int64_t parts) {
-    __shared__ double red[kOneNT / 64];
-    Four s{};
-    for (int64_t k = threadIdx.x; k < parts; k += kOneNT) {
-        const double* o = c.part + 4 * k;
-        s.pg += o[0];
-        s.kl += o[1];
-        s.live += o[2];
-        s.over += o[3];
-    }
-    s.pg = wg_sum<kOneNT>(s.pg, red);
-    s.kl = wg_sum<kOneNT>(s.kl, red);
-    s.live = wg_sum<kOneNT>(s.live, red);
-    s.over = wg_sum<kOneNT>(s.over, red);
-    policy_out(c, s);
+    s = wg_policy<kOneNT>(s);
+    if (threadIdx.x == 0) policy_out(kl_coef, s, loss, counts);
 }
 // A small call whole.
-template <typename LP>
-__global__ __launch_bounds__(kOneNT) void k_policy_one(PolicyCall<LP> c, int64_t spans) {
-    __shared__ double red[kOneNT / 64];
+__global__ __launch_bounds__(kOneNT) void k_policy_one(PolicyCall f, uint32_t spans) {
+    __shared__ Maps<kOneNT, 1> maps;
+    const double all = small_weights<kOneNT>(f.c, spans, maps.mine());
     const Wave w;
-    for (int64_t s = w.id; s < spans; s += w.count) policy_count(c, s);
-    __syncthreads();
-    if (c.p.seq_mean)
-        for (int64_t q = w.id; q < c.sq.n; q += w.count) policy_weight(c, q);
-    else
-        policy_total<LP, kOneNT>(c, spans);
-    __syncthreads();
-    Four s{};
-    for (int64_t k = w.id; k < spans; k += w.count) policy_span(c, k, s);
-    s.pg = wg_sum<kOneNT>(s.pg, red);
-    s.kl = wg_sum<kOneNT>(s.kl, red);
-    s.live = wg_sum<kOneNT>(s.live, red);
-    s.over = wg_sum<kOneNT>(s.over, red);
-    policy_out(c, s);
+    PolicySums s{};
+    for (uint32_t k = w.id; k < spans; k += w.count) policy_span<1>(f, k, all, s, maps.mine());
+    s = wg_policy<kOneNT>(s);
+    if (threadIdx.x == 0) policy_out(f.c.p.kl_coef, s, f.loss, f.counts);
+}
+
+// Rows' terms of the loss from logits.
+template <int G>
+__device__ __forceinline__ void row_span(const Weights& c, uint32_t span, double all, RowTerm* terms, int* map) {
+    const Place<G> w(span, c.sq.tokens);
+    const uint32_t live = c.live.bits(w);
+    Ids<G> ids;
+    if (!c.p.token_adv || c.by_seq()) ids = seq_ids(c.sq, w, map);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        float adv[4];
+        double wt[4] = {all, all, all, all};
+        if (c.p.token_adv) load4(c.p.adv, w.at(g), w.p1, adv);
+        else by_token(ids, g, adv, [&](uint32_t q) { return c.p.adv[q]; });
+        if (c.by_seq()) by_token(ids, g, wt, [&](uint32_t q) { return c.weight_of(q); });
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (w.at(g) + i < w.p1)
+                terms[w.at(g) + i] = RowTerm{(live >> (4 * g + i)) & 1u ? wt[i] : 0.0, adv[i], 0.0f};
+    }
+}
+__global__ __launch_bounds__(kLossNT) void k_row_terms(Weights c, uint32_t spans, RowTerm* terms) {
+    __shared__ Maps<kLossNT, kSpanG> maps;
+    const double all = shared_weight<kLossNT>(c);
+    const Wave w;
+    for (uint32_t k = w.id; k < spans; k += w.count) row_span<kSpanG>(c, k, all, terms, maps.mine());
+}
+__global__ __launch_bounds__(kOneNT) void k_row_terms_one(Weights c, uint32_t spans, RowTerm* terms) {
+    __shared__ Maps<kOneNT, 1> maps;
+    const double all = small_weights<kOneNT>(c, spans, maps.mine());
+    const Wave w;
+    for (uint32_t k = w.id; k < spans; k += w.count) row_span<1>(c, k, all, terms, maps.mine());
+}
+
+constexpr int kCountGrid = 512;  // workgroups that count, their counts read by every later workgroup
+
+struct WeightsPlan {
+    Taker t;
+    SumsPlan sums;
+    size_t off_weight, off_counted, bytes;
+    WeightsPlan(int64_t tokens, int64_t seqs) : sums(t, tokens, seqs) {
+        off_weight = t.take(seqs, sizeof(double));
+        off_counted = t.take(kCountGrid, sizeof(int));
+        bytes = t.at;
+    }
+};
+
+Weights make_weights(const Policy& p, const Live& live, const Seqs& sq, const WeightsPlan& pl, char* ws) {
+    return Weights{p, live, sq, pl.sums.at(ws), reinterpret_cast<double*>(ws + pl.off_weight),
+                   reinterpret_cast<int*>(ws + pl.off_counted), 0};
+}
+bool small_call(const Seqs& sq) { return sq.tokens <= kOneMax && sq.n <= kOneMax; }
+
+// What the weights of a larger call take: tokens counted, by sequence or by
+// workgroup.  Nothing where every token takes part.
+void start_weights(Weights& c, hipStream_t st) {
+    if (c.live.all()) return;
+    const uint32_t spans = spans_of(c.sq.tokens, kSpanG);
+    const dim3 nt(kLossNT);
+    if (c.p.seq_mean) {
+        hipLaunchKernelGGL(k_count_by_seq, wave_grid(spans), nt, 0, st, c, spans);
+        hipLaunchKernelGGL(k_weigh_seqs, wave_grid(c.sq.n), nt, 0, st, c);
+    } else {
+        const dim3 grid = wave_grid(spans, kCountGrid);
+        c.parts = grid.x;
+        hipLaunchKernelGGL(k_count, grid, nt, 0, st, c, spans);
+    }
 }
 
 struct PolicyPlan {
-    size_t off_total, off_head, off_tail, off_whole, off_weight, off_part, bytes;
+    WeightsPlan w;
+    size_t off_part, bytes;
+    PolicyPlan(int64_t tokens, int64_t seqs) : w(tokens, seqs) {
+        off_part = w.t.take((int64_t)wave_grid(spans_of(tokens, kTermG)).x, sizeof(PolicySums));
+        bytes = w.t.at;
+    }
 };
-PolicyPlan policy_plan(int64_t tokens, int64_t seqs) {
-    PolicyPlan p;
-    size_t at = 0;
-    auto take = [&](int64_t n, size_t size) {
-        const size_t o = at;
-        at += ((size_t)n * size + 255) / 256 * 256;
-        return o;
-    };
-    p.off_total = take(1, sizeof(double2));
-    p.off_head = take(spans_of(tokens), sizeof(double2));
-    p.off_tail = take(spans_of(tokens), sizeof(double2));
-    p.off_whole = take(seqs, sizeof(double2));
-    p.off_weight = take(seqs, sizeof(double));
-    p.off_part = take(4 * (int64_t)wave_grid(spans_of(tokens)).x, sizeof(double));
-    p.bytes = at;
-    return p;
-}
 
 bool seqs_ok(const int32_t* off, int64_t seqs, int64_t tokens) {
     if (seqs < 0 || tokens < 0 || tokens > 0x7fffffffLL || seqs > 0x7fffffffLL) return false;
@@ -565,46 +778,26 @@ Policy make_policy(const float* old_logp, const float* ref_logp, const float* ad
     return p;
 }
 
-size_t policy_workspace(int64_t tokens, int64_t seqs) {
-    if (tokens < 0 || seqs < 0 || tokens > 0x7fffffffLL || seqs > 0x7fffffffLL) return 0;
-    return policy_plan(tokens, seqs).bytes;
-}
+size_t row_terms_workspace(int64_t rows, int64_t seqs) { return WeightsPlan(rows, seqs).bytes; }
 
-template <typename LP>
-hipError_t launch_policy(const Policy& p, const LP* logp, const uint8_t* mask, const int32_t* target,
-                         const Seqs& sq, float* loss, int32_t* counts, float* grad, void* workspace,
-                         hipStream_t st) {
-    const PolicyPlan pl = policy_plan(sq.tokens, sq.n);
-    char* ws = static_cast<char*>(workspace);
-    PolicyCall<LP> c;
-    c.p = p;
-    c.logp = logp;
-    c.live = Live{mask, target};
-    c.sq = sq;
-    c.loss = loss;
-    c.counts = counts;
-    c.grad = grad;
-    c.total = reinterpret_cast<double2*>(ws + pl.off_total);
-    c.sums = PartSums{reinterpret_cast<double2*>(ws + pl.off_head), reinterpret_cast<double2*>(ws + pl.off_tail),
-                      reinterpret_cast<double2*>(ws + pl.off_whole)};
-    c.weight = reinterpret_cast<double*>(ws + pl.off_weight);
-    c.part = reinterpret_cast<double*>(ws + pl.off_part);
-    const int64_t spans = spans_of(sq.tokens);
-    if (sq.tokens <= kOneMax && sq.n <= kOneMax) {
-        hipLaunchKernelGGL((k_policy_one<LP>), dim3(1), dim3(kOneNT), 0, st, c, spans);
+hipError_t launch_row_terms(const Policy& p, const int32_t* target, const Seqs& sq, RowTerm* terms, void* workspace,
+                            hipStream_t st) {
+    Weights c = make_weights(p, Live{nullptr, target}, sq, WeightsPlan(sq.tokens, sq.n), static_cast<char*>(workspace));
+    if (small_call(sq)) {
+        hipLaunchKernelGGL(k_row_terms_one, dim3(1), dim3(kOneNT), 0, st, c, spans_of(sq.tokens, 1), terms);
         return hipGetLastError();
     }
-    const dim3 grid = wave_grid(spans), nt(kLossNT);
-    hipLaunchKernelGGL((k_policy_count<LP>), grid, nt, 0, st, c, spans);
-    hipLaunchKernelGGL((k_policy_weights<LP>), p.seq_mean ? wave_grid(sq.n) : dim3(1), nt, 0, st, c, spans);
-    hipLaunchKernelGGL((k_policy_tokens<LP>), grid, nt, 0, st, c, spans);
-    hipLaunchKernelGGL((k_policy_sum<LP>), dim3(1), dim3(kOneNT), 0, st, c, (int64_t)grid.x);
+    start_weights(c, st);
+    const uint32_t spans = spans_of(sq.tokens, kSpanG);
+    hipLaunchKernelGGL(k_row_terms, wave_grid(spans), dim3(kLossNT), 0, st, c, spans, terms);
     return hipGetLastError();
 }
-template hipError_t launch_policy<float>(const Policy&, const float*, const uint8_t*, const int32_t*, const Seqs&,
-                                         float*, int32_t*, float*, void*, hipStream_t);
-template hipError_t launch_policy<double>(const Policy&, const double*, const uint8_t*, const int32_t*, const Seqs&,
-                                          float*, int32_t*, float*, void*, hipStream_t);
+
+hipError_t launch_policy_out(const Policy& p, const PolicySums* part, int parts, float* loss, int32_t* counts,
+                             hipStream_t st) {
+    hipLaunchKernelGGL(k_policy_out, dim3(1), dim3(kOneNT), 0, st, p.kl_coef, part, parts, loss, counts);
+    return hipGetLastError();
+}
 
 }  // namespace iso
 
@@ -612,7 +805,7 @@ extern "C" {
 
 size_t iso_pref_loss_workspace_bytes(int64_t tokens, int64_t pairs) {
     if (tokens < 0 || pairs < 0 || tokens > 0x7fffffffLL || pairs > 0x3fffffffLL) return 0;
-    return iso::pref_plan(tokens, pairs).bytes;
+    return iso::PrefPlan(tokens, pairs).bytes;
 }
 
 int iso_pref_loss(const float* logp, const float* ref_logp, const uint8_t* mask, const int32_t* seq_off,
@@ -637,14 +830,14 @@ int iso_pref_loss(const float* logp, const float* ref_logp, const uint8_t* mask,
     if (need && (!workspace || workspace_bytes < need)) return ISO_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return ISO_ERR_ARG;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const PrefPlan pl = pref_plan(tokens, pairs);
+    const PrefPlan pl(tokens, pairs);
     char* ws = static_cast<char*>(workspace);
     Pref p;
     p.logp = logp;
     p.ref = ref_logp;
     p.live = Live{mask, nullptr};
-    p.sq = Seqs{seq_off, 2 * pairs, tokens, pairs ? tokens / (2 * pairs) : 0};
-    p.pairs = pairs;
+    p.sq = make_seqs(seq_off, 2 * pairs, tokens);
+    p.pairs = (uint32_t)pairs;
     p.beta = beta;
     p.smooth = label_smoothing;
     p.mean = (flags & ISO_PREF_MEAN) != 0;
@@ -654,23 +847,25 @@ int iso_pref_loss(const float* logp, const float* ref_logp, const uint8_t* mask,
     p.pair_loss = pair_loss;
     p.reward = reward;
     p.grad = grad;
-    p.sums = PartSums{reinterpret_cast<double2*>(ws + pl.off_head), reinterpret_cast<double2*>(ws + pl.off_tail),
-                      reinterpret_cast<double2*>(ws + pl.off_whole)};
+    p.sums = pl.sums.at(ws);
     p.each = reinterpret_cast<double*>(ws + pl.off_each);
     p.coef = reinterpret_cast<float*>(ws + pl.off_coef);
-    const int64_t spans = pairs ? spans_of(tokens) : 0;
-    if (tokens <= kOneMax && pairs <= kOneMax) {
-        hipLaunchKernelGGL(k_pref_one, dim3(1), dim3(kOneNT), 0, st, p, spans);
+    if (small_call(p.sq)) {
+        hipLaunchKernelGGL(k_pref_one, dim3(1), dim3(kOneNT), 0, st, p, spans_of(tokens, 1));
         return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
     }
     const dim3 nt(kLossNT);
+    const uint32_t spans = spans_of(tokens, kSpanG);
     hipLaunchKernelGGL(k_pref_sums, wave_grid(spans), nt, 0, st, p, spans);
     hipLaunchKernelGGL(k_pref_pairs, wave_grid(pairs), nt, 0, st, p);
     hipLaunchKernelGGL(k_pref_grad, dim3(grad ? wave_grid(spans).x + 1 : 1), nt, 0, st, p, spans);
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 
-size_t iso_policy_loss_workspace_bytes(int64_t tokens, int64_t seqs) { return iso::policy_workspace(tokens, seqs); }
+size_t iso_policy_loss_workspace_bytes(int64_t tokens, int64_t seqs) {
+    if (tokens < 0 || seqs < 0 || tokens > 0x7fffffffLL || seqs > 0x7fffffffLL) return 0;
+    return iso::PolicyPlan(tokens, seqs).bytes;
+}
 
 int iso_policy_loss(const float* logp, const float* old_logp, const float* ref_logp, const float* adv,
                     const uint8_t* mask, const int32_t* seq_off, int64_t seqs, int64_t tokens, double clip_lo,
@@ -691,11 +886,21 @@ int iso_policy_loss(const float* logp, const float* old_logp, const float* ref_l
     const size_t need = iso_policy_loss_workspace_bytes(tokens, seqs);
     if (!workspace || workspace_bytes < need) return ISO_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return ISO_ERR_ARG;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    const PolicyPlan pl(tokens, seqs);
     const Policy p = make_policy(old_logp, ref_logp, adv, clip_lo, clip_hi, kl_coef, norm, grad_scale, flags);
-    const Seqs sq{seq_off, seqs, tokens, seqs ? tokens / seqs : 0};
-    const hipError_t e = launch_policy<float>(p, logp, mask, nullptr, sq, loss, counts, grad, workspace,
-                                              static_cast<hipStream_t>(stream));
-    return e == hipSuccess ? ISO_OK : ISO_ERR_HIP;
+    PolicyCall f{make_weights(p, Live{mask, nullptr}, make_seqs(seq_off, seqs, tokens), pl.w, ws), logp, loss, counts,
+                 grad, reinterpret_cast<PolicySums*>(ws + pl.off_part)};
+    if (small_call(f.c.sq)) {
+        hipLaunchKernelGGL(k_policy_one, dim3(1), dim3(kOneNT), 0, st, f, spans_of(tokens, 1));
+        return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
+    }
+    start_weights(f.c, st);
+    const uint32_t spans = spans_of(tokens, kTermG);
+    const dim3 grid = wave_grid(spans);
+    hipLaunchKernelGGL(k_policy_tokens, grid, dim3(kLossNT), 0, st, f, spans);
+    return launch_policy_out(p, f.part, (int)grid.x, loss, counts, st) == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 
 }  // extern "C"

@@ -9,19 +9,69 @@
 
 namespace iso {
 
+// A value of another lane by data-parallel primitive (row_shr and the row
+// broadcasts of a wave scan, shifts by one lane); lanes without a source keep `old`.
+template <int CTRL, int RM>
+__device__ __forceinline__ int dpp(int old, int v) {
+    return __builtin_amdgcn_update_dpp(old, v, CTRL, RM, 0xf, false);
+}
+template <int CTRL, int RM>
+__device__ __forceinline__ double dpp(double v) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)dpp<CTRL, RM>(0, (int)(uint32_t)u);
+    const uint32_t hi = (uint32_t)dpp<CTRL, RM>(0, (int)(uint32_t)(u >> 32));
+    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+constexpr int kShl1 = 0x130, kShr1 = 0x138;  // by one lane, over the whole wave
+
+// f.template step<CTRL, ROW_MASK>() for each step of an inclusive scan over a wave.
+template <typename F>
+__device__ __forceinline__ void wave_scan(F& f) {
+    f.template step<0x111, 0xf>();  // row_shr 1, 2, 4, 8 within rows of 16 lanes
+    f.template step<0x112, 0xf>();
+    f.template step<0x114, 0xf>();
+    f.template step<0x118, 0xf>();
+    f.template step<0x142, 0xa>();  // lane 15 of rows 0, 2 to rows 1, 3
+    f.template step<0x143, 0xc>();  // lane 31 to rows 2, 3
+}
+
+__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+__device__ __forceinline__ double lane_value(double v, int lane) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)lane_value((int)(uint32_t)u, lane);
+    const uint32_t hi = (uint32_t)lane_value((int)(uint32_t)(u >> 32), lane);
+    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+
+// Sums over the wave, the same value in every lane (all lanes active).
+struct SumStep {
+    double v;
+    template <int CTRL, int RM>
+    __device__ __forceinline__ void step() { v += dpp<CTRL, RM>(v); }
+};
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-    return v;
+    SumStep s{v};
+    wave_scan(s);
+    return lane_value(s.v, 63);
+}
+struct IntSumStep {
+    int v;
+    template <int CTRL, int RM>
+    __device__ __forceinline__ void step() { v += dpp<CTRL, RM>(0, v); }
+};
+__device__ __forceinline__ int wave_sum(int v) {
+    IntSumStep s{v};
+    wave_scan(s);
+    return lane_value(s.v, 63);
 }
 
 // Sum over the workgroup (NT threads), the same value in every thread.
-template <int NT>
-__device__ __forceinline__ double wg_sum(double v, double* red) {
+template <int NT, typename T>
+__device__ __forceinline__ T wg_sum(T v, T* red) {
     v = wave_sum(v);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    double s = 0.0;
+    T s = 0;
 #pragma unroll
     for (int k = 0; k < NT / 64; ++k) s += red[k];
     __syncthreads();
@@ -29,22 +79,22 @@ __device__ __forceinline__ double wg_sum(double v, double* red) {
 }
 
 // Sequences of tokens: packed by offsets (held inside [0, tokens]), or all of
-// one length.
+// one length.  Tokens and sequences are below 2^31.
 struct Seqs {
     const int32_t* off;
-    int64_t n;       // sequences
-    int64_t tokens;
-    int64_t len;     // common length (off == NULL)
-    __device__ __forceinline__ int64_t begin(int64_t q) const {
+    uint32_t n;  // sequences
+    uint32_t tokens;
+    uint32_t len;  // common length (off == NULL)
+    __device__ __forceinline__ uint32_t begin(uint32_t q) const {
         if (!off) return q * len;
-        const int64_t b = off[q];
-        return b < 0 ? 0 : b > tokens ? tokens : b;
+        const int32_t b = off[q];
+        return b < 0 ? 0u : min((uint32_t)b, tokens);
     }
-    __device__ __forceinline__ int64_t end(int64_t q) const {
-        const int64_t b = begin(q), e = begin(q + 1);
-        return e < b ? b : e;
-    }
+    __device__ __forceinline__ uint32_t end(uint32_t q) const { return max(begin(q), begin(q + 1)); }
 };
+inline Seqs make_seqs(const int32_t* off, int64_t seqs, int64_t tokens) {
+    return Seqs{off, (uint32_t)seqs, (uint32_t)tokens, seqs ? (uint32_t)(tokens / seqs) : 0u};
+}
 
 // The clipped policy loss of one token.  With d = logp - old (exact in f64 for
 // f32 inputs), the clip is decided on d against the logarithms of the bounds:
@@ -61,6 +111,42 @@ struct Policy {
     double norm;               // > 0: in place of the count of tokens or sequences
     double grad_scale;
 };
+// exp(x), exp(x) - 1 and exp(x) - 1 - x in f64.  Cody and Waite's reduction
+// x = k ln 2 + r with |r| <= ln(2)/2, then Taylor's series of exp(r) - 1 - r to
+// r^11 (the rest is below 6e-15 of 1): where k = 0 the small differences come
+// from the series alone and keep their relative accuracy.  A third of the
+// instructions of the library's exp and expm1, whose last bits an f32 output
+// does not show (the policy loss of 8e6 tokens is bound by them).
+struct ExpTerms {
+    double e, m1, m2;  // exp(x), exp(x) - 1, exp(x) - 1 - x
+};
+__device__ __forceinline__ ExpTerms exp_terms(double x) {
+    constexpr double kRound = 0x1.8p52;  // adding it rounds to a whole number, held in the low bits
+    const double c = x > 800.0 ? 800.0 : x < -800.0 ? -800.0 : x;  // NaN stays
+    const double t = fma(c, 1.4426950408889634, kRound);
+    const double kd = t - kRound;
+    const int k = (int)(uint32_t)__double_as_longlong(t);
+    double r = fma(kd, -0x1.62e42fefa39efp-1, c);  // ln 2 in f64, and the rest of it
+    r = fma(kd, -0x1.abc9e3b39803fp-56, r);
+    double q = 1.0 / 39916800.0;
+    q = fma(q, r, 1.0 / 3628800.0);
+    q = fma(q, r, 1.0 / 362880.0);
+    q = fma(q, r, 1.0 / 40320.0);
+    q = fma(q, r, 1.0 / 5040.0);
+    q = fma(q, r, 1.0 / 720.0);
+    q = fma(q, r, 1.0 / 120.0);
+    q = fma(q, r, 1.0 / 24.0);
+    q = fma(q, r, 1.0 / 6.0);
+    q = fma(q, r, 0.5);
+    q *= r * r;
+    ExpTerms o;
+    o.e = ldexp(1.0 + (r + q), k);
+    const bool near0 = kd == 0.0;
+    o.m1 = near0 ? r + q : o.e - 1.0;
+    o.m2 = near0 ? q : o.m1 - x;
+    return o;
+}
+
 struct PolicyTerm {
     double pg, kl, slope;  // slope: derivative of pg + kl_coef kl in logp
     bool over;             // held by the clip
@@ -69,26 +155,37 @@ __device__ __forceinline__ PolicyTerm policy_term(const Policy& p, double lp, do
     const double d = lp - old;
     PolicyTerm o;
     o.over = a > 0.0 ? d > p.up : a < 0.0 ? d < p.low : false;
-    const double ra = exp(d) * a;
+    const double ra = exp_terms(d).e * a;
     o.pg = o.over ? -(a > 0.0 ? p.edge_hi : p.edge_lo) * a : -ra;
     o.slope = o.over ? 0.0 : -ra;
     o.kl = 0.0;
     if (p.ref_logp) {
-        const double u = ref - lp;
-        const double em = expm1(u);
-        o.kl = em - u;
-        o.slope -= p.kl_coef * em;
+        const ExpTerms u = exp_terms(ref - lp);
+        o.kl = u.m2;
+        o.slope -= p.kl_coef * u.m1;
     }
     return o;
 }
 
-// The policy loss over tokens' log-probabilities (LP: f32, or f64 from the
-// logits), live where mask is NULL or non-zero and target is NULL or >= 0.
-size_t policy_workspace(int64_t tokens, int64_t seqs);
-template <typename LP>
-hipError_t launch_policy(const Policy& p, const LP* logp, const uint8_t* mask, const int32_t* target,
-                         const Seqs& sq, float* loss, int32_t* counts, float* grad, void* workspace,
-                         hipStream_t st);
+// Sums over tokens: w pg, w kl; tokens that take part, tokens held by the clip.
+struct PolicySums {
+    double pg, kl;
+    int live, over;
+};
+
+// A row's part in the policy loss from logits: its weight w_t (0: it takes no
+// part) and its advantage.
+struct RowTerm {
+    double w;
+    float adv, pad;
+};
+// Every row's, from the rows' targets (negative: no part) and the sequences.
+size_t row_terms_workspace(int64_t rows, int64_t seqs);
+hipError_t launch_row_terms(const Policy& p, const int32_t* target, const Seqs& sq, RowTerm* terms, void* workspace,
+                            hipStream_t st);
+// The loss and the counts from `parts` sums.
+hipError_t launch_policy_out(const Policy& p, const PolicySums* part, int parts, float* loss, int32_t* counts,
+                             hipStream_t st);
 
 // Argument checks of the policy loss that do not depend on where logp comes from.
 bool policy_args_ok(const float* old_logp, const float* ref_logp, const float* adv, const int32_t* seq_off,
