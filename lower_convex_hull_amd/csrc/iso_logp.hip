@@ -5,6 +5,8 @@
 #include "../../include/iso.h"
 #include "iso_losses.hpp"
 
+#include <type_traits>
+
 namespace iso {
 namespace {
 
@@ -22,15 +24,6 @@ struct Wide {
 template <typename T>
 __device__ __forceinline__ typename Wide<T>::V load_wide(const T* p) {
     return *reinterpret_cast<const typename Wide<T>::V*>(p);
-}
-
-// The same with elements at or past `avail` filled with -infinity (they add nothing).
-template <typename T>
-__device__ __forceinline__ typename Wide<T>::V load_part(const T* p, int64_t avail) {
-    typename Wide<T>::V v;
-#pragma unroll
-    for (int i = 0; i < Wide<T>::N; ++i) v[i] = i < avail ? p[i] : (T)-INFINITY;
-    return v;
 }
 
 // exp((x - m)/T) = exp2((x - m) c), c = log2(e)/T.  The difference to the
@@ -79,35 +72,60 @@ __device__ __forceinline__ Stat wave_join(Stat a, const Scale& sc) {
     return a;
 }
 
-// The statistics of x[k0, k1) by a workgroup of NT threads; thread 0 has them.
-// Each thread takes U vectors at a time: their maximum first, then the sums in
-// f32 (U*8 terms at most), joined in f64 to the sums so far, which are scaled
-// when the maximum rises.
-template <typename T, bool ENT, int NT, int U>
-__device__ __forceinline__ Stat row_stat(const T* __restrict__ x, int64_t k0, int64_t k1, const Scale& sc,
-                                         Stat* part) {
-    constexpr int N = Wide<T>::N;
-    float m = -INFINITY;
-    double s = 0.0, h = 0.0;
-    for (int64_t k = k0; k < k1; k += (int64_t)NT * N * U) {
-        typename Wide<T>::V v[U];
-        const int64_t at = k + (int64_t)threadIdx.x * N;
-        if (k + (int64_t)NT * N * U <= k1) {
+// Positions in a row are below 2^30.  Of a piece [k0, k1) of a row, the whole
+// vectors go through chunks; up to N - 1 elements are left, one a thread.
+template <typename T>
+__device__ __forceinline__ int body_end(int k0, int k1) { return k0 + (k1 - k0) / Wide<T>::N * Wide<T>::N; }
+
+// A chunk of a row: U vectors a thread of NT, those past k1 filled with
+// -infinity (they add nothing).
+template <typename T, int NT, int U>
+struct Chunk {
+    static constexpr int N = Wide<T>::N;
+    static constexpr int kSize = NT * U * N;
+    typename Wide<T>::V v[U];
+    __device__ __forceinline__ static int at(int k, int u) { return k + u * NT * N + (int)threadIdx.x * N; }
+    __device__ __forceinline__ void load(const T* x, int k, int k1) {
+        const T* b = x + k;
+        if (k1 - k >= kSize) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = load_wide<T>(x + at + (int64_t)u * NT * N);
+            for (int u = 0; u < U; ++u) v[u] = load_wide<T>(b + u * NT * N + threadIdx.x * N);
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t p = at + (int64_t)u * NT * N;
-                if (p + N <= k1) v[u] = load_wide<T>(x + p);
-                else v[u] = load_part<T>(x + p, k1 - p);
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[u][i] = (T)-INFINITY;
+                if (at(k, u) < k1) v[u] = load_wide<T>(b + u * NT * N + threadIdx.x * N);
             }
         }
+    }
+    // What was computed of the values so far is not kept in registers, only
+    // the values: their f32 forms take twice the room and are made again.
+    __device__ __forceinline__ void forget() {
+        typedef int Raw __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            Raw r = __builtin_bit_cast(Raw, v[u]);
+            asm volatile("" : "+v"(r));
+            v[u] = __builtin_bit_cast(typename Wide<T>::V, r);
+        }
+    }
+};
+
+// A thread's running statistics.  A chunk adds its maximum first, then its sums
+// in f32 (U*8 terms at most), joined in f64 to the sums so far, which are
+// scaled when the maximum rises.
+template <typename T, bool ENT, int NT, int U>
+struct Running {
+    float m = -INFINITY;
+    double s = 0.0, h = 0.0;
+    __device__ __forceinline__ void add(Chunk<T, NT, U>& c, const Scale& sc) {
+        constexpr int N = Wide<T>::N;
         float bm = -INFINITY;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < N; ++i) bm = fmaxf(bm, (float)v[u][i]);
+            for (int i = 0; i < N; ++i) bm = fmaxf(bm, (float)c.v[u][i]);
         if (bm > m) {
             if (m != -INFINITY) {
                 const float d = held((m - bm) * sc.cf), f = __builtin_amdgcn_exp2f(d);
@@ -118,11 +136,12 @@ __device__ __forceinline__ Stat row_stat(const T* __restrict__ x, int64_t k0, in
         }
         const float base = base_of(m);
         float fs = 0.0f, fh = 0.0f;
+        c.forget();
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float a = ((float)v[u][i] - base) * sc.cf;
+                const float a = ((float)c.v[u][i] - base) * sc.cf;
                 const float e = __builtin_amdgcn_exp2f(a);
                 fs += e;
                 if (ENT) fh = fmaf(e, held(a), fh);
@@ -130,13 +149,41 @@ __device__ __forceinline__ Stat row_stat(const T* __restrict__ x, int64_t k0, in
         s += (double)fs;
         if (ENT) h += (double)fh;
     }
-    Stat a = wave_join<ENT>(Stat{(double)m, s, h}, sc);
-    if (NT == 64) return a;
-    const int lane = threadIdx.x & 63;
-    if (lane == 0) part[threadIdx.x >> 6] = a;
-    __syncthreads();
-    if (threadIdx.x < 64) a = wave_join<ENT>(lane < NT / 64 ? part[lane] : Stat{-INFINITY, 0.0, 0.0}, sc);
-    return a;
+    // One more value, of those that whole vectors leave over.
+    __device__ __forceinline__ void add_one(float x, const Scale& sc) {
+        Stat a{(double)m, s, h};
+        if (x > m) {
+            rebase<ENT>(a, (double)x, sc);
+            m = x;
+        }
+        const float d = (x - base_of(m)) * sc.cf, e = __builtin_amdgcn_exp2f(d);
+        s = a.s + (double)e;
+        if (ENT) h = a.h + (double)(e * held(d));
+    }
+    // The workgroup's, in thread 0.
+    __device__ __forceinline__ Stat join(const Scale& sc, Stat* part) const {
+        Stat a = wave_join<ENT>(Stat{(double)m, s, h}, sc);
+        if (NT == 64) return a;
+        const int lane = threadIdx.x & 63;
+        if (lane == 0) part[threadIdx.x >> 6] = a;
+        __syncthreads();
+        if (threadIdx.x < 64) a = wave_join<ENT>(lane < NT / 64 ? part[lane] : Stat{-INFINITY, 0.0, 0.0}, sc);
+        return a;
+    }
+};
+
+// The statistics of x[k0, k1) by a workgroup of NT threads; thread 0 has them.
+template <typename T, bool ENT, int NT, int U>
+__device__ __forceinline__ Stat row_stat(const T* __restrict__ x, int k0, int k1, const Scale& sc, Stat* part) {
+    Running<T, ENT, NT, U> run;
+    const int end = body_end<T>(k0, k1);
+    for (int k = k0; k < end; k += Chunk<T, NT, U>::kSize) {
+        Chunk<T, NT, U> c;
+        c.load(x, k, end);
+        run.add(c, sc);
+    }
+    if ((int)threadIdx.x < k1 - end) run.add_one((float)x[end + threadIdx.x], sc);
+    return run.join(sc, part);
 }
 
 // A row's log-sum and its target's log-probability from its statistics and the
@@ -146,11 +193,11 @@ struct RowLogp {
     double lse, logp, entropy;
 };
 template <typename T>
-__device__ __forceinline__ RowLogp row_logp(const T* x, int32_t j, int64_t vocab, double inv_t, const Stat& a) {
+__device__ __forceinline__ RowLogp row_logp(T xj, int32_t j, int vocab, double inv_t, const Stat& a) {
     const double ls = log(a.s);
     const bool none = a.m == -INFINITY;
     return RowLogp{none ? __builtin_nan("") : a.m * inv_t + ls,
-                   none || j >= vocab ? __builtin_nan("") : ((double)(float)x[j] - a.m) * inv_t - ls,
+                   none || j >= vocab ? __builtin_nan("") : ((double)(float)xj - a.m) * inv_t - ls,
                    none ? __builtin_nan("") : ls - kLn2 * (a.h / a.s)};
 }
 
@@ -159,9 +206,9 @@ struct LogpOut {
     float *logp, *lse, *ent;
 };
 template <typename T>
-__device__ __forceinline__ void write_row(const LogpOut& o, int64_t r, const T* x, int32_t j, int64_t vocab,
+__device__ __forceinline__ void write_row(const LogpOut& o, int64_t r, const T* x, int32_t j, int vocab,
                                           double inv_t, const Stat& a) {
-    const RowLogp v = j >= 0 ? row_logp(x, j, vocab, inv_t, a) : RowLogp{0.0, 0.0, 0.0};
+    const RowLogp v = j >= 0 ? row_logp(x[j < vocab ? j : 0], j, vocab, inv_t, a) : RowLogp{0.0, 0.0, 0.0};
     o.logp[r] = (float)v.logp;
     o.lse[r] = (float)v.lse;
     if (o.ent) o.ent[r] = (float)v.entropy;
@@ -175,9 +222,9 @@ inline dim3 grid_of(int64_t items) { return dim3((unsigned)(items < kMaxGrid ? i
 // Item = (row, part of it).  With one part a row its outputs are written, else
 // the part's statistics.
 template <typename T, bool ENT, int NT>
-__global__ __launch_bounds__(NT) void k_token_logp(const T* __restrict__ logits, int64_t rows, int64_t vocab,
+__global__ __launch_bounds__(NT) void k_token_logp(const T* __restrict__ logits, int64_t rows, int vocab,
                                                    int64_t ld, const int32_t* __restrict__ target, Scale sc,
-                                                   int splits, int64_t chunk, LogpOut o, Stat* __restrict__ parts) {
+                                                   int splits, int chunk, LogpOut o, Stat* __restrict__ parts) {
     __shared__ Stat part[NT / 64];
     for (int64_t item = blockIdx.x; item < rows * splits; item += gridDim.x) {
         const int64_t r = item / splits;
@@ -185,7 +232,7 @@ __global__ __launch_bounds__(NT) void k_token_logp(const T* __restrict__ logits,
         const T* x = logits + r * ld;
         Stat a{};
         if (j >= 0) {
-            const int64_t k0 = (item - r * splits) * chunk, k1 = min(k0 + chunk, vocab);
+            const int k0 = (int)(item - r * splits) * chunk, k1 = min(k0 + chunk, vocab);
             a = row_stat<T, ENT, NT, 4>(x, k0, k1, sc, part);
         }
         if (threadIdx.x == 0) {
@@ -199,8 +246,8 @@ __global__ __launch_bounds__(NT) void k_token_logp(const T* __restrict__ logits,
 // A wave a row: the parts' statistics joined (in a fixed order), the outputs written.
 constexpr int kJoinNT = 256;
 template <typename T, bool ENT>
-__global__ __launch_bounds__(kJoinNT) void k_token_logp_join(const T* __restrict__ logits, int64_t rows,
-                                                             int64_t vocab, int64_t ld,
+__global__ __launch_bounds__(kJoinNT) void k_token_logp_join(const T* __restrict__ logits, int64_t rows, int vocab,
+                                                             int64_t ld,
                                                              const int32_t* __restrict__ target, Scale sc,
                                                              int splits, const Stat* __restrict__ parts, LogpOut o) {
     const int lane = threadIdx.x & 63;
@@ -238,19 +285,22 @@ __device__ __forceinline__ RowGrad row_grad(double lse, double g, double ent, do
     return o;
 }
 
+// An element's gradient (but for the target's own g/T).
+template <bool ENT>
+__device__ __forceinline__ float grad_one(float x, const RowGrad& q, float cf) {
+    const float d = x - q.mh;
+    const float p = __builtin_amdgcn_exp2f(d * cf);
+    return ENT ? p * fmaf(q.b, held(d), q.a) : p * q.a;
+}
 // N elements of a row's gradient from position k on; j: the target's position.
 template <typename T, bool ENT>
-__device__ __forceinline__ typename Wide<T>::V grad_wide(const typename Wide<T>::V& x, int64_t k, int64_t j,
-                                                         const RowGrad& q, float cf) {
+__device__ __forceinline__ typename Wide<T>::V grad_wide(const typename Wide<T>::V& x, int k, int j, const RowGrad& q,
+                                                         float cf) {
     constexpr int N = Wide<T>::N;
     float v[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float d = (float)x[i] - q.mh;
-        const float p = __builtin_amdgcn_exp2f(d * cf);
-        v[i] = ENT ? p * fmaf(q.b, held(d), q.a) : p * q.a;
-    }
-    if ((uint64_t)(j - k) < (uint64_t)N) {
+    for (int i = 0; i < N; ++i) v[i] = grad_one<ENT>((float)x[i], q, cf);
+    if ((unsigned)(j - k) < (unsigned)N) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (j - k == i) v[i] += q.hot;
@@ -262,72 +312,59 @@ __device__ __forceinline__ typename Wide<T>::V grad_wide(const typename Wide<T>:
 }
 
 template <typename T>
-__device__ __forceinline__ void store_wide(T* p, const typename Wide<T>::V& v, int64_t avail) {
-    constexpr int N = Wide<T>::N;
-    if (avail >= N) {
-        *reinterpret_cast<typename Wide<T>::V*>(p) = v;
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (i < avail) p[i] = v[i];
-    }
+__device__ __forceinline__ void store_wide(T* p, const typename Wide<T>::V& v) {
+    __builtin_nontemporal_store(v, reinterpret_cast<typename Wide<T>::V*>(p));
 }
 
-// The gradient of x[k0, k1) by NT threads, U vectors at a time.
+// A chunk's gradient written, from position k on.
 template <typename T, bool ENT, int NT, int U>
-__device__ __forceinline__ void row_grads(const T* x, T* o, int64_t k0, int64_t k1, int64_t j, const RowGrad& q,
-                                          float cf) {
-    constexpr int N = Wide<T>::N;
-    for (int64_t k = k0; k < k1; k += (int64_t)NT * N * U) {
-        const int64_t at = k + (int64_t)threadIdx.x * N;
-        typename Wide<T>::V v[U];
-        if (k + (int64_t)NT * N * U <= k1) {
+__device__ __forceinline__ void store_grads(const Chunk<T, NT, U>& c, T* o, int k, int k1, int j, const RowGrad& q,
+                                            float cf) {
+    typedef Chunk<T, NT, U> C;
+    T* b = o + k;
+    if (k1 - k >= C::kSize) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = load_wide<T>(x + at + (int64_t)u * NT * N);
+        for (int u = 0; u < U; ++u)
+            store_wide<T>(b + u * NT * C::N + threadIdx.x * C::N, grad_wide<T, ENT>(c.v[u], C::at(k, u), j, q, cf));
+    } else {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t p = at + (int64_t)u * NT * N;
-                *reinterpret_cast<typename Wide<T>::V*>(o + p) = grad_wide<T, ENT>(v[u], p, j, q, cf);
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t p = at + (int64_t)u * NT * N;
-                if (p + N <= k1) v[u] = load_wide<T>(x + p);
-                else v[u] = load_part<T>(x + p, k1 - p);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t p = at + (int64_t)u * NT * N;
-                store_wide<T>(o + p, grad_wide<T, ENT>(v[u], p, j, q, cf), k1 - p);
-            }
-        }
+        for (int u = 0; u < U; ++u)
+            if (C::at(k, u) < k1)
+                store_wide<T>(b + u * NT * C::N + threadIdx.x * C::N, grad_wide<T, ENT>(c.v[u], C::at(k, u), j, q, cf));
     }
+}
+// That of the elements that whole vectors leave over, one a thread.
+template <typename T, bool ENT>
+__device__ __forceinline__ void store_rest(const T* x, T* o, int end, int k1, int j, const RowGrad& q, float cf) {
+    const int k = end + (int)threadIdx.x;
+    if (k < k1) o[k] = (T)(grad_one<ENT>((float)x[k], q, cf) + (j == k ? q.hot : 0.0f));
 }
 
 // A row's gradient where it is one value: 0 (ignored) or NaN.
 template <typename T, int NT>
-__device__ __forceinline__ void fill_row(T* o, int64_t k0, int64_t k1, T v) {
+__device__ __forceinline__ void fill_row(T* o, int k0, int k1, T v) {
     constexpr int N = Wide<T>::N;
     typename Wide<T>::V w;
 #pragma unroll
     for (int i = 0; i < N; ++i) w[i] = v;
-    for (int64_t k = k0 + (int64_t)threadIdx.x * N; k < k1; k += (int64_t)NT * N) store_wide<T>(o + k, w, k1 - k);
+    const int end = body_end<T>(k0, k1);
+    for (int k = k0 + (int)threadIdx.x * N; k < end; k += NT * N) store_wide<T>(o + k, w);
+    if ((int)threadIdx.x < k1 - end) o[end + threadIdx.x] = v;
 }
 
 constexpr int kVjpNT = 256;
 
 // Item = (row, chunk of it).
 template <typename T, bool ENT>
-__global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t rows, int64_t vocab, int64_t ld,
+__global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t rows, int vocab, int64_t ld,
                                                      const int32_t* __restrict__ target, double inv_t,
-                                                     double temperature, float cf, int splits, int64_t chunk,
+                                                     double temperature, float cf, int splits, int chunk,
                                                      const float* __restrict__ lse, const float* __restrict__ ent,
                                                      const float* __restrict__ g_logp,
                                                      const float* __restrict__ g_ent, T* grad, int64_t ldg) {
     for (int64_t item = blockIdx.x; item < rows * splits; item += gridDim.x) {
         const int64_t r = item / splits;
-        const int64_t k0 = (item - r * splits) * chunk, k1 = min(k0 + chunk, vocab);
+        const int k0 = (int)(item - r * splits) * chunk, k1 = min(k0 + chunk, vocab);
         const int32_t j = target[r];
         const T* x = logits + r * ld;
         T* o = grad + r * ldg;
@@ -337,7 +374,13 @@ __global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t ro
         }
         const RowGrad q = row_grad((double)lse[r], (double)g_logp[r], ENT ? (double)ent[r] : 0.0,
                                    ENT ? (double)g_ent[r] : 0.0, inv_t, temperature);
-        row_grads<T, ENT, kVjpNT, 4>(x, o, k0, k1, j, q, cf);
+        const int end = body_end<T>(k0, k1);
+        for (int k = k0; k < end; k += Chunk<T, kVjpNT, 4>::kSize) {
+            Chunk<T, kVjpNT, 4> c;
+            c.load(x, k, end);
+            store_grads<T, ENT>(c, o, k, end, j, q, cf);
+        }
+        store_rest<T, ENT>(x, o, end, k1, j, q, cf);
     }
 }
 
@@ -346,15 +389,20 @@ __global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t ro
 // again while the last-level cache may still have it.  Every row's weight and
 // advantage are known before (they depend on the targets alone).
 template <typename T, int NT, int U>
-__global__ __launch_bounds__(NT, 8) void k_policy_rows(const T* logits, int64_t rows, int64_t vocab, int64_t ld,
+__global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t rows, int vocab, int64_t ld,
                                                        const int32_t* __restrict__ target, Scale sc,
                                                        double temperature, Policy p,
                                                        const RowTerm* __restrict__ terms, float* __restrict__ logp,
                                                        T* grad, int64_t ldg, PolicySums* __restrict__ sums) {
+    typedef Chunk<T, NT, U> C;
     __shared__ Stat part[NT / 64];
     __shared__ double of_row[2];  // log-sum, gradient of the token's logp
     __shared__ PolicySums total;  // thread 0's
     if (threadIdx.x == 0) total = PolicySums{0.0, 0.0, 0, 0};
+    // the first chunk is what whole chunks leave over
+    const int end = body_end<T>(0, vocab);
+    const int before = end ? (end - 1) / C::kSize : 0;  // whole chunks after it
+    const int first = end - before * C::kSize;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const int32_t j = target[r];
         const T* x = logits + r * ld;
@@ -364,28 +412,50 @@ __global__ __launch_bounds__(NT, 8) void k_policy_rows(const T* logits, int64_t 
             if (grad) fill_row<T, NT>(o, 0, vocab, (T)0.0f);
             continue;
         }
-        const Stat a = row_stat<T, false, NT, U>(x, 0, vocab, sc, part);
+        const RowTerm t = terms[r];
+        const float old = p.old_logp[r], ref = p.ref_logp ? p.ref_logp[r] : 0.0f;
+        const T xj = x[j < vocab ? j : 0];
+        C c;
+        Running<T, false, NT, U> run;
+        int k = 0, e = first;
+        do {
+            c.load(x, k, e);
+            run.add(c, sc);
+            k = e;
+            e += C::kSize;
+        } while (k < end);
+        if ((int)threadIdx.x < vocab - end) run.add_one((float)x[end + threadIdx.x], sc);
+        c.forget();
+        const Stat a = run.join(sc, part);
         if (threadIdx.x == 0) {
-            const RowLogp v = row_logp(x, j, vocab, sc.inv_t, a);
-            const RowTerm t = terms[r];
-            const PolicyTerm k = policy_term(p, v.logp, (double)p.old_logp[r], p.ref_logp ? (double)p.ref_logp[r] : 0.0,
-                                             (double)t.adv);
+            const RowLogp v = row_logp(xj, j, vocab, sc.inv_t, a);
+            const double d[1] = {v.logp - (double)old}, u[1] = {p.ref_logp ? (double)ref - v.logp : 0.0};
+            const float adv[1] = {t.adv};
+            PolicyTerm o1[1];
+            policy_terms(p, ExpSeries(), d, u, adv, o1);
+            const PolicyTerm& k1 = o1[0];
             logp[r] = (float)v.logp;
-            total.pg += t.w * k.pg;
-            total.kl += t.w * k.kl;
+            total.pg += t.w * k1.pg;
+            total.kl += t.w * k1.kl;
             total.live += 1;
-            total.over += k.over ? 1 : 0;
+            total.over += k1.over ? 1 : 0;
             of_row[0] = v.lse;
-            of_row[1] = k.slope * (t.w * p.grad_scale);
+            of_row[1] = k1.slope * (t.w * p.grad_scale);
         }
         __syncthreads();
-        if (grad) {
-            if (j >= vocab) {
-                fill_row<T, NT>(o, 0, vocab, (T)__builtin_nanf(""));
-            } else {
-                const RowGrad q = row_grad(of_row[0], of_row[1], 0.0, 0.0, sc.inv_t, temperature);
-                row_grads<T, false, NT, U>(x, o, 0, vocab, j, q, sc.cf);
+        if (grad && j < vocab) {
+            const RowGrad q = row_grad(of_row[0], of_row[1], 0.0, 0.0, sc.inv_t, temperature);
+            store_rest<T, false>(x, o, end, vocab, j, q, sc.cf);
+            // the last chunk is still in registers, the others follow backwards
+            for (e = end;;) {
+                k = max(e - C::kSize, 0);
+                store_grads<T, false>(c, o, k, e, j, q, sc.cf);
+                if (k == 0) break;
+                e = k;
+                c.load(x, max(e - C::kSize, 0), e);
             }
+        } else if (grad) {
+            fill_row<T, NT>(o, 0, vocab, (T)__builtin_nanf(""));
         }
         __syncthreads();  // part and of_row are used again
     }
@@ -448,14 +518,14 @@ void start_logp_t(const T* x, int64_t rows, int64_t vocab, int64_t ld, const int
     const Scale sc = scale_of(temperature);
     Stat* parts = static_cast<Stat*>(workspace);
     if (rows * pl.splits < kLogpGrid)
-        hipLaunchKernelGGL((k_token_logp<T, ENT, 1024>), grid_of(rows * pl.splits), dim3(1024), 0, st, x, rows, vocab,
-                           ld, target, sc, pl.splits, pl.chunk, o, parts);
+        hipLaunchKernelGGL((k_token_logp<T, ENT, 1024>), grid_of(rows * pl.splits), dim3(1024), 0, st, x, rows,
+                           (int)vocab, ld, target, sc, pl.splits, (int)pl.chunk, o, parts);
     else
-        hipLaunchKernelGGL((k_token_logp<T, ENT, 256>), grid_of(rows * pl.splits), dim3(256), 0, st, x, rows, vocab, ld,
-                           target, sc, pl.splits, pl.chunk, o, parts);
+        hipLaunchKernelGGL((k_token_logp<T, ENT, 256>), grid_of(rows * pl.splits), dim3(256), 0, st, x, rows,
+                           (int)vocab, ld, target, sc, pl.splits, (int)pl.chunk, o, parts);
     if (pl.splits > 1)
         hipLaunchKernelGGL((k_token_logp_join<T, ENT>), grid_of((rows + kJoinNT / 64 - 1) / (kJoinNT / 64)),
-                           dim3(kJoinNT), 0, st, x, rows, vocab, ld, target, sc, pl.splits, parts, o);
+                           dim3(kJoinNT), 0, st, x, rows, (int)vocab, ld, target, sc, pl.splits, parts, o);
 }
 
 template <typename T>
@@ -473,14 +543,14 @@ void start_vjp(const void* logits, int64_t rows, int64_t vocab, int64_t ld, cons
     const Scale sc = scale_of(temperature);
     const T* x = static_cast<const T*>(logits);
     T* o = static_cast<T*>(grad);
-    const int64_t chunk = 4 * 4 * kVjpNT * Wide<T>::N;
+    const int chunk = 4 * 4 * kVjpNT * Wide<T>::N;
     const int splits = (int)((vocab + chunk - 1) / chunk);
     const dim3 grid = grid_of(rows * splits), nt(kVjpNT);
     if (g_ent)
-        hipLaunchKernelGGL((k_logp_vjp<T, true>), grid, nt, 0, st, x, rows, vocab, ld, target, sc.inv_t, temperature,
-                           sc.cf, splits, chunk, lse, ent, g_logp, g_ent, o, ldg);
+        hipLaunchKernelGGL((k_logp_vjp<T, true>), grid, nt, 0, st, x, rows, (int)vocab, ld, target, sc.inv_t,
+                           temperature, sc.cf, splits, chunk, lse, ent, g_logp, g_ent, o, ldg);
     else
-        hipLaunchKernelGGL((k_logp_vjp<T, false>), grid, nt, 0, st, x, rows, vocab, ld, target, sc.inv_t,
+        hipLaunchKernelGGL((k_logp_vjp<T, false>), grid, nt, 0, st, x, rows, (int)vocab, ld, target, sc.inv_t,
                            temperature, sc.cf, splits, chunk, lse, ent, g_logp, g_ent, o, ldg);
 }
 
@@ -493,7 +563,8 @@ void by_dtype(int dtype, F f) {
 }
 
 // Workspace and grid of iso_policy_loss_logits.
-constexpr int64_t kHeadGrid = 2048;
+constexpr int64_t kHeadGrid = 8192;
+constexpr int64_t kHeadWide = 128 << 10, kHeadMid = 40 << 10, kHeadNarrow = 8 << 10;  // bytes of a row
 struct HeadPlan {
     int grid;
     size_t off_terms, off_sums, off_weights, bytes;
@@ -515,12 +586,18 @@ void start_rows(const void* logits, int64_t rows, int64_t vocab, int64_t ld, con
     const T* x = static_cast<const T*>(logits);
     T* o = static_cast<T*>(grad);
     const Scale sc = scale_of(temperature);
-    if (vocab * (int64_t)sizeof(T) >= 32 << 10)
-        hipLaunchKernelGGL((k_policy_rows<T, 1024, 4>), dim3(grid), dim3(1024), 0, st, x, rows, vocab, ld, target, sc,
+    const int64_t bytes = vocab * (int64_t)sizeof(T);
+    auto start = [&](auto nt, auto u) {
+        constexpr int NT = decltype(nt)::value, U = decltype(u)::value;
+        hipLaunchKernelGGL((k_policy_rows<T, NT, U>), dim3(grid), dim3(NT), 0, st, x, rows, (int)vocab, ld, target, sc,
                            temperature, p, terms, logp, o, ldg, sums);
-    else
-        hipLaunchKernelGGL((k_policy_rows<T, 256, 4>), dim3(grid), dim3(256), 0, st, x, rows, vocab, ld, target, sc,
-                           temperature, p, terms, logp, o, ldg, sums);
+    };
+    typedef std::integral_constant<int, 4> Four;
+    typedef std::integral_constant<int, 8> Eight;
+    if (bytes > kHeadWide) start(std::integral_constant<int, 1024>{}, Eight{});
+    else if (bytes > kHeadMid) start(std::integral_constant<int, 512>{}, Eight{});
+    else if (bytes > kHeadNarrow) start(std::integral_constant<int, 256>{}, Four{});
+    else start(std::integral_constant<int, 64>{}, Four{});
 }
 
 }  // namespace

@@ -9,10 +9,11 @@ namespace iso {
 namespace {
 
 constexpr int kLossNT = 256;        // threads of a workgroup over many tokens: four waves, a span each
-constexpr int kSpanG = 4;           // a wave's span: 4 groups of 256 tokens, 4 a lane in each
+constexpr int kSpanG = 2;           // a wave's span: 2 groups of 256 tokens, 4 a lane in each
 constexpr int kTermG = 2;           // the same where the policy's terms are computed, which take more registers
+constexpr int kTermWaves = 4;       // waves a SIMD holds of them
 constexpr int kOneNT = 1024;        // the one workgroup of a small call, whose spans are one group
-constexpr int64_t kOneMax = 16384;  // tokens (and sequences) up to which one workgroup takes the whole call
+constexpr int64_t kOneMax = 4096;  // tokens (and sequences) up to which one workgroup takes the whole call
 
 // A span of G groups and a lane's tokens of it: group g holds tokens at(g) .. at(g)+3.
 template <int G>
@@ -29,7 +30,26 @@ struct Place {
 
 typedef float Float4 __attribute__((ext_vector_type(4), aligned(4)));
 
-// The four values from t on, those at or past `end` 0.
+// A lane's four values of each group, those at or past the span's end 0.
+// Whole spans (all but a call's last) take one wide load a group.
+template <int G>
+__device__ __forceinline__ void load_span(const float* __restrict__ p, const Place<G>& w, float* v) {
+    if (w.p1 - w.p0 == 256u * G) {
+        const float* b = p + w.p0;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const Float4 x = *reinterpret_cast<const Float4*>(b + (g * 256u + w.lane * 4u));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * g + i] = x[i];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4 * G; ++k) {
+            const uint32_t t = w.at(k / 4) + k % 4;
+            v[k] = t < w.p1 ? p[t] : 0.0f;
+        }
+    }
+}
 __device__ __forceinline__ void load4(const float* __restrict__ p, uint32_t t, uint32_t end, float* v) {
     if (t + 4 <= end) {
         const Float4 x = *reinterpret_cast<const Float4*>(p + t);
@@ -66,8 +86,9 @@ struct Live {
             if (mask) {
                 uint32_t x;
                 __builtin_memcpy(&x, mask + t, 4);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) b |= ((x >> (8 * i)) & 255u) ? 1u << i : 0u;
+                // the top bit of each byte that is not 0, moved to its lowest; bytes 1, 2, 4, 8 times them summed
+                x = ((((x & 0x7f7f7f7fu) + 0x7f7f7f7fu) | x) & 0x80808080u) >> 7;
+                return __builtin_amdgcn_udot4(x, 0x08040201u, 0u, false);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) b |= target[t + i] >= 0 ? 1u << i : 0u;
@@ -268,14 +289,16 @@ __device__ __forceinline__ void sum_span(const Place<G>& w, uint32_t span, const
     }
 }
 
-// f(t's sequence) for each of a lane's tokens of group g, called once where
-// neighbours share a sequence.
-template <int G, typename V, typename F>
-__device__ __forceinline__ void by_token(const Ids<G>& s, int g, V* v, F f) {
+// f(i, sequence) for a lane's tokens i of group g: once for all four, then
+// f.same(), where they are in one sequence (nearly all lanes).
+template <int G, typename F>
+__device__ __forceinline__ void by_token(const Ids<G>& s, int g, F f) {
+    const int* id = s.id + 4 * g;
+    f(0, s.q0 + (uint32_t)id[0]);
+    f.same();
+    if (id[0] != id[3]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (i > 0 && s.id[4 * g + i] == s.id[4 * g + (i > 0 ? i - 1 : 0)]) v[i] = v[i > 0 ? i - 1 : 0];
-        else v[i] = f(s.q0 + (uint32_t)s.id[4 * g + i]);
+        for (int i = 1; i < 4; ++i) f(i, s.q0 + (uint32_t)id[i]);
     }
 }
 
@@ -353,11 +376,9 @@ __device__ __forceinline__ void pref_sums(const Pref& p, uint32_t span, int* map
     float x[4 * G], y[4 * G];
     double v[4 * G];
     const uint32_t live = p.live.bits(w);
-#pragma unroll
-    for (int g = 0; g < G; ++g) load4(p.logp, w.at(g), w.p1, x + 4 * g);
+    load_span(p.logp, w, x);
     if (p.ref) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) load4(p.ref, w.at(g), w.p1, y + 4 * g);
+        load_span(p.ref, w, y);
     } else {
 #pragma unroll
         for (int k = 0; k < 4 * G; ++k) y[k] = 0.0f;
@@ -394,6 +415,12 @@ __device__ __forceinline__ void pref_pair(const Pref& p, uint32_t i, uint32_t si
     p.reward[2 * i + 1] = (float)(p.beta * r.sum);
 }
 
+struct Coefs {
+    const float* coef;
+    float* c;
+    __device__ __forceinline__ void operator()(int i, uint32_t q) const { c[i] = coef[q]; }
+    __device__ __forceinline__ void same() const { c[1] = c[2] = c[3] = c[0]; }
+};
 template <int G>
 __device__ __forceinline__ void pref_grad(const Pref& p, uint32_t span, int* map) {
     const Place<G> w(span, p.sq.tokens);
@@ -402,7 +429,7 @@ __device__ __forceinline__ void pref_grad(const Pref& p, uint32_t span, int* map
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         float c[4];
-        by_token(s, g, c, [&](uint32_t q) { return p.coef[q]; });
+        by_token(s, g, Coefs{p.coef, c});
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[i] = (live >> (4 * g + i)) & 1u ? c[i] : 0.0f;
         store4(p.grad, w.at(g), w.p1, c);
@@ -482,8 +509,20 @@ struct Weights {
     __device__ __forceinline__ double token_weight(int count) const {
         return 1.0 / (p.norm > 0.0 ? p.norm : fmax((double)count, 1.0));
     }
-    __device__ __forceinline__ double weight_of(uint32_t q) const {
-        return live.all() ? seq_weight((double)(sq.end(q) - sq.begin(q))) : weight[q];
+};
+
+// What tokens take from their sequence: its advantage, its weight.
+struct SeqTerms {
+    const Weights& c;
+    float* adv;
+    double* wt;
+    __device__ __forceinline__ void operator()(int i, uint32_t q) const {
+        if (!c.p.token_adv) adv[i] = c.p.adv[q];
+        if (c.by_seq()) wt[i] = c.weight[q];
+    }
+    __device__ __forceinline__ void same() const {
+        if (!c.p.token_adv) adv[1] = adv[2] = adv[3] = adv[0];
+        if (c.by_seq()) wt[1] = wt[2] = wt[3] = wt[0];
     }
 };
 
@@ -496,7 +535,7 @@ __device__ __forceinline__ void count_by_seq(const Weights& c, uint32_t span, in
     sum_span<G, false>(w, span, s, nullptr, live, c.sums);
 }
 __device__ __forceinline__ void weigh_seq(const Weights& c, uint32_t q, uint32_t size) {
-    const double n = c.sums.get(c.sq, q, size).count;
+    const double n = c.live.all() ? (double)(c.sq.end(q) - c.sq.begin(q)) : c.sums.get(c.sq, q, size).count;
     if ((threadIdx.x & 63) == 0) c.weight[q] = c.seq_weight(n);
 }
 
@@ -516,14 +555,16 @@ template <int NT>
 __device__ __forceinline__ double small_weights(const Weights& c, uint32_t spans, int* map) {
     __shared__ int red[NT / 64];
     const Wave w;
-    if (c.live.all()) return shared_weight<NT>(c);
     if (c.by_seq()) {
-        for (uint32_t s = w.id; s < spans; s += w.count) count_by_seq<1>(c, s, map);
-        __syncthreads();
+        if (!c.live.all()) {
+            for (uint32_t s = w.id; s < spans; s += w.count) count_by_seq<1>(c, s, map);
+            __syncthreads();
+        }
         for (uint32_t q = w.id; q < c.sq.n; q += w.count) weigh_seq(c, q, 256);
         __syncthreads();
         return 0.0;
     }
+    if (c.live.all()) return c.token_weight((int)c.sq.tokens);
     int n = 0;
     for (uint32_t s = w.id; s < spans; s += w.count) n += (int)__popc(c.live.bits(Place<1>(s, c.sq.tokens)));
     return c.token_weight(wg_sum<NT>(n, red));
@@ -558,48 +599,64 @@ struct PolicyCall {
 
 // The terms of a span's tokens, summed into s by lane; their gradient is written.
 template <int G>
-__device__ __forceinline__ void policy_span(const PolicyCall& f, uint32_t span, double all, PolicySums& s, int* map) {
+__device__ __forceinline__ void policy_span(const PolicyCall& f, uint32_t span, double all, const ExpSeries& ex,
+                                            PolicySums& s, int* map) {
     const Weights& c = f.c;
     const Policy& p = c.p;
     const Place<G> w(span, c.sq.tokens);
     float lp[4 * G], old[4 * G], ref[4 * G], adv[4 * G];
     const uint32_t live = c.live.bits(w);
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        load4(f.logp, w.at(g), w.p1, lp + 4 * g);
-        load4(p.old_logp, w.at(g), w.p1, old + 4 * g);
-    }
+    load_span(f.logp, w, lp);
+    load_span(p.old_logp, w, old);
     if (p.ref_logp) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) load4(p.ref_logp, w.at(g), w.p1, ref + 4 * g);
+        load_span(p.ref_logp, w, ref);
     } else {
 #pragma unroll
         for (int k = 0; k < 4 * G; ++k) ref[k] = 0.0f;
     }
-    if (p.token_adv) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) load4(p.adv, w.at(g), w.p1, adv + 4 * g);
-    }
+    if (p.token_adv) load_span(p.adv, w, adv);
     Ids<G> ids;
-    if (!p.token_adv || c.by_seq()) ids = seq_ids(c.sq, w, map);
+    const bool need_ids = !p.token_adv || c.by_seq();
+    if (need_ids) ids = seq_ids(c.sq, w, map);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         double wt[4] = {all, all, all, all};
-        if (!p.token_adv) by_token(ids, g, adv + 4 * g, [&](uint32_t q) { return p.adv[q]; });
-        if (c.by_seq()) by_token(ids, g, wt, [&](uint32_t q) { return c.weight_of(q); });
-        float o4[4];
+        if (need_ids) by_token(ids, g, SeqTerms{c, adv + 4 * g, wt});
+        float o4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint32_t on = (live >> (4 * g)) & 15u;
+        if (__any(on)) {
+            double d[4], u[4];
+            float a[4];
+            PolicyTerm o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int k = 4 * g + i;
-            o4[i] = 0.0f;
-            if ((live >> k) & 1u) {
-                const PolicyTerm o = policy_term(p, (double)lp[k], (double)old[k], (double)ref[k], (double)adv[k]);
-                s.pg += wt[i] * o.pg;
-                s.kl += wt[i] * o.kl;
-                s.over += o.over ? 1 : 0;
-                s.live += 1;
-                o4[i] = (float)(o.slope * (wt[i] * p.grad_scale));
+            for (int i = 0; i < 4; ++i) a[i] = adv[4 * g + i];
+            if (on != 15u) {
+                // a token that takes no part: d, u and a are 0 whatever it holds, and so are its terms
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = 4 * g + i;
+                    const bool in = (on >> i) & 1u;
+                    lp[k] = in ? lp[k] : 0.0f;
+                    old[k] = in ? old[k] : 0.0f;
+                    ref[k] = in ? ref[k] : 0.0f;
+                    a[i] = in ? a[i] : 0.0f;
+                }
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = 4 * g + i;
+                d[i] = (double)lp[k] - (double)old[k];
+                u[i] = p.ref_logp ? (double)ref[k] - (double)lp[k] : 0.0;
+            }
+            policy_terms(p, ex, d, u, a, o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s.pg += wt[i] * o[i].pg;
+                s.kl += wt[i] * o[i].kl;
+                s.over += o[i].over ? 1 : 0;
+                o4[i] = (float)(o[i].slope * (wt[i] * p.grad_scale));
+            }
+            s.live += (int)__popc(on);
         }
         if (f.grad) store4(f.grad, w.at(g), w.p1, o4);
     }
@@ -629,12 +686,13 @@ __device__ __forceinline__ void policy_out(double kl_coef, const PolicySums& s, 
     counts[1] = s.over;
 }
 
-__global__ __launch_bounds__(kLossNT) void k_policy_tokens(PolicyCall f, uint32_t spans) {
+__global__ __launch_bounds__(kLossNT, kTermWaves) void k_policy_tokens(PolicyCall f, uint32_t spans) {
     __shared__ Maps<kLossNT, kTermG> maps;
     const double all = shared_weight<kLossNT>(f.c);
     const Wave w;
+    const ExpSeries ex;
     PolicySums s{};
-    for (uint32_t k = w.id; k < spans; k += w.count) policy_span<kTermG>(f, k, all, s, maps.mine());
+    for (uint32_t k = w.id; k < spans; k += w.count) policy_span<kTermG>(f, k, all, ex, s, maps.mine());
     s = wg_policy<kLossNT>(s);
     if (threadIdx.x == 0) f.part[blockIdx.x] = s;
 }
@@ -656,8 +714,9 @@ __global__ __launch_bounds__(kOneNT) void k_policy_one(PolicyCall f, uint32_t sp
     __shared__ Maps<kOneNT, 1> maps;
     const double all = small_weights<kOneNT>(f.c, spans, maps.mine());
     const Wave w;
+    const ExpSeries ex;
     PolicySums s{};
-    for (uint32_t k = w.id; k < spans; k += w.count) policy_span<1>(f, k, all, s, maps.mine());
+    for (uint32_t k = w.id; k < spans; k += w.count) policy_span<1>(f, k, all, ex, s, maps.mine());
     s = wg_policy<kOneNT>(s);
     if (threadIdx.x == 0) policy_out(f.c.p.kl_coef, s, f.loss, f.counts);
 }
@@ -668,14 +727,14 @@ __device__ __forceinline__ void row_span(const Weights& c, uint32_t span, double
     const Place<G> w(span, c.sq.tokens);
     const uint32_t live = c.live.bits(w);
     Ids<G> ids;
-    if (!c.p.token_adv || c.by_seq()) ids = seq_ids(c.sq, w, map);
+    const bool need_ids = !c.p.token_adv || c.by_seq();
+    if (need_ids) ids = seq_ids(c.sq, w, map);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         float adv[4];
         double wt[4] = {all, all, all, all};
         if (c.p.token_adv) load4(c.p.adv, w.at(g), w.p1, adv);
-        else by_token(ids, g, adv, [&](uint32_t q) { return c.p.adv[q]; });
-        if (c.by_seq()) by_token(ids, g, wt, [&](uint32_t q) { return c.weight_of(q); });
+        if (need_ids) by_token(ids, g, SeqTerms{c, adv, wt});
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (w.at(g) + i < w.p1)
@@ -714,16 +773,15 @@ Weights make_weights(const Policy& p, const Live& live, const Seqs& sq, const We
 }
 bool small_call(const Seqs& sq) { return sq.tokens <= kOneMax && sq.n <= kOneMax; }
 
-// What the weights of a larger call take: tokens counted, by sequence or by
-// workgroup.  Nothing where every token takes part.
+// What the weights of a larger call take: tokens counted (if not all take
+// part), by sequence or by workgroup, and each sequence's weight.
 void start_weights(Weights& c, hipStream_t st) {
-    if (c.live.all()) return;
     const uint32_t spans = spans_of(c.sq.tokens, kSpanG);
     const dim3 nt(kLossNT);
     if (c.p.seq_mean) {
-        hipLaunchKernelGGL(k_count_by_seq, wave_grid(spans), nt, 0, st, c, spans);
+        if (!c.live.all()) hipLaunchKernelGGL(k_count_by_seq, wave_grid(spans), nt, 0, st, c, spans);
         hipLaunchKernelGGL(k_weigh_seqs, wave_grid(c.sq.n), nt, 0, st, c);
-    } else {
+    } else if (!c.live.all()) {
         const dim3 grid = wave_grid(spans, kCountGrid);
         c.parts = grid.x;
         hipLaunchKernelGGL(k_count, grid, nt, 0, st, c, spans);

@@ -112,59 +112,100 @@ struct Policy {
     double grad_scale;
 };
 // exp(x), exp(x) - 1 and exp(x) - 1 - x in f64.  Cody and Waite's reduction
-// x = k ln 2 + r with |r| <= ln(2)/2, then Taylor's series of exp(r) - 1 - r to
-// r^11 (the rest is below 6e-15 of 1): where k = 0 the small differences come
-// from the series alone and keep their relative accuracy.  A third of the
-// instructions of the library's exp and expm1, whose last bits an f32 output
-// does not show (the policy loss of 8e6 tokens is bound by them).
+// x = k ln 2 + r with |r| <= ln(2)/2, then Taylor's series q of exp(r) - 1 - r
+// to r^11 (the rest is below 6e-15 of 1).  With s = 2^k the small differences
+// are s q + (s r + (s - 1) - x): for k = 0 that is q, with its relative
+// accuracy.  A third of the instructions of the library's exp and expm1, whose
+// last bits an f32 output does not show.  The coefficients are held in scalar
+// registers: as literals each would be copied to a vector register before its
+// multiply-add, twice the instructions.
 struct ExpTerms {
     double e, m1, m2;  // exp(x), exp(x) - 1, exp(x) - 1 - x
 };
-__device__ __forceinline__ ExpTerms exp_terms(double x) {
-    constexpr double kRound = 0x1.8p52;  // adding it rounds to a whole number, held in the low bits
-    const double c = x > 800.0 ? 800.0 : x < -800.0 ? -800.0 : x;  // NaN stays
-    const double t = fma(c, 1.4426950408889634, kRound);
-    const double kd = t - kRound;
-    const int k = (int)(uint32_t)__double_as_longlong(t);
-    double r = fma(kd, -0x1.62e42fefa39efp-1, c);  // ln 2 in f64, and the rest of it
-    r = fma(kd, -0x1.abc9e3b39803fp-56, r);
-    double q = 1.0 / 39916800.0;
-    q = fma(q, r, 1.0 / 3628800.0);
-    q = fma(q, r, 1.0 / 362880.0);
-    q = fma(q, r, 1.0 / 40320.0);
-    q = fma(q, r, 1.0 / 5040.0);
-    q = fma(q, r, 1.0 / 720.0);
-    q = fma(q, r, 1.0 / 120.0);
-    q = fma(q, r, 1.0 / 24.0);
-    q = fma(q, r, 1.0 / 6.0);
-    q = fma(q, r, 0.5);
-    q *= r * r;
-    ExpTerms o;
-    o.e = ldexp(1.0 + (r + q), k);
-    const bool near0 = kd == 0.0;
-    o.m1 = near0 ? r + q : o.e - 1.0;
-    o.m2 = near0 ? q : o.m1 - x;
-    return o;
-}
+struct ExpSeries {
+    double c[9], log2e, ln2, ln2_rest;
+    static constexpr double kFar = 700.0;  // s is a normal number up to here
+    __device__ __forceinline__ ExpSeries() {
+        double f = 6.0;
+#pragma unroll
+        for (int i = 0; i < 9; ++i) {
+            c[i] = 1.0 / f;  // 1/3!, ..., 1/11!
+            f *= i + 4.0;
+            asm("" : "+s"(c[i]));
+        }
+        log2e = 1.4426950408889634;
+        ln2 = -0x1.62e42fefa39efp-1;  // ln 2 in f64, and the rest of it
+        ln2_rest = -0x1.abc9e3b39803fp-56;
+        asm("" : "+s"(log2e), "+s"(ln2), "+s"(ln2_rest));
+    }
+    // for |x| <= kFar (NaN stays NaN); else far() makes it right
+    __device__ __forceinline__ ExpTerms operator()(double x) const {
+        constexpr double kRound = 0x1.8p52;  // adding it rounds to a whole number, held in the low bits
+        const double t = fma(x, log2e, kRound);
+        const double kd = t - kRound;
+        const uint32_t k = (uint32_t)__double_as_longlong(t);
+        double r = fma(kd, ln2, x);
+        r = fma(kd, ln2_rest, r);
+        double q = fma(c[8], r, c[7]);
+#pragma unroll
+        for (int i = 6; i >= 0; --i) q = fma(q, r, c[i]);
+        q = fma(q, r, 0.5) * (r * r);
+        const double s = __hiloint2double((int)((k + 1023u) << 20), 0);
+        ExpTerms o;
+        o.e = fma(s, r + q, s);
+        o.m2 = fma(s, q, fma(s, r, s - 1.0) - x);
+        o.m1 = o.m2 + x;
+        return o;
+    }
+    // Beyond kFar: infinity or 0, which is what f32 outputs make of it.
+    __device__ __forceinline__ static void far(double x, ExpTerms& o) {
+        if (fabs(x) > kFar) {
+            o.e = x > 0.0 ? INFINITY : 0.0;
+            o.m1 = o.e - 1.0;
+            o.m2 = o.m1 - x;
+        }
+    }
+};
 
 struct PolicyTerm {
     double pg, kl, slope;  // slope: derivative of pg + kl_coef kl in logp
     bool over;             // held by the clip
 };
-__device__ __forceinline__ PolicyTerm policy_term(const Policy& p, double lp, double old, double ref, double a) {
-    const double d = lp - old;
-    PolicyTerm o;
-    o.over = a > 0.0 ? d > p.up : a < 0.0 ? d < p.low : false;
-    const double ra = exp_terms(d).e * a;
-    o.pg = o.over ? -(a > 0.0 ? p.edge_hi : p.edge_lo) * a : -ra;
-    o.slope = o.over ? 0.0 : -ra;
-    o.kl = 0.0;
-    if (p.ref_logp) {
-        const ExpTerms u = exp_terms(ref - lp);
-        o.kl = u.m2;
-        o.slope -= p.kl_coef * u.m1;
+// The terms of N tokens, d = logp - old, u = ref_logp - logp (0 without a
+// reference), a the advantage; no branches but for what is far off, so that the
+// tokens' chains overlap.
+template <int N>
+__device__ __forceinline__ void policy_terms(const Policy& p, const ExpSeries& ex, const double (&d)[N],
+                                             const double (&u)[N], const float (&a)[N], PolicyTerm (&o)[N]) {
+    ExpTerms r[N], k[N];
+    bool far = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        r[i] = ex(d[i]);
+        far |= fmax(fabs(d[i]), fabs(u[i])) > ExpSeries::kFar;
     }
-    return o;
+    if (p.ref_logp) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) k[i] = ex(u[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) k[i] = ExpTerms{1.0, 0.0, 0.0};
+    }
+    if (far) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            ExpSeries::far(d[i], r[i]);
+            ExpSeries::far(u[i], k[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        o[i].over = (a[i] > 0.0f && d[i] > p.up) || (a[i] < 0.0f && d[i] < p.low);
+        const double f = o[i].over ? (a[i] > 0.0f ? p.edge_hi : p.edge_lo) : r[i].e;
+        o[i].pg = -f * (double)a[i];
+        o[i].slope = fma(-p.kl_coef, k[i].m1, o[i].over ? 0.0 : o[i].pg);
+        o[i].kl = k[i].m2;
+    }
 }
 
 // Sums over tokens: w pg, w kl; tokens that take part, tokens held by the clip.
