@@ -432,7 +432,8 @@ __global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t 
             const double d[1] = {v.logp - (double)old}, u[1] = {p.ref_logp ? (double)ref - v.logp : 0.0};
             const float adv[1] = {t.adv};
             PolicyTerm o1[1];
-            policy_terms(p, ExpSeries(), d, u, adv, o1);
+            if (p.ref_logp) policy_terms<true>(p, ExpSeries(), d, u, adv, o1);
+            else policy_terms<false>(p, ExpSeries(), d, u, adv, o1);
             const PolicyTerm& k1 = o1[0];
             logp[r] = (float)v.logp;
             total.pg += t.w * k1.pg;

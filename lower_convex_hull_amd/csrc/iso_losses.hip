@@ -5,12 +5,15 @@
 #include "../../include/iso.h"
 #include "iso_losses.hpp"
 
+#include <type_traits>
+
 namespace iso {
 namespace {
 
 constexpr int kLossNT = 256;        // threads of a workgroup over many tokens: four waves, a span each
 constexpr int kSpanG = 2;           // a wave's span: 2 groups of 256 tokens, 4 a lane in each
 constexpr int kTermG = 2;           // the same where the policy's terms are computed, which take more registers
+constexpr int64_t kTermGrid = 1024;  // workgroups that take them: four a CU
 constexpr int kTermWaves = 4;       // waves a SIMD holds of them
 constexpr int kOneNT = 1024;        // the one workgroup of a small call, whose spans are one group
 constexpr int64_t kOneMax = 4096;  // tokens (and sequences) up to which one workgroup takes the whole call
@@ -512,17 +515,18 @@ struct Weights {
 };
 
 // What tokens take from their sequence: its advantage, its weight.
+template <bool ADV, bool WEIGHT>
 struct SeqTerms {
     const Weights& c;
     float* adv;
     double* wt;
     __device__ __forceinline__ void operator()(int i, uint32_t q) const {
-        if (!c.p.token_adv) adv[i] = c.p.adv[q];
-        if (c.by_seq()) wt[i] = c.weight[q];
+        if (ADV) adv[i] = c.p.adv[q];
+        if (WEIGHT) wt[i] = c.weight[q];
     }
     __device__ __forceinline__ void same() const {
-        if (!c.p.token_adv) adv[1] = adv[2] = adv[3] = adv[0];
-        if (c.by_seq()) wt[1] = wt[2] = wt[3] = wt[0];
+        if (ADV) adv[1] = adv[2] = adv[3] = adv[0];
+        if (WEIGHT) wt[1] = wt[2] = wt[3] = wt[0];
     }
 };
 
@@ -597,8 +601,29 @@ struct PolicyCall {
     PolicySums* part;  // a workgroup's sums
 };
 
+// What a policy call has: advantages by token, weights by sequence, a
+// reference.  The kernels over tokens are made for each combination: asked at
+// run time, the questions are half of the instructions (67 -> ... us at 8e6 tokens).
+template <bool TOKEN_ADV, bool BY_SEQ, bool REF>
+struct Kind {
+    static constexpr bool token_adv = TOKEN_ADV, by_seq = BY_SEQ, ref = REF;
+};
+template <typename F>
+void by_kind(const Policy& p, F f) {
+    auto third = [&](auto t, auto s) {
+        if (p.ref_logp) f(Kind<decltype(t)::value, decltype(s)::value, true>{});
+        else f(Kind<decltype(t)::value, decltype(s)::value, false>{});
+    };
+    auto second = [&](auto t) {
+        if (p.seq_mean) third(t, std::true_type{});
+        else third(t, std::false_type{});
+    };
+    if (p.token_adv) second(std::true_type{});
+    else second(std::false_type{});
+}
+
 // The terms of a span's tokens, summed into s by lane; their gradient is written.
-template <int G>
+template <typename K, int G>
 __device__ __forceinline__ void policy_span(const PolicyCall& f, uint32_t span, double all, const ExpSeries& ex,
                                             PolicySums& s, int* map) {
     const Weights& c = f.c;
@@ -608,20 +633,15 @@ __device__ __forceinline__ void policy_span(const PolicyCall& f, uint32_t span, 
     const uint32_t live = c.live.bits(w);
     load_span(f.logp, w, lp);
     load_span(p.old_logp, w, old);
-    if (p.ref_logp) {
-        load_span(p.ref_logp, w, ref);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4 * G; ++k) ref[k] = 0.0f;
-    }
-    if (p.token_adv) load_span(p.adv, w, adv);
+    if (K::ref) load_span(p.ref_logp, w, ref);
+    if (K::token_adv) load_span(p.adv, w, adv);
     Ids<G> ids;
-    const bool need_ids = !p.token_adv || c.by_seq();
+    constexpr bool need_ids = !K::token_adv || K::by_seq;
     if (need_ids) ids = seq_ids(c.sq, w, map);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         double wt[4] = {all, all, all, all};
-        if (need_ids) by_token(ids, g, SeqTerms{c, adv + 4 * g, wt});
+        if (need_ids) by_token(ids, g, SeqTerms<!K::token_adv, K::by_seq>{c, adv + 4 * g, wt});
         float o4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         const uint32_t on = (live >> (4 * g)) & 15u;
         if (__any(on)) {
@@ -638,7 +658,7 @@ __device__ __forceinline__ void policy_span(const PolicyCall& f, uint32_t span, 
                     const bool in = (on >> i) & 1u;
                     lp[k] = in ? lp[k] : 0.0f;
                     old[k] = in ? old[k] : 0.0f;
-                    ref[k] = in ? ref[k] : 0.0f;
+                    if (K::ref) ref[k] = in ? ref[k] : 0.0f;
                     a[i] = in ? a[i] : 0.0f;
                 }
             }
@@ -646,9 +666,9 @@ __device__ __forceinline__ void policy_span(const PolicyCall& f, uint32_t span, 
             for (int i = 0; i < 4; ++i) {
                 const int k = 4 * g + i;
                 d[i] = (double)lp[k] - (double)old[k];
-                u[i] = p.ref_logp ? (double)ref[k] - (double)lp[k] : 0.0;
+                u[i] = K::ref ? (double)ref[k] - (double)lp[k] : 0.0;
             }
-            policy_terms(p, ex, d, u, a, o);
+            policy_terms<K::ref>(p, ex, d, u, a, o);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 s.pg += wt[i] * o[i].pg;
@@ -686,13 +706,14 @@ __device__ __forceinline__ void policy_out(double kl_coef, const PolicySums& s, 
     counts[1] = s.over;
 }
 
+template <typename K>
 __global__ __launch_bounds__(kLossNT, kTermWaves) void k_policy_tokens(PolicyCall f, uint32_t spans) {
     __shared__ Maps<kLossNT, kTermG> maps;
     const double all = shared_weight<kLossNT>(f.c);
     const Wave w;
     const ExpSeries ex;
     PolicySums s{};
-    for (uint32_t k = w.id; k < spans; k += w.count) policy_span<kTermG>(f, k, all, ex, s, maps.mine());
+    for (uint32_t k = w.id; k < spans; k += w.count) policy_span<K, kTermG>(f, k, all, ex, s, maps.mine());
     s = wg_policy<kLossNT>(s);
     if (threadIdx.x == 0) f.part[blockIdx.x] = s;
 }
@@ -710,13 +731,14 @@ __global__ __launch_bounds__(kOneNT) void k_policy_out(double kl_coef, const Pol
     if (threadIdx.x == 0) policy_out(kl_coef, s, loss, counts);
 }
 // A small call whole.
+template <typename K>
 __global__ __launch_bounds__(kOneNT) void k_policy_one(PolicyCall f, uint32_t spans) {
     __shared__ Maps<kOneNT, 1> maps;
     const double all = small_weights<kOneNT>(f.c, spans, maps.mine());
     const Wave w;
     const ExpSeries ex;
     PolicySums s{};
-    for (uint32_t k = w.id; k < spans; k += w.count) policy_span<1>(f, k, all, ex, s, maps.mine());
+    for (uint32_t k = w.id; k < spans; k += w.count) policy_span<K, 1>(f, k, all, ex, s, maps.mine());
     s = wg_policy<kOneNT>(s);
     if (threadIdx.x == 0) policy_out(f.c.p.kl_coef, s, f.loss, f.counts);
 }
@@ -734,7 +756,10 @@ __device__ __forceinline__ void row_span(const Weights& c, uint32_t span, double
         float adv[4];
         double wt[4] = {all, all, all, all};
         if (c.p.token_adv) load4(c.p.adv, w.at(g), w.p1, adv);
-        if (need_ids) by_token(ids, g, SeqTerms{c, adv, wt});
+        if (need_ids) {
+            if (!c.p.token_adv) by_token(ids, g, SeqTerms<true, false>{c, adv, wt});
+            if (c.by_seq()) by_token(ids, g, SeqTerms<false, true>{c, adv, wt});
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (w.at(g) + i < w.p1)
@@ -792,7 +817,7 @@ struct PolicyPlan {
     WeightsPlan w;
     size_t off_part, bytes;
     PolicyPlan(int64_t tokens, int64_t seqs) : w(tokens, seqs) {
-        off_part = w.t.take((int64_t)wave_grid(spans_of(tokens, kTermG)).x, sizeof(PolicySums));
+        off_part = w.t.take((int64_t)wave_grid(spans_of(tokens, kTermG), kTermGrid).x, sizeof(PolicySums));
         bytes = w.t.at;
     }
 };
@@ -951,13 +976,17 @@ int iso_policy_loss(const float* logp, const float* old_logp, const float* ref_l
     PolicyCall f{make_weights(p, Live{mask, nullptr}, make_seqs(seq_off, seqs, tokens), pl.w, ws), logp, loss, counts,
                  grad, reinterpret_cast<PolicySums*>(ws + pl.off_part)};
     if (small_call(f.c.sq)) {
-        hipLaunchKernelGGL(k_policy_one, dim3(1), dim3(kOneNT), 0, st, f, spans_of(tokens, 1));
+        by_kind(p, [&](auto k) {
+            hipLaunchKernelGGL((k_policy_one<decltype(k)>), dim3(1), dim3(kOneNT), 0, st, f, spans_of(tokens, 1));
+        });
         return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
     }
     start_weights(f.c, st);
     const uint32_t spans = spans_of(tokens, kTermG);
-    const dim3 grid = wave_grid(spans);
-    hipLaunchKernelGGL(k_policy_tokens, grid, dim3(kLossNT), 0, st, f, spans);
+    const dim3 grid = wave_grid(spans, kTermGrid);
+    by_kind(p, [&](auto k) {
+        hipLaunchKernelGGL((k_policy_tokens<decltype(k)>), grid, dim3(kLossNT), 0, st, f, spans);
+    });
     return launch_policy_out(p, f.part, (int)grid.x, loss, counts, st) == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 

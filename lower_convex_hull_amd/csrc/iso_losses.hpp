@@ -174,7 +174,7 @@ struct PolicyTerm {
 // The terms of N tokens, d = logp - old, u = ref_logp - logp (0 without a
 // reference), a the advantage; no branches but for what is far off, so that the
 // tokens' chains overlap.
-template <int N>
+template <bool REF, int N>
 __device__ __forceinline__ void policy_terms(const Policy& p, const ExpSeries& ex, const double (&d)[N],
                                              const double (&u)[N], const float (&a)[N], PolicyTerm (&o)[N]) {
     ExpTerms r[N], k[N];
@@ -182,20 +182,14 @@ __device__ __forceinline__ void policy_terms(const Policy& p, const ExpSeries& e
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         r[i] = ex(d[i]);
-        far |= fmax(fabs(d[i]), fabs(u[i])) > ExpSeries::kFar;
-    }
-    if (p.ref_logp) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) k[i] = ex(u[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) k[i] = ExpTerms{1.0, 0.0, 0.0};
+        k[i] = REF ? ex(u[i]) : ExpTerms{1.0, 0.0, 0.0};
+        far |= (REF ? fmax(fabs(d[i]), fabs(u[i])) : fabs(d[i])) > ExpSeries::kFar;
     }
     if (far) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             ExpSeries::far(d[i], r[i]);
-            ExpSeries::far(u[i], k[i]);
+            if (REF) ExpSeries::far(u[i], k[i]);
         }
     }
 #pragma unroll
@@ -203,7 +197,8 @@ __device__ __forceinline__ void policy_terms(const Policy& p, const ExpSeries& e
         o[i].over = (a[i] > 0.0f && d[i] > p.up) || (a[i] < 0.0f && d[i] < p.low);
         const double f = o[i].over ? (a[i] > 0.0f ? p.edge_hi : p.edge_lo) : r[i].e;
         o[i].pg = -f * (double)a[i];
-        o[i].slope = fma(-p.kl_coef, k[i].m1, o[i].over ? 0.0 : o[i].pg);
+        o[i].slope = o[i].over ? 0.0 : o[i].pg;
+        if (REF) o[i].slope = fma(-p.kl_coef, k[i].m1, o[i].slope);
         o[i].kl = k[i].m2;
     }
 }
