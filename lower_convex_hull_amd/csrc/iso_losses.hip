@@ -13,7 +13,7 @@ namespace {
 constexpr int kLossNT = 256;        // threads of a workgroup over many tokens: four waves, a span each
 constexpr int kSpanG = 2;           // a wave's span: 2 groups of 256 tokens, 4 a lane in each
 constexpr int kTermG = 2;           // the same where the policy's terms are computed, which take more registers
-constexpr int64_t kTermGrid = 1024;  // workgroups that take them: four a CU
+constexpr int64_t kGrid = 1024;     // workgroups over spans: four a CU
 constexpr int kTermWaves = 4;       // waves a SIMD holds of them
 constexpr int kOneNT = 1024;        // the one workgroup of a small call, whose spans are one group
 constexpr int64_t kOneMax = 4096;  // tokens (and sequences) up to which one workgroup takes the whole call
@@ -149,27 +149,46 @@ struct MaxStep {
     template <int CTRL, int RM>
     __device__ __forceinline__ void step() { v = max(v, dpp<CTRL, RM>(0, v)); }
 };
+// A wave takes spans that follow each other, and looks for a span's first
+// sequence from the last one of the span before: 64 sequences in one load,
+// which mostly holds all that begin inside the span too.
+struct Cursor {
+    uint32_t q = 0xffffffffu;  // one that begins at or before the next span, or none known
+};
 // Each sequence that begins inside the span marks its first token in `map`
 // (G * 256 words of the wave's own in LDS; the last one where some are empty);
 // a running maximum then tells every token's.  The cost does not depend on how
 // many sequences there are, and offsets that are not non-decreasing give some
-// ids below n - q0.
+// sequences below n.
 template <int G>
-__device__ __forceinline__ Ids<G> seq_ids(const Seqs& sq, const Place<G>& w, int* map) {
+__device__ __forceinline__ Ids<G> seq_ids(const Seqs& sq, const Place<G>& w, int* map, Cursor& cur) {
+    auto begin_of = [&](uint32_t k) { return k < sq.n ? sq.begin(k) : 0xffffffffu; };
+    if (!sq.off) cur.q = w.p0 / sq.len;
+    else if (cur.q == 0xffffffffu) cur.q = sq.n <= 64 ? 0u : find_seq(sq, w.p0);
+    uint32_t k = cur.q + 1 + w.lane, b = begin_of(k);
+    uint32_t passed = (uint32_t)__popcll(__ballot(b <= w.p0));
+    if (passed == 64) {
+        cur.q = find_seq(sq, w.p0);
+        k = cur.q + 1 + w.lane;
+        b = begin_of(k);
+        passed = (uint32_t)__popcll(__ballot(b <= w.p0));
+    }
     Ids<G> s;
-    s.q0 = w.p0 < w.p1 ? (uint32_t)__builtin_amdgcn_readfirstlane((int)find_seq(sq, w.p0)) : 0u;
+    s.q0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(cur.q + passed));
+    cur.q = s.q0;
 #pragma unroll
-    for (int k = 0; k < 4 * G; ++k) s.id[k] = 0;
-    s.one = w.p0 >= w.p1 || s.q0 + 1 >= sq.n || sq.begin(s.q0 + 1) >= w.p1;
+    for (int i = 0; i < 4 * G; ++i) s.id[i] = 0;
+    s.one = !__any(b > w.p0 && b < w.p1);
     if (s.one) return s;
     int4* m = reinterpret_cast<int4*>(map);
 #pragma unroll
     for (int g = 0; g < G; ++g) m[g * 64 + w.lane] = make_int4(0, 0, 0, 0);
     wave_order();
-    for (uint32_t k = s.q0 + 1 + w.lane;; k += 64) {
-        const uint32_t b = k < sq.n ? sq.begin(k) : 0xffffffffu;
+    for (;;) {
         if (b > w.p0 && b < w.p1) atomicMax(map + (b - w.p0), (int)(k - s.q0));
         if (!__all(b < w.p1)) break;
+        k += 64;
+        b = begin_of(k);
     }
     wave_order();
     int before = 0;
@@ -188,6 +207,7 @@ __device__ __forceinline__ Ids<G> seq_ids(const Seqs& sq, const Place<G>& w, int
         for (int i = 0; i < 4; ++i) id[i] = max(id[i], low);
         before = max(before, lane_value(x.v, 63));
     }
+    cur.q = s.q0 + (uint32_t)before;
     return s;
 }
 
@@ -308,18 +328,25 @@ __device__ __forceinline__ void by_token(const Ids<G>& s, int g, F f) {
 uint32_t spans_of(int64_t tokens, int g) { return (uint32_t)((tokens + 256 * g - 1) / (256 * g)); }
 
 // Workgroups for `waves` waves' work, at most `most` (each then takes more).
-dim3 wave_grid(int64_t waves, int64_t most = 65536) {
+dim3 wave_grid(int64_t waves, int64_t most = kGrid) {
     const int64_t g = (waves + kLossNT / 64 - 1) / (kLossNT / 64);
     return dim3((unsigned)(g < 1 ? 1 : g > most ? most : g));
 }
 
-// A wave's number among all of a launch, and their number.
+// A wave's number among all of a launch, and their number; its share of n
+// items, which follow each other.
 struct Wave {
     uint32_t id, count;
-    __device__ __forceinline__ Wave() {
+    __device__ __forceinline__ explicit Wave(uint32_t first_block = 0) {
         const uint32_t nw = blockDim.x >> 6;
-        id = blockIdx.x * nw + (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-        count = gridDim.x * nw;
+        id = (blockIdx.x - first_block) * nw + (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+        count = (gridDim.x - first_block) * nw;
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(uint32_t n, F f) const {
+        const uint32_t part = (n + count - 1) / count;
+        const uint32_t e = min((id + 1) * part, n);
+        for (uint32_t i = id * part; i < e; ++i) f(i);
     }
 };
 
@@ -374,7 +401,7 @@ struct Pref {
 __device__ __forceinline__ double softplus_neg(double h) { return fmax(-h, 0.0) + log1p(exp(-fabs(h))); }
 
 template <int G>
-__device__ __forceinline__ void pref_sums(const Pref& p, uint32_t span, int* map) {
+__device__ __forceinline__ void pref_sums(const Pref& p, uint32_t span, int* map, Cursor& cur) {
     const Place<G> w(span, p.sq.tokens);
     float x[4 * G], y[4 * G];
     double v[4 * G];
@@ -386,7 +413,7 @@ __device__ __forceinline__ void pref_sums(const Pref& p, uint32_t span, int* map
 #pragma unroll
         for (int k = 0; k < 4 * G; ++k) y[k] = 0.0f;
     }
-    const Ids<G> s = seq_ids(p.sq, w, map);
+    const Ids<G> s = seq_ids(p.sq, w, map, cur);
 #pragma unroll
     for (int k = 0; k < 4 * G; ++k) v[k] = (live >> k) & 1u ? (double)x[k] - (double)y[k] : 0.0;
     sum_span<G, true>(w, span, s, v, live, p.sums);
@@ -425,10 +452,10 @@ struct Coefs {
     __device__ __forceinline__ void same() const { c[1] = c[2] = c[3] = c[0]; }
 };
 template <int G>
-__device__ __forceinline__ void pref_grad(const Pref& p, uint32_t span, int* map) {
+__device__ __forceinline__ void pref_grad(const Pref& p, uint32_t span, int* map, Cursor& cur) {
     const Place<G> w(span, p.sq.tokens);
     const uint32_t live = p.live.bits(w);
-    const Ids<G> s = seq_ids(p.sq, w, map);
+    const Ids<G> s = seq_ids(p.sq, w, map, cur);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         float c[4];
@@ -451,7 +478,8 @@ __device__ __forceinline__ void pref_mean(const Pref& p) {
 __global__ __launch_bounds__(kLossNT) void k_pref_sums(Pref p, uint32_t spans) {
     __shared__ Maps<kLossNT, kSpanG> maps;
     const Wave w;
-    for (uint32_t s = w.id; s < spans; s += w.count) pref_sums<kSpanG>(p, s, maps.mine());
+    Cursor cur;
+    w.each(spans, [&](uint32_t s) { pref_sums<kSpanG>(p, s, maps.mine(), cur); });
 }
 __global__ __launch_bounds__(kLossNT) void k_pref_pairs(Pref p) {
     const Wave w;
@@ -464,20 +492,20 @@ __global__ __launch_bounds__(kLossNT) void k_pref_grad(Pref p, uint32_t spans) {
         pref_mean<kLossNT>(p);
         return;
     }
-    const Wave w;
-    const uint32_t first = kLossNT / 64;
-    for (uint32_t s = w.id - first; s < spans; s += w.count - first) pref_grad<kSpanG>(p, s, maps.mine());
+    const Wave w(1);
+    Cursor cur;
+    w.each(spans, [&](uint32_t s) { pref_grad<kSpanG>(p, s, maps.mine(), cur); });
 }
 // A small call whole: the three steps by one workgroup.
 __global__ __launch_bounds__(kOneNT) void k_pref_one(Pref p, uint32_t spans) {
     __shared__ Maps<kOneNT, 1> maps;
     const Wave w;
-    for (uint32_t s = w.id; s < spans; s += w.count) pref_sums<1>(p, s, maps.mine());
+    Cursor first, second;
+    w.each(spans, [&](uint32_t s) { pref_sums<1>(p, s, maps.mine(), first); });
     __syncthreads();
     for (uint32_t i = w.id; i < p.pairs; i += w.count) pref_pair(p, i, 256);
     __syncthreads();
-    if (p.grad)
-        for (uint32_t s = w.id; s < spans; s += w.count) pref_grad<1>(p, s, maps.mine());
+    if (p.grad) w.each(spans, [&](uint32_t s) { pref_grad<1>(p, s, maps.mine(), second); });
     pref_mean<kOneNT>(p);
 }
 
@@ -532,10 +560,10 @@ struct SeqTerms {
 
 // Tokens that take part, by sequence.
 template <int G>
-__device__ __forceinline__ void count_by_seq(const Weights& c, uint32_t span, int* map) {
+__device__ __forceinline__ void count_by_seq(const Weights& c, uint32_t span, int* map, Cursor& cur) {
     const Place<G> w(span, c.sq.tokens);
     const uint32_t live = c.live.bits(w);
-    const Ids<G> s = seq_ids(c.sq, w, map);
+    const Ids<G> s = seq_ids(c.sq, w, map, cur);
     sum_span<G, false>(w, span, s, nullptr, live, c.sums);
 }
 __device__ __forceinline__ void weigh_seq(const Weights& c, uint32_t q, uint32_t size) {
@@ -561,7 +589,8 @@ __device__ __forceinline__ double small_weights(const Weights& c, uint32_t spans
     const Wave w;
     if (c.by_seq()) {
         if (!c.live.all()) {
-            for (uint32_t s = w.id; s < spans; s += w.count) count_by_seq<1>(c, s, map);
+            Cursor cur;
+            w.each(spans, [&](uint32_t s) { count_by_seq<1>(c, s, map, cur); });
             __syncthreads();
         }
         for (uint32_t q = w.id; q < c.sq.n; q += w.count) weigh_seq(c, q, 256);
@@ -577,7 +606,8 @@ __device__ __forceinline__ double small_weights(const Weights& c, uint32_t spans
 __global__ __launch_bounds__(kLossNT) void k_count_by_seq(Weights c, uint32_t spans) {
     __shared__ Maps<kLossNT, kSpanG> maps;
     const Wave w;
-    for (uint32_t s = w.id; s < spans; s += w.count) count_by_seq<kSpanG>(c, s, maps.mine());
+    Cursor cur;
+    w.each(spans, [&](uint32_t s) { count_by_seq<kSpanG>(c, s, maps.mine(), cur); });
 }
 __global__ __launch_bounds__(kLossNT) void k_weigh_seqs(Weights c) {
     const Wave w;
@@ -625,7 +655,7 @@ void by_kind(const Policy& p, F f) {
 // The terms of a span's tokens, summed into s by lane; their gradient is written.
 template <typename K, int G>
 __device__ __forceinline__ void policy_span(const PolicyCall& f, uint32_t span, double all, const ExpSeries& ex,
-                                            PolicySums& s, int* map) {
+                                            PolicySums& s, int* map, Cursor& cur) {
     const Weights& c = f.c;
     const Policy& p = c.p;
     const Place<G> w(span, c.sq.tokens);
@@ -637,7 +667,7 @@ __device__ __forceinline__ void policy_span(const PolicyCall& f, uint32_t span, 
     if (K::token_adv) load_span(p.adv, w, adv);
     Ids<G> ids;
     constexpr bool need_ids = !K::token_adv || K::by_seq;
-    if (need_ids) ids = seq_ids(c.sq, w, map);
+    if (need_ids) ids = seq_ids(c.sq, w, map, cur);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         double wt[4] = {all, all, all, all};
@@ -713,7 +743,8 @@ __global__ __launch_bounds__(kLossNT, kTermWaves) void k_policy_tokens(PolicyCal
     const Wave w;
     const ExpSeries ex;
     PolicySums s{};
-    for (uint32_t k = w.id; k < spans; k += w.count) policy_span<K, kTermG>(f, k, all, ex, s, maps.mine());
+    Cursor cur;
+    w.each(spans, [&](uint32_t k) { policy_span<K, kTermG>(f, k, all, ex, s, maps.mine(), cur); });
     s = wg_policy<kLossNT>(s);
     if (threadIdx.x == 0) f.part[blockIdx.x] = s;
 }
@@ -738,19 +769,21 @@ __global__ __launch_bounds__(kOneNT) void k_policy_one(PolicyCall f, uint32_t sp
     const Wave w;
     const ExpSeries ex;
     PolicySums s{};
-    for (uint32_t k = w.id; k < spans; k += w.count) policy_span<K, 1>(f, k, all, ex, s, maps.mine());
+    Cursor cur;
+    w.each(spans, [&](uint32_t k) { policy_span<K, 1>(f, k, all, ex, s, maps.mine(), cur); });
     s = wg_policy<kOneNT>(s);
     if (threadIdx.x == 0) policy_out(f.c.p.kl_coef, s, f.loss, f.counts);
 }
 
 // Rows' terms of the loss from logits.
 template <int G>
-__device__ __forceinline__ void row_span(const Weights& c, uint32_t span, double all, RowTerm* terms, int* map) {
+__device__ __forceinline__ void row_span(const Weights& c, uint32_t span, double all, RowTerm* terms, int* map,
+                                         Cursor& cur) {
     const Place<G> w(span, c.sq.tokens);
     const uint32_t live = c.live.bits(w);
     Ids<G> ids;
     const bool need_ids = !c.p.token_adv || c.by_seq();
-    if (need_ids) ids = seq_ids(c.sq, w, map);
+    if (need_ids) ids = seq_ids(c.sq, w, map, cur);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         float adv[4];
@@ -770,13 +803,15 @@ __global__ __launch_bounds__(kLossNT) void k_row_terms(Weights c, uint32_t spans
     __shared__ Maps<kLossNT, kSpanG> maps;
     const double all = shared_weight<kLossNT>(c);
     const Wave w;
-    for (uint32_t k = w.id; k < spans; k += w.count) row_span<kSpanG>(c, k, all, terms, maps.mine());
+    Cursor cur;
+    w.each(spans, [&](uint32_t k) { row_span<kSpanG>(c, k, all, terms, maps.mine(), cur); });
 }
 __global__ __launch_bounds__(kOneNT) void k_row_terms_one(Weights c, uint32_t spans, RowTerm* terms) {
     __shared__ Maps<kOneNT, 1> maps;
     const double all = small_weights<kOneNT>(c, spans, maps.mine());
     const Wave w;
-    for (uint32_t k = w.id; k < spans; k += w.count) row_span<1>(c, k, all, terms, maps.mine());
+    Cursor cur;
+    w.each(spans, [&](uint32_t k) { row_span<1>(c, k, all, terms, maps.mine(), cur); });
 }
 
 constexpr int kCountGrid = 512;  // workgroups that count, their counts read by every later workgroup
@@ -805,7 +840,7 @@ void start_weights(Weights& c, hipStream_t st) {
     const dim3 nt(kLossNT);
     if (c.p.seq_mean) {
         if (!c.live.all()) hipLaunchKernelGGL(k_count_by_seq, wave_grid(spans), nt, 0, st, c, spans);
-        hipLaunchKernelGGL(k_weigh_seqs, wave_grid(c.sq.n), nt, 0, st, c);
+        hipLaunchKernelGGL(k_weigh_seqs, wave_grid(c.sq.n, 65536), nt, 0, st, c);
     } else if (!c.live.all()) {
         const dim3 grid = wave_grid(spans, kCountGrid);
         c.parts = grid.x;
@@ -817,7 +852,7 @@ struct PolicyPlan {
     WeightsPlan w;
     size_t off_part, bytes;
     PolicyPlan(int64_t tokens, int64_t seqs) : w(tokens, seqs) {
-        off_part = w.t.take((int64_t)wave_grid(spans_of(tokens, kTermG), kTermGrid).x, sizeof(PolicySums));
+        off_part = w.t.take((int64_t)wave_grid(spans_of(tokens, kTermG)).x, sizeof(PolicySums));
         bytes = w.t.at;
     }
 };
@@ -940,7 +975,7 @@ int iso_pref_loss(const float* logp, const float* ref_logp, const uint8_t* mask,
     const dim3 nt(kLossNT);
     const uint32_t spans = spans_of(tokens, kSpanG);
     hipLaunchKernelGGL(k_pref_sums, wave_grid(spans), nt, 0, st, p, spans);
-    hipLaunchKernelGGL(k_pref_pairs, wave_grid(pairs), nt, 0, st, p);
+    hipLaunchKernelGGL(k_pref_pairs, wave_grid(pairs, 65536), nt, 0, st, p);
     hipLaunchKernelGGL(k_pref_grad, dim3(grad ? wave_grid(spans).x + 1 : 1), nt, 0, st, p, spans);
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
@@ -983,7 +1018,7 @@ int iso_policy_loss(const float* logp, const float* old_logp, const float* ref_l
     }
     start_weights(f.c, st);
     const uint32_t spans = spans_of(tokens, kTermG);
-    const dim3 grid = wave_grid(spans, kTermGrid);
+    const dim3 grid = wave_grid(spans);
     by_kind(p, [&](auto k) {
         hipLaunchKernelGGL((k_policy_tokens<decltype(k)>), grid, dim3(kLossNT), 0, st, f, spans);
     });
