@@ -13,8 +13,8 @@ namespace {
 constexpr double kLog2e = 1.4426950408889634;
 constexpr double kLn2 = 0.6931471805599453;
 
-// 16 bytes of logits at element alignment: rows of an odd length or stride
-// start anywhere, and global loads and stores need no wider alignment.
+// 16 bytes of logits at element alignment: logits and their gradient can have
+// strides that no shift aligns both of, and global loads and stores need none.
 template <typename T>
 struct Wide {
     static constexpr int N = 16 / sizeof(T);
@@ -72,10 +72,29 @@ __device__ __forceinline__ Stat wave_join(Stat a, const Scale& sc) {
     return a;
 }
 
-// Positions in a row are below 2^30.  Of a piece [k0, k1) of a row, the whole
-// vectors go through chunks; up to N - 1 elements are left, one a thread.
+// Piece number s of a row, of `chunk` elements from the first 16-byte aligned
+// one on: whole vectors from..to, and the elements at the row's ends that no
+// aligned vector holds, one a thread (N - 1 at each end at most).  Rows of an
+// odd length begin anywhere; vectors that straddle cache lines cost 5 us of 90
+// at 515 x 99991 f32.  Positions in a row are below 2^30.
 template <typename T>
-__device__ __forceinline__ int body_end(int k0, int k1) { return k0 + (k1 - k0) / Wide<T>::N * Wide<T>::N; }
+struct Piece {
+    int head, from, to, k1;
+    __device__ __forceinline__ Piece(const T* aligned_to, int s, int chunk, int vocab) {
+        constexpr int N = Wide<T>::N;
+        const int skew = (int)((0u - (unsigned)(uintptr_t)aligned_to) & 15u) / (int)sizeof(T);
+        head = min(skew, vocab);
+        from = min(head + s * chunk, vocab);
+        k1 = chunk >= vocab - from ? vocab : from + chunk;
+        to = from + (k1 - from) / N * N;
+        if (s > 0) head = 0;
+    }
+    // the thread's own element, -1 if it has none
+    __device__ __forceinline__ int edge() const {
+        const int t = (int)threadIdx.x, k = to + t - head;
+        return t < head ? t : k < k1 ? k : -1;
+    }
+};
 
 // A chunk of a row: U vectors a thread of NT, those past k1 filled with
 // -infinity (they add nothing).
@@ -172,17 +191,17 @@ struct Running {
     }
 };
 
-// The statistics of x[k0, k1) by a workgroup of NT threads; thread 0 has them.
+// The statistics of a piece of a row by a workgroup of NT threads; thread 0 has them.
 template <typename T, bool ENT, int NT, int U>
-__device__ __forceinline__ Stat row_stat(const T* __restrict__ x, int k0, int k1, const Scale& sc, Stat* part) {
+__device__ __forceinline__ Stat row_stat(const T* __restrict__ x, const Piece<T>& w, const Scale& sc, Stat* part) {
     Running<T, ENT, NT, U> run;
-    const int end = body_end<T>(k0, k1);
-    for (int k = k0; k < end; k += Chunk<T, NT, U>::kSize) {
+    for (int k = w.from; k < w.to; k += Chunk<T, NT, U>::kSize) {
         Chunk<T, NT, U> c;
-        c.load(x, k, end);
+        c.load(x, k, w.to);
         run.add(c, sc);
     }
-    if ((int)threadIdx.x < k1 - end) run.add_one((float)x[end + threadIdx.x], sc);
+    const int k = w.edge();
+    if (k >= 0) run.add_one((float)x[k], sc);
     return run.join(sc, part);
 }
 
@@ -232,8 +251,7 @@ __global__ __launch_bounds__(NT) void k_token_logp(const T* __restrict__ logits,
         const T* x = logits + r * ld;
         Stat a{};
         if (j >= 0) {
-            const int k0 = (int)(item - r * splits) * chunk, k1 = min(k0 + chunk, vocab);
-            a = row_stat<T, ENT, NT, 4>(x, k0, k1, sc, part);
+            a = row_stat<T, ENT, NT, 4>(x, Piece<T>(x, (int)(item - r * splits), chunk, vocab), sc, part);
         }
         if (threadIdx.x == 0) {
             if (splits == 1) write_row(o, r, x, j, vocab, sc.inv_t, a);
@@ -333,23 +351,22 @@ __device__ __forceinline__ void store_grads(const Chunk<T, NT, U>& c, T* o, int 
                 store_wide<T>(b + u * NT * C::N + threadIdx.x * C::N, grad_wide<T, ENT>(c.v[u], C::at(k, u), j, q, cf));
     }
 }
-// That of the elements that whole vectors leave over, one a thread.
+// That of the thread's own element at the row's ends.
 template <typename T, bool ENT>
-__device__ __forceinline__ void store_rest(const T* x, T* o, int end, int k1, int j, const RowGrad& q, float cf) {
-    const int k = end + (int)threadIdx.x;
-    if (k < k1) o[k] = (T)(grad_one<ENT>((float)x[k], q, cf) + (j == k ? q.hot : 0.0f));
+__device__ __forceinline__ void store_edge(const T* x, T* o, int k, int j, const RowGrad& q, float cf) {
+    if (k >= 0) o[k] = (T)(grad_one<ENT>((float)x[k], q, cf) + (j == k ? q.hot : 0.0f));
 }
 
 // A row's gradient where it is one value: 0 (ignored) or NaN.
 template <typename T, int NT>
-__device__ __forceinline__ void fill_row(T* o, int k0, int k1, T v) {
+__device__ __forceinline__ void fill_row(T* o, const Piece<T>& w, T v) {
     constexpr int N = Wide<T>::N;
-    typename Wide<T>::V w;
+    typename Wide<T>::V x;
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = v;
-    const int end = body_end<T>(k0, k1);
-    for (int k = k0 + (int)threadIdx.x * N; k < end; k += NT * N) store_wide<T>(o + k, w);
-    if ((int)threadIdx.x < k1 - end) o[end + threadIdx.x] = v;
+    for (int i = 0; i < N; ++i) x[i] = v;
+    for (int k = w.from + (int)threadIdx.x * N; k < w.to; k += NT * N) store_wide<T>(o + k, x);
+    const int k = w.edge();
+    if (k >= 0) o[k] = v;
 }
 
 constexpr int kVjpNT = 256;
@@ -364,23 +381,22 @@ __global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t ro
                                                      const float* __restrict__ g_ent, T* grad, int64_t ldg) {
     for (int64_t item = blockIdx.x; item < rows * splits; item += gridDim.x) {
         const int64_t r = item / splits;
-        const int k0 = (int)(item - r * splits) * chunk, k1 = min(k0 + chunk, vocab);
         const int32_t j = target[r];
         const T* x = logits + r * ld;
         T* o = grad + r * ldg;
+        const Piece<T> w(o, (int)(item - r * splits), chunk, vocab);
         if (j < 0 || j >= vocab) {
-            fill_row<T, kVjpNT>(o, k0, k1, j < 0 ? (T)0.0f : (T)__builtin_nanf(""));
+            fill_row<T, kVjpNT>(o, w, j < 0 ? (T)0.0f : (T)__builtin_nanf(""));
             continue;
         }
         const RowGrad q = row_grad((double)lse[r], (double)g_logp[r], ENT ? (double)ent[r] : 0.0,
                                    ENT ? (double)g_ent[r] : 0.0, inv_t, temperature);
-        const int end = body_end<T>(k0, k1);
-        for (int k = k0; k < end; k += Chunk<T, kVjpNT, 4>::kSize) {
+        for (int k = w.from; k < w.to; k += Chunk<T, kVjpNT, 4>::kSize) {
             Chunk<T, kVjpNT, 4> c;
-            c.load(x, k, end);
-            store_grads<T, ENT>(c, o, k, end, j, q, cf);
+            c.load(x, k, w.to);
+            store_grads<T, ENT>(c, o, k, w.to, j, q, cf);
         }
-        store_rest<T, ENT>(x, o, end, k1, j, q, cf);
+        store_edge<T, ENT>(x, o, w.edge(), j, q, cf);
     }
 }
 
@@ -399,17 +415,14 @@ __global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t 
     __shared__ double of_row[2];  // log-sum, gradient of the token's logp
     __shared__ PolicySums total;  // thread 0's
     if (threadIdx.x == 0) total = PolicySums{0.0, 0.0, 0, 0};
-    // the first chunk is what whole chunks leave over
-    const int end = body_end<T>(0, vocab);
-    const int before = end ? (end - 1) / C::kSize : 0;  // whole chunks after it
-    const int first = end - before * C::kSize;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const int32_t j = target[r];
         const T* x = logits + r * ld;
         T* o = grad + r * ldg;
+        const Piece<T> w(x, 0, vocab, vocab);  // by the logits, with or without a gradient: the same sums
         if (j < 0) {
             if (threadIdx.x == 0) logp[r] = 0.0f;
-            if (grad) fill_row<T, NT>(o, 0, vocab, (T)0.0f);
+            if (grad) fill_row<T, NT>(o, w, (T)0.0f);
             continue;
         }
         const RowTerm t = terms[r];
@@ -417,14 +430,17 @@ __global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t 
         const T xj = x[j < vocab ? j : 0];
         C c;
         Running<T, false, NT, U> run;
-        int k = 0, e = first;
+        // the first chunk is what whole chunks leave over
+        const int after = w.to > w.from ? (w.to - w.from - 1) / C::kSize : 0;
+        int k = w.from, e = w.to - after * C::kSize;
         do {
             c.load(x, k, e);
             run.add(c, sc);
             k = e;
             e += C::kSize;
-        } while (k < end);
-        if ((int)threadIdx.x < vocab - end) run.add_one((float)x[end + threadIdx.x], sc);
+        } while (k < w.to);
+        const int edge = w.edge();
+        if (edge >= 0) run.add_one((float)x[edge], sc);
         c.forget();
         const Stat a = run.join(sc, part);
         if (threadIdx.x == 0) {
@@ -446,17 +462,17 @@ __global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t 
         __syncthreads();
         if (grad && j < vocab) {
             const RowGrad q = row_grad(of_row[0], of_row[1], 0.0, 0.0, sc.inv_t, temperature);
-            store_rest<T, false>(x, o, end, vocab, j, q, sc.cf);
+            store_edge<T, false>(x, o, edge, j, q, sc.cf);
             // the last chunk is still in registers, the others follow backwards
-            for (e = end;;) {
-                k = max(e - C::kSize, 0);
+            for (e = w.to;;) {
+                k = max(e - C::kSize, w.from);
                 store_grads<T, false>(c, o, k, e, j, q, sc.cf);
-                if (k == 0) break;
+                if (k == w.from) break;
                 e = k;
-                c.load(x, max(e - C::kSize, 0), e);
+                c.load(x, max(e - C::kSize, w.from), e);
             }
         } else if (grad) {
-            fill_row<T, NT>(o, 0, vocab, (T)__builtin_nanf(""));
+            fill_row<T, NT>(o, w, (T)__builtin_nanf(""));
         }
         __syncthreads();  // part and of_row are used again
     }
