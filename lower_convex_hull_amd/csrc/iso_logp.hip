@@ -19,6 +19,7 @@ template <typename T>
 struct Wide {
     static constexpr int N = 16 / sizeof(T);
     typedef T V __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+    typedef T A __attribute__((ext_vector_type(16 / sizeof(T))));  // aligned, in LDS
 };
 
 template <typename T>
@@ -117,6 +118,15 @@ struct Chunk {
                 if (at(k, u) < k1) v[u] = load_wide<T>(b + u * NT * N + threadIdx.x * N);
             }
         }
+    }
+    // The thread's own vectors to LDS and back.
+    __device__ __forceinline__ void put(typename Wide<T>::A* keep) const {
+#pragma unroll
+        for (int u = 0; u < U; ++u) keep[u * NT + threadIdx.x] = v[u];
+    }
+    __device__ __forceinline__ void take(const typename Wide<T>::A* keep) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = keep[u * NT + threadIdx.x];
     }
     // What was computed of the values so far is not kept in registers, only
     // the values: their f32 forms take twice the room and are made again.
@@ -369,7 +379,7 @@ __device__ __forceinline__ void fill_row(T* o, const Piece<T>& w, T v) {
     if (k >= 0) o[k] = v;
 }
 
-constexpr int kVjpNT = 256;
+constexpr int kVjpNT = 256, kVjpU = 2;
 
 // Item = (row, chunk of it).
 template <typename T, bool ENT>
@@ -391,8 +401,8 @@ __global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t ro
         }
         const RowGrad q = row_grad((double)lse[r], (double)g_logp[r], ENT ? (double)ent[r] : 0.0,
                                    ENT ? (double)g_ent[r] : 0.0, inv_t, temperature);
-        for (int k = w.from; k < w.to; k += Chunk<T, kVjpNT, 4>::kSize) {
-            Chunk<T, kVjpNT, 4> c;
+        for (int k = w.from; k < w.to; k += Chunk<T, kVjpNT, kVjpU>::kSize) {
+            Chunk<T, kVjpNT, kVjpU> c;
             c.load(x, k, w.to);
             store_grads<T, ENT>(c, o, k, w.to, j, q, cf);
         }
@@ -414,6 +424,8 @@ __global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t 
     __shared__ Stat part[NT / 64];
     __shared__ double of_row[2];  // log-sum, gradient of the token's logp
     __shared__ PolicySums total;  // thread 0's
+    constexpr bool kKeep = NT * U >= 4096;
+    __shared__ typename Wide<T>::A keep[kKeep ? NT * U : 1];
     if (threadIdx.x == 0) total = PolicySums{0.0, 0.0, 0, 0};
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const int32_t j = target[r];
@@ -436,6 +448,7 @@ __global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t 
         do {
             c.load(x, k, e);
             run.add(c, sc);
+            if (kKeep && e + C::kSize == w.to) c.put(keep);
             k = e;
             e += C::kSize;
         } while (k < w.to);
@@ -469,7 +482,8 @@ __global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t 
                 store_grads<T, false>(c, o, k, e, j, q, sc.cf);
                 if (k == w.from) break;
                 e = k;
-                c.load(x, max(e - C::kSize, w.from), e);
+                if (kKeep && e + C::kSize == w.to) c.take(keep);
+                else c.load(x, max(e - C::kSize, w.from), e);
             }
         } else if (grad) {
             fill_row<T, NT>(o, w, (T)__builtin_nanf(""));
@@ -560,7 +574,7 @@ void start_vjp(const void* logits, int64_t rows, int64_t vocab, int64_t ld, cons
     const Scale sc = scale_of(temperature);
     const T* x = static_cast<const T*>(logits);
     T* o = static_cast<T*>(grad);
-    const int chunk = 4 * 4 * kVjpNT * Wide<T>::N;
+    const int chunk = kVjpU * kVjpNT * Wide<T>::N;
     const int splits = (int)((vocab + chunk - 1) / chunk);
     const dim3 grid = grid_of(rows * splits), nt(kVjpNT);
     if (g_ent)
@@ -581,7 +595,7 @@ void by_dtype(int dtype, F f) {
 
 // Workspace and grid of iso_policy_loss_logits.
 constexpr int64_t kHeadGrid = 8192;
-constexpr int64_t kHeadWide = 128 << 10, kHeadMid = 40 << 10, kHeadNarrow = 8 << 10;  // bytes of a row
+constexpr int64_t kHeadWide = 160 << 10, kHeadMid = 40 << 10, kHeadNarrow = 8 << 10;  // bytes of a row
 struct HeadPlan {
     int grid;
     size_t off_terms, off_sums, off_weights, bytes;
