@@ -517,25 +517,36 @@ bool grad_ok(const void* logits, void* grad, int dtype, int64_t rows, int64_t vo
     return !overlap({grad, matrix_bytes(dtype, rows, vocab, ldg)}, {logits, matrix_bytes(dtype, rows, vocab, ld)});
 }
 
-// How a row is split over workgroups: one takes a whole row where there are
-// enough rows, else parts of at least kMinPart bytes.
+// How a row is split over workgroups, and how many threads take a piece.
+// Few rows of many bytes are split (1 x 131072 bf16: 10.4 us whole, 6.2 in
+// pieces of 16 KB; 96 x 131072 f16 14.4 and 12.5), others not: the pieces are
+// joined by a second launch (1 x 32768 bf16: 4.9 us whole, 6.1 split; 256 x
+// 131072 14.9 and 17.8, 150 x 65536 7.7 and 10.6).  Threads are as many as one chunk of the piece takes
+// (900 x 4000 bf16: 5.1 us with 64, 6.6 with 256, 20.6 with 1024), at most 256 where there
+// are workgroups enough to fill the GPU without.
 struct LogpPlan {
-    int splits;
+    int splits, threads;
     int64_t chunk;
     size_t bytes;
 };
-constexpr int64_t kLogpGrid = 1024;     // workgroups wanted
-constexpr int64_t kMinPart = 64 << 10;  // bytes of a row
+constexpr int64_t kFewRows = 128, kWholeRow = 96 << 10;  // split below / above
+constexpr int64_t kPart = 16 << 10, kPartsMax = 2048;     // bytes of a piece, pieces wanted at most
+constexpr int64_t kManyPieces = 1024;
 LogpPlan logp_plan(int64_t rows, int64_t vocab, int dtype) {
-    const int64_t parts = (vocab * (int64_t)size_of(dtype) + kMinPart - 1) / kMinPart;
-    const int64_t want = rows ? (kLogpGrid + rows - 1) / rows : 1;
-    int64_t splits = parts < want ? parts : want;
-    if (splits < 1) splits = 1;
-    // parts of whole steps of a workgroup
-    const int64_t step = 8192;
-    const int64_t chunk = splits == 1 ? vocab : ((vocab + splits - 1) / splits + step - 1) / step * step;
-    splits = (vocab + chunk - 1) / chunk;
-    return LogpPlan{(int)splits, chunk, splits > 1 ? (size_t)rows * (size_t)splits * sizeof(Stat) : 0};
+    const int64_t size = (int64_t)size_of(dtype), step = kPart / size;
+    int64_t chunk = vocab;
+    if (rows && rows < kFewRows && vocab * size > kWholeRow) {
+        const int64_t most = kPartsMax / rows;
+        const int64_t parts = (vocab + step - 1) / step;
+        chunk = (parts + most - 1) / most * step;
+    }
+    const int64_t splits = (vocab + chunk - 1) / chunk, bytes = chunk * size;
+    LogpPlan p;
+    p.splits = (int)splits;
+    p.chunk = chunk;
+    p.threads = bytes <= 8 << 10 ? 64 : bytes <= 16 << 10 || rows * splits >= kManyPieces ? 256 : bytes <= 32 << 10 ? 512 : 1024;
+    p.bytes = splits > 1 ? (size_t)rows * (size_t)splits * sizeof(Stat) : 0;
+    return p;
 }
 
 Scale scale_of(double temperature) {
@@ -548,12 +559,15 @@ void start_logp_t(const T* x, int64_t rows, int64_t vocab, int64_t ld, const int
                   const LogpOut& o, const LogpPlan& pl, void* workspace, hipStream_t st) {
     const Scale sc = scale_of(temperature);
     Stat* parts = static_cast<Stat*>(workspace);
-    if (rows * pl.splits < kLogpGrid)
-        hipLaunchKernelGGL((k_token_logp<T, ENT, 1024>), grid_of(rows * pl.splits), dim3(1024), 0, st, x, rows,
-                           (int)vocab, ld, target, sc, pl.splits, (int)pl.chunk, o, parts);
-    else
-        hipLaunchKernelGGL((k_token_logp<T, ENT, 256>), grid_of(rows * pl.splits), dim3(256), 0, st, x, rows,
-                           (int)vocab, ld, target, sc, pl.splits, (int)pl.chunk, o, parts);
+    auto start = [&](auto nt) {
+        constexpr int NT = decltype(nt)::value;
+        hipLaunchKernelGGL((k_token_logp<T, ENT, NT>), grid_of(rows * pl.splits), dim3(NT), 0, st, x, rows, (int)vocab,
+                           ld, target, sc, pl.splits, (int)pl.chunk, o, parts);
+    };
+    if (pl.threads == 64) start(std::integral_constant<int, 64>{});
+    else if (pl.threads == 256) start(std::integral_constant<int, 256>{});
+    else if (pl.threads == 512) start(std::integral_constant<int, 512>{});
+    else start(std::integral_constant<int, 1024>{});
     if (pl.splits > 1)
         hipLaunchKernelGGL((k_token_logp_join<T, ENT>), grid_of((rows + kJoinNT / 64 - 1) / (kJoinNT / 64)),
                            dim3(kJoinNT), 0, st, x, rows, (int)vocab, ld, target, sc, pl.splits, parts, o);
