@@ -206,8 +206,9 @@ def run(state):
             return iso.token_logp_vjp(state["g"], state["logits"], state["target"], state["lse"], temperature=case["temperature"],
                                       entropy=state["ent"], g_entropy=state["gent"])
         if kind == "pref":
+            smoothing = 0.0 if case["squared"] else case["smoothing"]  # the squared loss has none
             return iso.pref_loss(state["logp"], state["ref"], state["off"], mask=state["mask"], beta=case["beta"],
-                                 label_smoothing=case["smoothing"], squared=case["squared"], mean=case["mean"])
+                                 label_smoothing=smoothing, squared=case["squared"], mean=case["mean"])
         if kind == "policy":
             return iso.policy_loss(state["logp"], state["old"], state["adv"], ref_logp=state["ref"], mask=state["mask"],
                                    seq_off=state["off"], clip_lo=case["lo"], clip_hi=case["hi"], kl_coef=case["kl"],
