@@ -32,7 +32,11 @@ __device__ __forceinline__ typename Wide<T>::V load_wide(const T* p) {
 // term counts, the largest term is exactly 1, and no finite logit overflows.
 struct Scale {
     double inv_t, c;
-    float cf;  // c in f32
+    float cf, rest;  // c rounded down to f32, and what that leaves off (> 0: -infinity stays -infinity)
+    float near;      // c in f32, for single terms
+    // An exponent.  All terms of a sum carry the rounding of c alike, so it is
+    // taken back: 1.5e-7 of lse at 32768 logits.
+    __device__ __forceinline__ float times(float d) const { return fmaf(d, rest, d * cf); }
 };
 
 // The maximum that differences are taken to: 0 where everything so far is
@@ -157,7 +161,7 @@ struct Running {
             for (int i = 0; i < N; ++i) bm = fmaxf(bm, (float)c.v[u][i]);
         if (bm > m) {
             if (m != -INFINITY) {
-                const float d = held((m - bm) * sc.cf), f = __builtin_amdgcn_exp2f(d);
+                const float d = held(sc.times(m - bm)), f = __builtin_amdgcn_exp2f(d);
                 if (ENT) h = (h + s * (double)d) * (double)f;
                 s *= (double)f;
             }
@@ -170,7 +174,7 @@ struct Running {
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float a = ((float)c.v[u][i] - base) * sc.cf;
+                const float a = sc.times((float)c.v[u][i] - base);
                 const float e = __builtin_amdgcn_exp2f(a);
                 fs += e;
                 if (ENT) fh = fmaf(e, held(a), fh);
@@ -185,7 +189,7 @@ struct Running {
             rebase<ENT>(a, (double)x, sc);
             m = x;
         }
-        const float d = (x - base_of(m)) * sc.cf, e = __builtin_amdgcn_exp2f(d);
+        const float d = sc.times(x - base_of(m)), e = __builtin_amdgcn_exp2f(d);
         s = a.s + (double)e;
         if (ENT) h = a.h + (double)(e * held(d));
     }
@@ -475,11 +479,11 @@ __global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t 
         __syncthreads();
         if (grad && j < vocab) {
             const RowGrad q = row_grad(of_row[0], of_row[1], 0.0, 0.0, sc.inv_t, temperature);
-            store_edge<T, false>(x, o, edge, j, q, sc.cf);
+            store_edge<T, false>(x, o, edge, j, q, sc.near);
             // the last chunk is still in registers, the others follow backwards
             for (e = w.to;;) {
                 k = max(e - C::kSize, w.from);
-                store_grads<T, false>(c, o, k, e, j, q, sc.cf);
+                store_grads<T, false>(c, o, k, e, j, q, sc.near);
                 if (k == w.from) break;
                 e = k;
                 if (kKeep && e + C::kSize == w.to) c.take(keep);
@@ -551,7 +555,10 @@ LogpPlan logp_plan(int64_t rows, int64_t vocab, int dtype) {
 
 Scale scale_of(double temperature) {
     const double c = kLog2e / temperature;
-    return Scale{1.0 / temperature, c, (float)c};
+    const float near = (float)c;
+    float cf = near;
+    if ((double)cf > c) cf = nextafterf(cf, 0.0f);
+    return Scale{1.0 / temperature, c, cf, fmaxf((float)(c - (double)cf), 1e-30f), near};
 }
 
 template <typename T, bool ENT>
@@ -593,10 +600,10 @@ void start_vjp(const void* logits, int64_t rows, int64_t vocab, int64_t ld, cons
     const dim3 grid = grid_of(rows * splits), nt(kVjpNT);
     if (g_ent)
         hipLaunchKernelGGL((k_logp_vjp<T, true>), grid, nt, 0, st, x, rows, (int)vocab, ld, target, sc.inv_t,
-                           temperature, sc.cf, splits, chunk, lse, ent, g_logp, g_ent, o, ldg);
+                           temperature, sc.near, splits, chunk, lse, ent, g_logp, g_ent, o, ldg);
     else
         hipLaunchKernelGGL((k_logp_vjp<T, false>), grid, nt, 0, st, x, rows, (int)vocab, ld, target, sc.inv_t,
-                           temperature, sc.cf, splits, chunk, lse, ent, g_logp, g_ent, o, ldg);
+                           temperature, sc.near, splits, chunk, lse, ent, g_logp, g_ent, o, ldg);
 }
 
 // f called with a value of the logits' type.
