@@ -417,13 +417,15 @@ __global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t ro
 // The policy loss from the logits, a row of a workgroup at a time: its
 // statistics, its token's terms, and its gradient, for which the row is read
 // again while the last-level cache may still have it.  Every row's weight and
-// advantage are known before (they depend on the targets alone).
+// advantage depend on the targets alone and are known before (terms), or (NULL;
+// few rows) are found here, which saves a launch.
 template <typename T, int NT, int U>
 __global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t rows, int vocab, int64_t ld,
                                                        const int32_t* __restrict__ target, Scale sc,
                                                        double temperature, Policy p,
-                                                       const RowTerm* __restrict__ terms, float* __restrict__ logp,
-                                                       T* grad, int64_t ldg, PolicySums* __restrict__ sums) {
+                                                       const RowTerm* __restrict__ terms, Seqs sq,
+                                                       float* __restrict__ logp, T* grad, int64_t ldg,
+                                                       PolicySums* __restrict__ sums) {
     typedef Chunk<T, NT, U> C;
     __shared__ Stat part[NT / 64];
     __shared__ double of_row[2];  // log-sum, gradient of the token's logp
@@ -441,7 +443,7 @@ __global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t 
             if (grad) fill_row<T, NT>(o, w, (T)0.0f);
             continue;
         }
-        const RowTerm t = terms[r];
+        const RowTerm t = terms ? terms[r] : own_row_term<NT>(p, target, sq, (uint32_t)r);
         const float old = p.old_logp[r], ref = p.ref_logp ? p.ref_logp[r] : 0.0f;
         const T xj = x[j < vocab ? j : 0];
         C c;
@@ -616,6 +618,7 @@ void by_dtype(int dtype, F f) {
 
 // Workspace and grid of iso_policy_loss_logits.
 constexpr int64_t kHeadGrid = 8192;
+constexpr int64_t kOwnTerms = 256;  // rows and sequences up to which a row's workgroup finds its term itself
 constexpr int64_t kHeadWide = 160 << 10, kHeadMid = 40 << 10, kHeadNarrow = 8 << 10;  // bytes of a row
 struct HeadPlan {
     int grid;
@@ -633,7 +636,7 @@ HeadPlan head_plan(int64_t rows, int64_t seqs) {
 
 template <typename T>
 void start_rows(const void* logits, int64_t rows, int64_t vocab, int64_t ld, const int32_t* target,
-                double temperature, const Policy& p, const RowTerm* terms, float* logp, void* grad, int64_t ldg,
+                double temperature, const Policy& p, const RowTerm* terms, const Seqs& sq, float* logp, void* grad, int64_t ldg,
                 PolicySums* sums, int grid, hipStream_t st) {
     const T* x = static_cast<const T*>(logits);
     T* o = static_cast<T*>(grad);
@@ -642,7 +645,7 @@ void start_rows(const void* logits, int64_t rows, int64_t vocab, int64_t ld, con
     auto start = [&](auto nt, auto u) {
         constexpr int NT = decltype(nt)::value, U = decltype(u)::value;
         hipLaunchKernelGGL((k_policy_rows<T, NT, U>), dim3(grid), dim3(NT), 0, st, x, rows, (int)vocab, ld, target, sc,
-                           temperature, p, terms, logp, o, ldg, sums);
+                           temperature, p, terms, sq, logp, o, ldg, sums);
     };
     typedef std::integral_constant<int, 4> Four;
     typedef std::integral_constant<int, 8> Eight;
@@ -745,11 +748,12 @@ int iso_policy_loss_logits(const void* logits, int dtype, int64_t rows, int64_t 
     PolicySums* sums = reinterpret_cast<PolicySums*>(ws + pl.off_sums);
     const Policy p = make_policy(old_logp, ref_logp, adv, clip_lo, clip_hi, kl_coef, norm, grad_scale, flags);
     if (rows) {
-        if (launch_row_terms(p, target, make_seqs(seq_off, seqs, rows), terms, ws + pl.off_weights, st) != hipSuccess)
-            return ISO_ERR_HIP;
+        const Seqs sq = make_seqs(seq_off, seqs, rows);
+        const bool own = rows <= kOwnTerms && seqs <= kOwnTerms;
+        if (!own && launch_row_terms(p, target, sq, terms, ws + pl.off_weights, st) != hipSuccess) return ISO_ERR_HIP;
         by_dtype(dtype, [&](auto v) {
-            start_rows<decltype(v)>(logits, rows, vocab, ld, target, temperature, p, terms, logp, grad, ld_grad, sums,
-                                    pl.grid, st);
+            start_rows<decltype(v)>(logits, rows, vocab, ld, target, temperature, p, own ? nullptr : terms, sq, logp, grad,
+                                    ld_grad, sums, pl.grid, st);
         });
     }
     return launch_policy_out(p, sums, pl.grid, loss, counts, st) == hipSuccess ? ISO_OK : ISO_ERR_HIP;

@@ -532,14 +532,6 @@ struct Weights {
     int* counted;     // a workgroup's tokens that take part (else)
     uint32_t parts;   // how many of them
     __device__ __forceinline__ bool by_seq() const { return p.seq_mean != 0; }
-    // a sequence's w_t, from the tokens that take part in it
-    __device__ __forceinline__ double seq_weight(double count) const {
-        return 1.0 / ((p.norm > 0.0 ? p.norm : (double)sq.n) * fmax(count, 1.0));
-    }
-    // every token's w_t where they are alike
-    __device__ __forceinline__ double token_weight(int count) const {
-        return 1.0 / (p.norm > 0.0 ? p.norm : fmax((double)count, 1.0));
-    }
 };
 
 // What tokens take from their sequence: its advantage, its weight.
@@ -568,7 +560,7 @@ __device__ __forceinline__ void count_by_seq(const Weights& c, uint32_t span, in
 }
 __device__ __forceinline__ void weigh_seq(const Weights& c, uint32_t q, uint32_t size) {
     const double n = c.live.all() ? (double)(c.sq.end(q) - c.sq.begin(q)) : c.sums.get(c.sq, q, size).count;
-    if ((threadIdx.x & 63) == 0) c.weight[q] = c.seq_weight(n);
+    if ((threadIdx.x & 63) == 0) c.weight[q] = c.p.seq_weight(c.sq.n, n);
 }
 
 // The weight that all tokens share, for every thread of a workgroup: from the
@@ -577,10 +569,10 @@ template <int NT>
 __device__ __forceinline__ double shared_weight(const Weights& c) {
     __shared__ int red[NT / 64];
     if (c.by_seq()) return 0.0;
-    if (c.live.all()) return c.token_weight((int)c.sq.tokens);
+    if (c.live.all()) return c.p.token_weight((int)c.sq.tokens);
     int n = 0;
     for (uint32_t k = threadIdx.x; k < c.parts; k += NT) n += c.counted[k];
-    return c.token_weight(wg_sum<NT>(n, red));
+    return c.p.token_weight(wg_sum<NT>(n, red));
 }
 // The weights of a small call, by one workgroup: every token's if they are alike.
 template <int NT>
@@ -597,10 +589,10 @@ __device__ __forceinline__ double small_weights(const Weights& c, uint32_t spans
         __syncthreads();
         return 0.0;
     }
-    if (c.live.all()) return c.token_weight((int)c.sq.tokens);
+    if (c.live.all()) return c.p.token_weight((int)c.sq.tokens);
     int n = 0;
     for (uint32_t s = w.id; s < spans; s += w.count) n += (int)__popc(c.live.bits(Place<1>(s, c.sq.tokens)));
-    return c.token_weight(wg_sum<NT>(n, red));
+    return c.p.token_weight(wg_sum<NT>(n, red));
 }
 
 __global__ __launch_bounds__(kLossNT) void k_count_by_seq(Weights c, uint32_t spans) {

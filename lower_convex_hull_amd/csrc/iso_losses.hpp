@@ -110,6 +110,14 @@ struct Policy {
     double kl_coef;
     double norm;               // > 0: in place of the count of tokens or sequences
     double grad_scale;
+    // w_t of a sequence's tokens (ISO_POLICY_SEQ_MEAN), from those that take part in it
+    __device__ __forceinline__ double seq_weight(uint32_t seqs, double count) const {
+        return 1.0 / ((norm > 0.0 ? norm : (double)seqs) * fmax(count, 1.0));
+    }
+    // every token's w_t where they are alike
+    __device__ __forceinline__ double token_weight(int count) const {
+        return 1.0 / (norm > 0.0 ? norm : fmax((double)count, 1.0));
+    }
 };
 // exp(x), exp(x) - 1 and exp(x) - 1 - x in f64.  Cody and Waite's reduction
 // x = k ln 2 + r with |r| <= ln(2)/2, then Taylor's series q of exp(r) - 1 - r
@@ -215,6 +223,23 @@ struct RowTerm {
     double w;
     float adv, pad;
 };
+// Row r's, by a workgroup of NT threads that each look at some sequences and
+// targets.
+template <int NT>
+__device__ __forceinline__ RowTerm own_row_term(const Policy& p, const int32_t* __restrict__ target, const Seqs& sq,
+                                                uint32_t r) {
+    uint32_t q = 0;
+    if (sq.off) {
+        for (uint32_t k = 1; k < sq.n; k += NT)
+            q += (uint32_t)__syncthreads_count(k + threadIdx.x < sq.n && sq.begin(k + threadIdx.x) <= r);
+    } else {
+        q = r / sq.len;
+    }
+    const uint32_t b = p.seq_mean ? sq.begin(q) : 0u, e = p.seq_mean ? sq.end(q) : sq.tokens;
+    int count = 0;
+    for (uint32_t t = b; t < e; t += NT) count += __syncthreads_count(t + threadIdx.x < e && target[t + threadIdx.x] >= 0);
+    return RowTerm{p.seq_mean ? p.seq_weight(sq.n, (double)count) : p.token_weight(count), p.adv[p.token_adv ? r : q], 0.0f};
+}
 // Every row's, from the rows' targets (negative: no part) and the sequences.
 size_t row_terms_workspace(int64_t rows, int64_t seqs);
 hipError_t launch_row_terms(const Policy& p, const int32_t* target, const Seqs& sq, RowTerm* terms, void* workspace,
