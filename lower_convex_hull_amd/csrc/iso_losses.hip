@@ -625,7 +625,7 @@ struct PolicyCall {
 
 // What a policy call has: advantages by token, weights by sequence, a
 // reference.  The kernels over tokens are made for each combination: asked at
-// run time, the questions are half of the instructions (67 -> ... us at 8e6 tokens).
+// run time, the questions are a third of the instructions (67 -> 61 us at 8e6 tokens).
 template <bool TOKEN_ADV, bool BY_SEQ, bool REF>
 struct Kind {
     static constexpr bool token_adv = TOKEN_ADV, by_seq = BY_SEQ, ref = REF;
