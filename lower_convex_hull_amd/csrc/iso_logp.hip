@@ -537,7 +537,7 @@ struct LogpPlan {
 };
 constexpr int64_t kFewRows = 128, kWholeRow = 96 << 10;  // split below / above
 constexpr int64_t kPart = 16 << 10, kPartsMax = 2048;     // bytes of a piece, pieces wanted at most
-constexpr int64_t kManyPieces = 1024;
+constexpr int64_t kFullPieces = 256, kManyPieces = 640;  // more than a CU's share of one, of two pieces
 LogpPlan logp_plan(int64_t rows, int64_t vocab, int dtype) {
     const int64_t size = (int64_t)size_of(dtype), step = kPart / size;
     int64_t chunk = vocab;
@@ -550,7 +550,11 @@ LogpPlan logp_plan(int64_t rows, int64_t vocab, int dtype) {
     LogpPlan p;
     p.splits = (int)splits;
     p.chunk = chunk;
-    p.threads = bytes <= 8 << 10 ? 64 : bytes <= 16 << 10 || rows * splits >= kManyPieces ? 256 : bytes <= 32 << 10 ? 512 : 1024;
+    const int64_t pieces = rows * splits;
+    p.threads = bytes <= 8 << 10                             ? 64
+                : bytes <= 16 << 10 || pieces > kManyPieces ? 256
+                : bytes <= 32 << 10 || pieces > kFullPieces ? 512
+                                                            : 1024;
     p.bytes = splits > 1 ? (size_t)rows * (size_t)splits * sizeof(Stat) : 0;
     return p;
 }
@@ -619,7 +623,7 @@ void by_dtype(int dtype, F f) {
 // Workspace and grid of iso_policy_loss_logits.
 constexpr int64_t kHeadGrid = 8192;
 constexpr int64_t kOwnTerms = 256;  // rows and sequences up to which a row's workgroup finds its term itself
-constexpr int64_t kHeadWide = 160 << 10, kHeadMid = 40 << 10, kHeadNarrow = 8 << 10;  // bytes of a row
+constexpr int64_t kHeadWide = 232 << 10, kHeadMid = 40 << 10, kHeadNarrow = 8 << 10;  // bytes of a row
 struct HeadPlan {
     int grid;
     size_t off_terms, off_sums, off_weights, bytes;

@@ -221,18 +221,30 @@ struct Part {
 // into tail, one between is whole.
 struct PartSums {
     Part *head, *tail, *whole;
-    // The sum of sequence q over spans of `size` tokens; all lanes of a wave together.
-    __device__ __forceinline__ Part get(const Seqs& sq, uint32_t q, uint32_t size) const {
+    // The sum of sequence q over spans of `size` tokens, by N lanes of which this
+    // is number i: the first span's part by where the sequence begins and ends in
+    // it, the others are their spans' first.
+    __device__ __forceinline__ Part some(const Seqs& sq, uint32_t q, uint32_t size, uint32_t i, uint32_t n) const {
         const uint32_t b = sq.begin(q), e = sq.end(q);
         Part v{0.0, 0.0};
         if (e <= b) return v;
         const uint32_t s0 = b / size, s1 = (e - 1) / size;
-        for (uint32_t s = s0 + (threadIdx.x & 63); s <= s1; s += 64) {
-            const Part x = b <= s * size ? head[s] : e >= min((s + 1) * size, sq.tokens) ? tail[s] : whole[q];
-            v.sum += x.sum;
-            v.count += x.count;
+        if (i == 0) v = b <= s0 * size ? head[s0] : e >= min((s0 + 1) * size, sq.tokens) ? tail[s0] : whole[q];
+#pragma unroll 4
+        for (uint32_t s = s0 + 1 + i; s <= s1; s += n) {
+            v.sum += head[s].sum;
+            v.count += head[s].count;
         }
+        return v;
+    }
+    // by a wave, all lanes together
+    __device__ __forceinline__ Part by_wave(const Seqs& sq, uint32_t q, uint32_t size) const {
+        const Part v = some(sq, q, size, threadIdx.x & 63, 64);
         return Part{wave_sum(v.sum), wave_sum(v.count)};
+    }
+    // by one thread: where a sequence has a few spans at most
+    __device__ __forceinline__ Part by_lane(const Seqs& sq, uint32_t q, uint32_t size) const {
+        return some(sq, q, size, 0, 1);
     }
 };
 
@@ -419,8 +431,8 @@ __device__ __forceinline__ void pref_sums(const Pref& p, uint32_t span, int* map
     sum_span<G, true>(w, span, s, v, live, p.sums);
 }
 
-__device__ __forceinline__ void pref_pair(const Pref& p, uint32_t i, uint32_t size) {
-    Part c = p.sums.get(p.sq, 2 * i, size), r = p.sums.get(p.sq, 2 * i + 1, size);
+// Pair i, of the sums c and r of its sequences.
+__device__ __forceinline__ void pref_pair(const Pref& p, uint32_t i, Part c, Part r) {
     const double fc = p.mean ? 1.0 / fmax(c.count, 1.0) : 1.0, fr = p.mean ? 1.0 / fmax(r.count, 1.0) : 1.0;
     c.sum *= fc;
     r.sum *= fr;
@@ -435,7 +447,6 @@ __device__ __forceinline__ void pref_pair(const Pref& p, uint32_t i, uint32_t si
         loss = (1.0 - p.smooth) * softplus_neg(h) + (p.smooth > 0.0 ? p.smooth * softplus_neg(-h) : 0.0);
         slope = p.beta * (p.smooth / (1.0 + exp(-h)) - (1.0 - p.smooth) / (1.0 + exp(h)));
     }
-    if ((threadIdx.x & 63) != 0) return;
     slope *= p.grad_scale / (double)p.pairs;
     p.each[i] = loss;
     p.coef[2 * i] = (float)(slope * fc);
@@ -483,7 +494,10 @@ __global__ __launch_bounds__(kLossNT) void k_pref_sums(Pref p, uint32_t spans) {
 }
 __global__ __launch_bounds__(kLossNT) void k_pref_pairs(Pref p) {
     const Wave w;
-    for (uint32_t i = w.id; i < p.pairs; i += w.count) pref_pair(p, i, 256 * kSpanG);
+    for (uint32_t i = w.id; i < p.pairs; i += w.count) {
+        const Part c = p.sums.by_wave(p.sq, 2 * i, 256 * kSpanG), r = p.sums.by_wave(p.sq, 2 * i + 1, 256 * kSpanG);
+        if ((threadIdx.x & 63) == 0) pref_pair(p, i, c, r);
+    }
 }
 // The first workgroup takes the mean of the pair losses, the others the tokens.
 __global__ __launch_bounds__(kLossNT) void k_pref_grad(Pref p, uint32_t spans) {
@@ -503,7 +517,8 @@ __global__ __launch_bounds__(kOneNT) void k_pref_one(Pref p, uint32_t spans) {
     Cursor first, second;
     w.each(spans, [&](uint32_t s) { pref_sums<1>(p, s, maps.mine(), first); });
     __syncthreads();
-    for (uint32_t i = w.id; i < p.pairs; i += w.count) pref_pair(p, i, 256);
+    for (uint32_t i = threadIdx.x; i < p.pairs; i += kOneNT)
+        pref_pair(p, i, p.sums.by_lane(p.sq, 2 * i, 256), p.sums.by_lane(p.sq, 2 * i + 1, 256));
     __syncthreads();
     if (p.grad) w.each(spans, [&](uint32_t s) { pref_grad<1>(p, s, maps.mine(), second); });
     pref_mean<kOneNT>(p);
@@ -558,9 +573,14 @@ __device__ __forceinline__ void count_by_seq(const Weights& c, uint32_t span, in
     const Ids<G> s = seq_ids(c.sq, w, map, cur);
     sum_span<G, false>(w, span, s, nullptr, live, c.sums);
 }
+// Sequence q's weight, from the count of its tokens that take part: by a wave,
+// or by one thread.
+template <bool WAVE>
 __device__ __forceinline__ void weigh_seq(const Weights& c, uint32_t q, uint32_t size) {
-    const double n = c.live.all() ? (double)(c.sq.end(q) - c.sq.begin(q)) : c.sums.get(c.sq, q, size).count;
-    if ((threadIdx.x & 63) == 0) c.weight[q] = c.p.seq_weight(c.sq.n, n);
+    const double n = c.live.all() ? (double)(c.sq.end(q) - c.sq.begin(q))
+                     : WAVE       ? c.sums.by_wave(c.sq, q, size).count
+                                  : c.sums.by_lane(c.sq, q, size).count;
+    if (!WAVE || (threadIdx.x & 63) == 0) c.weight[q] = c.p.seq_weight(c.sq.n, n);
 }
 
 // The weight that all tokens share, for every thread of a workgroup: from the
@@ -585,7 +605,7 @@ __device__ __forceinline__ double small_weights(const Weights& c, uint32_t spans
             w.each(spans, [&](uint32_t s) { count_by_seq<1>(c, s, map, cur); });
             __syncthreads();
         }
-        for (uint32_t q = w.id; q < c.sq.n; q += w.count) weigh_seq(c, q, 256);
+        for (uint32_t q = threadIdx.x; q < c.sq.n; q += NT) weigh_seq<false>(c, q, 256);
         __syncthreads();
         return 0.0;
     }
@@ -603,7 +623,7 @@ __global__ __launch_bounds__(kLossNT) void k_count_by_seq(Weights c, uint32_t sp
 }
 __global__ __launch_bounds__(kLossNT) void k_weigh_seqs(Weights c) {
     const Wave w;
-    for (uint32_t q = w.id; q < c.sq.n; q += w.count) weigh_seq(c, q, 256 * kSpanG);
+    for (uint32_t q = w.id; q < c.sq.n; q += w.count) weigh_seq<true>(c, q, 256 * kSpanG);
 }
 __global__ __launch_bounds__(kLossNT) void k_count(Weights c, uint32_t spans) {
     __shared__ int red[kLossNT / 64];

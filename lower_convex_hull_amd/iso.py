@@ -400,7 +400,7 @@ class _Launch:
         if not lead.is_cuda:
             raise TypeError("the tensors must be CUDA tensors")
         self.torch, self.dev, self.index = torch, lead.device, lead.get_device()
-        if self.index != torch.cuda.current_device():
+        if self.index != torch._C._cuda_getDevice():
             raise ValueError("the tensors must be on the current device")
         current = torch._C._cuda_getCurrentRawStream(self.index)
         self.handle = current if stream is None else stream.cuda_stream
