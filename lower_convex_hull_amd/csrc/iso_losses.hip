@@ -16,7 +16,7 @@ constexpr int kTermG = 2;           // the same where the policy's terms are com
 constexpr int64_t kGrid = 1024;     // workgroups over spans: four a CU
 constexpr int kTermWaves = 4;       // waves a SIMD holds of them
 constexpr int kOneNT = 1024;        // the one workgroup of a small call, whose spans are one group
-constexpr int64_t kOneMax = 4096;  // tokens (and sequences) up to which one workgroup takes the whole call
+constexpr int64_t kOneMax = 8192;  // tokens (and sequences) up to which one workgroup takes the whole call
 
 // A span of G groups and a lane's tokens of it: group g holds tokens at(g) .. at(g)+3.
 template <int G>

@@ -78,7 +78,7 @@ def test_rows_at_the_borders(torch, name, vocab):
 
 
 @pytest.mark.parametrize("seq_mean,token_adv,norm", [(True, False, 0.0), (False, False, 0.0), (False, True, 0.0), (True, True, 3.5)])
-@pytest.mark.parametrize("rows,seqs", [(1, 1), (255, 200), (256, 256), (257, 256), (300, 500), (4096, 30), (4097, 11), (9000, 3000)])
+@pytest.mark.parametrize("rows,seqs", [(1, 1), (255, 200), (256, 256), (257, 256), (300, 500), (4097, 11), (8192, 30), (8193, 2000), (9000, 3000)])
 def test_rows_and_their_terms(torch, rows, seqs, seq_mean, token_adv, norm):
     """Rows' weights and advantages found by the row, by one workgroup, by many; sequences that are empty or ignored."""
     say(f"[losses] terms {rows}/{seqs} {seq_mean} {token_adv}")
@@ -99,7 +99,7 @@ def piles(rng, seqs, tokens, places):
     return np.concatenate([[0], np.sort(rng.choice(at, seqs - 1)), [tokens]]).astype(np.int32)
 
 
-@pytest.mark.parametrize("tokens", [3000, 4096, 4097, 30011])
+@pytest.mark.parametrize("tokens", [3000, 8192, 8193, 30011])
 @pytest.mark.parametrize("kind", ["piles", "ones", "one-long", "all-in-the-last"])
 def test_sequences_in_a_span(torch, kind, tokens):
     """More sequences in a span than a wave has lanes, most of them empty; one token each; one that takes nearly all."""
