@@ -11,10 +11,12 @@ namespace iso {
 namespace {
 
 constexpr int kLossNT = 256;        // threads of a workgroup over many tokens: four waves, a span each
-constexpr int kSpanG = 2;           // a wave's span: 2 groups of 256 tokens, 4 a lane in each
+constexpr int kSpanG = 1;           // a wave's span: groups of 256 tokens, 4 a lane in each
 constexpr int kTermG = 2;           // the same where the policy's terms are computed, which take more registers
-constexpr int64_t kGrid = 1024;     // workgroups over spans: four a CU
+constexpr int64_t kGrid = 2048;      // workgroups over spans: eight a CU
+constexpr int64_t kTermGrid = 1024;  // four a CU where they take more registers
 constexpr int kTermWaves = 4;       // waves a SIMD holds of them
+constexpr int64_t kWideSeqs = 256;  // pairs or sequences up to which each has a workgroup for its spans
 constexpr int kOneNT = 1024;        // the one workgroup of a small call, whose spans are one group
 constexpr int64_t kOneMax = 8192;  // tokens (and sequences) up to which one workgroup takes the whole call
 
@@ -241,6 +243,12 @@ struct PartSums {
     __device__ __forceinline__ Part by_wave(const Seqs& sq, uint32_t q, uint32_t size) const {
         const Part v = some(sq, q, size, threadIdx.x & 63, 64);
         return Part{wave_sum(v.sum), wave_sum(v.count)};
+    }
+    // by a workgroup, all threads together
+    template <int NT>
+    __device__ __forceinline__ Part by_group(const Seqs& sq, uint32_t q, uint32_t size, double* red) const {
+        const Part v = some(sq, q, size, threadIdx.x, NT);
+        return Part{wg_sum<NT>(v.sum, red), wg_sum<NT>(v.count, red)};
     }
     // by one thread: where a sequence has a few spans at most
     __device__ __forceinline__ Part by_lane(const Seqs& sq, uint32_t q, uint32_t size) const {
@@ -492,11 +500,18 @@ __global__ __launch_bounds__(kLossNT) void k_pref_sums(Pref p, uint32_t spans) {
     Cursor cur;
     w.each(spans, [&](uint32_t s) { pref_sums<kSpanG>(p, s, maps.mine(), cur); });
 }
+// A wave a pair, or (WIDE) a workgroup: few pairs can be long.
+template <bool WIDE>
 __global__ __launch_bounds__(kLossNT) void k_pref_pairs(Pref p) {
+    __shared__ double red[kLossNT / 64];
     const Wave w;
-    for (uint32_t i = w.id; i < p.pairs; i += w.count) {
-        const Part c = p.sums.by_wave(p.sq, 2 * i, 256 * kSpanG), r = p.sums.by_wave(p.sq, 2 * i + 1, 256 * kSpanG);
-        if ((threadIdx.x & 63) == 0) pref_pair(p, i, c, r);
+    for (uint32_t i = WIDE ? blockIdx.x : w.id; i < p.pairs; i += WIDE ? gridDim.x : w.count) {
+        Part v[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            v[k] = WIDE ? p.sums.by_group<kLossNT>(p.sq, 2 * i + k, 256 * kSpanG, red)
+                        : p.sums.by_wave(p.sq, 2 * i + k, 256 * kSpanG);
+        if ((WIDE ? threadIdx.x : threadIdx.x & 63) == 0) pref_pair(p, i, v[0], v[1]);
     }
 }
 // The first workgroup takes the mean of the pair losses, the others the tokens.
@@ -573,14 +588,9 @@ __device__ __forceinline__ void count_by_seq(const Weights& c, uint32_t span, in
     const Ids<G> s = seq_ids(c.sq, w, map, cur);
     sum_span<G, false>(w, span, s, nullptr, live, c.sums);
 }
-// Sequence q's weight, from the count of its tokens that take part: by a wave,
-// or by one thread.
-template <bool WAVE>
-__device__ __forceinline__ void weigh_seq(const Weights& c, uint32_t q, uint32_t size) {
-    const double n = c.live.all() ? (double)(c.sq.end(q) - c.sq.begin(q))
-                     : WAVE       ? c.sums.by_wave(c.sq, q, size).count
-                                  : c.sums.by_lane(c.sq, q, size).count;
-    if (!WAVE || (threadIdx.x & 63) == 0) c.weight[q] = c.p.seq_weight(c.sq.n, n);
+// Sequence q's weight, from the count of its tokens that take part.
+__device__ __forceinline__ void weigh_seq(const Weights& c, uint32_t q, double count) {
+    c.weight[q] = c.p.seq_weight(c.sq.n, c.live.all() ? (double)(c.sq.end(q) - c.sq.begin(q)) : count);
 }
 
 // The weight that all tokens share, for every thread of a workgroup: from the
@@ -605,7 +615,8 @@ __device__ __forceinline__ double small_weights(const Weights& c, uint32_t spans
             w.each(spans, [&](uint32_t s) { count_by_seq<1>(c, s, map, cur); });
             __syncthreads();
         }
-        for (uint32_t q = threadIdx.x; q < c.sq.n; q += NT) weigh_seq<false>(c, q, 256);
+        for (uint32_t q = threadIdx.x; q < c.sq.n; q += NT)
+            weigh_seq(c, q, c.live.all() ? 0.0 : c.sums.by_lane(c.sq, q, 256).count);
         __syncthreads();
         return 0.0;
     }
@@ -621,9 +632,20 @@ __global__ __launch_bounds__(kLossNT) void k_count_by_seq(Weights c, uint32_t sp
     Cursor cur;
     w.each(spans, [&](uint32_t s) { count_by_seq<kSpanG>(c, s, maps.mine(), cur); });
 }
+// A thread a sequence where every token takes part, else a wave, or (WIDE) a workgroup.
+template <bool WIDE>
 __global__ __launch_bounds__(kLossNT) void k_weigh_seqs(Weights c) {
+    __shared__ double red[kLossNT / 64];
+    if (c.live.all()) {
+        for (uint32_t q = blockIdx.x * kLossNT + threadIdx.x; q < c.sq.n; q += gridDim.x * kLossNT) weigh_seq(c, q, 0.0);
+        return;
+    }
     const Wave w;
-    for (uint32_t q = w.id; q < c.sq.n; q += w.count) weigh_seq<true>(c, q, 256 * kSpanG);
+    for (uint32_t q = WIDE ? blockIdx.x : w.id; q < c.sq.n; q += WIDE ? gridDim.x : w.count) {
+        const double n = WIDE ? c.sums.by_group<kLossNT>(c.sq, q, 256 * kSpanG, red).count
+                              : c.sums.by_wave(c.sq, q, 256 * kSpanG).count;
+        if ((WIDE ? threadIdx.x : threadIdx.x & 63) == 0) weigh_seq(c, q, n);
+    }
 }
 __global__ __launch_bounds__(kLossNT) void k_count(Weights c, uint32_t spans) {
     __shared__ int red[kLossNT / 64];
@@ -852,7 +874,8 @@ void start_weights(Weights& c, hipStream_t st) {
     const dim3 nt(kLossNT);
     if (c.p.seq_mean) {
         if (!c.live.all()) hipLaunchKernelGGL(k_count_by_seq, wave_grid(spans), nt, 0, st, c, spans);
-        hipLaunchKernelGGL(k_weigh_seqs, wave_grid(c.sq.n, 65536), nt, 0, st, c);
+        if (c.sq.n <= kWideSeqs) hipLaunchKernelGGL((k_weigh_seqs<true>), dim3(c.sq.n ? c.sq.n : 1), nt, 0, st, c);
+        else hipLaunchKernelGGL((k_weigh_seqs<false>), wave_grid(c.sq.n, 65536), nt, 0, st, c);
     } else if (!c.live.all()) {
         const dim3 grid = wave_grid(spans, kCountGrid);
         c.parts = grid.x;
@@ -864,7 +887,7 @@ struct PolicyPlan {
     WeightsPlan w;
     size_t off_part, bytes;
     PolicyPlan(int64_t tokens, int64_t seqs) : w(tokens, seqs) {
-        off_part = w.t.take((int64_t)wave_grid(spans_of(tokens, kTermG)).x, sizeof(PolicySums));
+        off_part = w.t.take((int64_t)wave_grid(spans_of(tokens, kTermG), kTermGrid).x, sizeof(PolicySums));
         bytes = w.t.at;
     }
 };
@@ -987,7 +1010,8 @@ int iso_pref_loss(const float* logp, const float* ref_logp, const uint8_t* mask,
     const dim3 nt(kLossNT);
     const uint32_t spans = spans_of(tokens, kSpanG);
     hipLaunchKernelGGL(k_pref_sums, wave_grid(spans), nt, 0, st, p, spans);
-    hipLaunchKernelGGL(k_pref_pairs, wave_grid(pairs, 65536), nt, 0, st, p);
+    if (pairs <= kWideSeqs) hipLaunchKernelGGL((k_pref_pairs<true>), dim3((unsigned)(pairs ? pairs : 1)), nt, 0, st, p);
+    else hipLaunchKernelGGL((k_pref_pairs<false>), wave_grid(pairs, 65536), nt, 0, st, p);
     hipLaunchKernelGGL(k_pref_grad, dim3(grad ? wave_grid(spans).x + 1 : 1), nt, 0, st, p, spans);
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
@@ -1030,7 +1054,7 @@ int iso_policy_loss(const float* logp, const float* old_logp, const float* ref_l
     }
     start_weights(f.c, st);
     const uint32_t spans = spans_of(tokens, kTermG);
-    const dim3 grid = wave_grid(spans);
+    const dim3 grid = wave_grid(spans, kTermGrid);
     by_kind(p, [&](auto k) {
         hipLaunchKernelGGL((k_policy_tokens<decltype(k)>), grid, dim3(kLossNT), 0, st, f, spans);
     });
