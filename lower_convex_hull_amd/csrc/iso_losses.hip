@@ -70,7 +70,7 @@ __device__ __forceinline__ void store4(float* __restrict__ p, uint32_t t, uint32
         Float4 x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = v[i];
-        *reinterpret_cast<Float4*>(p + t) = x;
+        __builtin_nontemporal_store(x, reinterpret_cast<Float4*>(p + t));  // not left to the kernel end to write back
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
