@@ -22,9 +22,14 @@ struct Wide {
     typedef T A __attribute__((ext_vector_type(16 / sizeof(T))));  // aligned, in LDS
 };
 
-template <typename T>
+// STREAM: without a place in the caches, for logits that do not fit them anyway
+// (8192 x 65536 bf16 forward 145 -> 133 us); smaller ones may still be there
+// from the call before (300 x 30000 f32 backward: 12.3 us, streamed 13.8).
+template <bool STREAM, typename T>
 __device__ __forceinline__ typename Wide<T>::V load_wide(const T* p) {
-    return *reinterpret_cast<const typename Wide<T>::V*>(p);
+    const auto* v = reinterpret_cast<const typename Wide<T>::V*>(p);
+    if constexpr (STREAM) return __builtin_nontemporal_load(v);
+    else return *v;
 }
 
 // exp((x - m)/T) = exp2((x - m) c), c = log2(e)/T.  The difference to the
@@ -109,17 +114,18 @@ struct Chunk {
     static constexpr int kSize = NT * U * N;
     typename Wide<T>::V v[U];
     __device__ __forceinline__ static int at(int k, int u) { return k + u * NT * N + (int)threadIdx.x * N; }
+    template <bool STREAM = false>
     __device__ __forceinline__ void load(const T* x, int k, int k1) {
         const T* b = x + k;
         if (k1 - k >= kSize) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = load_wide<T>(b + u * NT * N + threadIdx.x * N);
+            for (int u = 0; u < U; ++u) v[u] = load_wide<STREAM>(b + u * NT * N + threadIdx.x * N);
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) v[u][i] = (T)-INFINITY;
-                if (at(k, u) < k1) v[u] = load_wide<T>(b + u * NT * N + threadIdx.x * N);
+                if (at(k, u) < k1) v[u] = load_wide<STREAM>(b + u * NT * N + threadIdx.x * N);
             }
         }
     }
@@ -206,12 +212,12 @@ struct Running {
 };
 
 // The statistics of a piece of a row by a workgroup of NT threads; thread 0 has them.
-template <typename T, bool ENT, int NT, int U>
+template <bool STREAM, typename T, bool ENT, int NT, int U>
 __device__ __forceinline__ Stat row_stat(const T* __restrict__ x, const Piece<T>& w, const Scale& sc, Stat* part) {
     Running<T, ENT, NT, U> run;
     for (int k = w.from; k < w.to; k += Chunk<T, NT, U>::kSize) {
         Chunk<T, NT, U> c;
-        c.load(x, k, w.to);
+        c.template load<STREAM>(x, k, w.to);
         run.add(c, sc);
     }
     const int k = w.edge();
@@ -254,7 +260,7 @@ inline dim3 grid_of(int64_t items) { return dim3((unsigned)(items < kMaxGrid ? i
 
 // Item = (row, part of it).  With one part a row its outputs are written, else
 // the part's statistics.
-template <typename T, bool ENT, int NT>
+template <typename T, bool ENT, int NT, bool STREAM>
 __global__ __launch_bounds__(NT) void k_token_logp(const T* __restrict__ logits, int64_t rows, int vocab,
                                                    int64_t ld, const int32_t* __restrict__ target, Scale sc,
                                                    int splits, int chunk, LogpOut o, Stat* __restrict__ parts) {
@@ -265,7 +271,7 @@ __global__ __launch_bounds__(NT) void k_token_logp(const T* __restrict__ logits,
         const T* x = logits + r * ld;
         Stat a{};
         if (j >= 0) {
-            a = row_stat<T, ENT, NT, 4>(x, Piece<T>(x, (int)(item - r * splits), chunk, vocab), sc, part);
+            a = row_stat<STREAM, T, ENT, NT, 4>(x, Piece<T>(x, (int)(item - r * splits), chunk, vocab), sc, part);
         }
         if (threadIdx.x == 0) {
             if (splits == 1) write_row(o, r, x, j, vocab, sc.inv_t, a);
@@ -386,7 +392,7 @@ __device__ __forceinline__ void fill_row(T* o, const Piece<T>& w, T v) {
 constexpr int kVjpNT = 256, kVjpU = 2;
 
 // Item = (row, chunk of it).
-template <typename T, bool ENT>
+template <typename T, bool ENT, bool STREAM>
 __global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t rows, int vocab, int64_t ld,
                                                      const int32_t* __restrict__ target, double inv_t,
                                                      double temperature, float cf, int splits, int chunk,
@@ -407,7 +413,7 @@ __global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t ro
                                    ENT ? (double)g_ent[r] : 0.0, inv_t, temperature);
         for (int k = w.from; k < w.to; k += Chunk<T, kVjpNT, kVjpU>::kSize) {
             Chunk<T, kVjpNT, kVjpU> c;
-            c.load(x, k, w.to);
+            c.template load<STREAM>(x, k, w.to);
             store_grads<T, ENT>(c, o, k, w.to, j, q, cf);
         }
         store_edge<T, ENT>(x, o, w.edge(), j, q, cf);
@@ -559,6 +565,10 @@ LogpPlan logp_plan(int64_t rows, int64_t vocab, int dtype) {
     return p;
 }
 
+// Logits past half of the last-level cache (256 MB).
+template <typename T>
+bool streamed(int64_t rows, int64_t vocab) { return rows * vocab * (int64_t)sizeof(T) > 128 << 20; }
+
 Scale scale_of(double temperature) {
     const double c = kLog2e / temperature;
     const float near = (float)c;
@@ -572,15 +582,17 @@ void start_logp_t(const T* x, int64_t rows, int64_t vocab, int64_t ld, const int
                   const LogpOut& o, const LogpPlan& pl, void* workspace, hipStream_t st) {
     const Scale sc = scale_of(temperature);
     Stat* parts = static_cast<Stat*>(workspace);
-    auto start = [&](auto nt) {
+    auto start = [&](auto nt, auto stream) {
         constexpr int NT = decltype(nt)::value;
-        hipLaunchKernelGGL((k_token_logp<T, ENT, NT>), grid_of(rows * pl.splits), dim3(NT), 0, st, x, rows, (int)vocab,
+        hipLaunchKernelGGL((k_token_logp<T, ENT, NT, decltype(stream)::value>), grid_of(rows * pl.splits), dim3(NT), 0, st, x, rows, (int)vocab,
                            ld, target, sc, pl.splits, (int)pl.chunk, o, parts);
     };
-    if (pl.threads == 64) start(std::integral_constant<int, 64>{});
-    else if (pl.threads == 256) start(std::integral_constant<int, 256>{});
-    else if (pl.threads == 512) start(std::integral_constant<int, 512>{});
-    else start(std::integral_constant<int, 1024>{});
+    // so many logits have workgroups of 256
+    if (pl.threads == 64) start(std::integral_constant<int, 64>{}, std::false_type{});
+    else if (pl.threads == 256 && streamed<T>(rows, vocab)) start(std::integral_constant<int, 256>{}, std::true_type{});
+    else if (pl.threads == 256) start(std::integral_constant<int, 256>{}, std::false_type{});
+    else if (pl.threads == 512) start(std::integral_constant<int, 512>{}, std::false_type{});
+    else start(std::integral_constant<int, 1024>{}, std::false_type{});
     if (pl.splits > 1)
         hipLaunchKernelGGL((k_token_logp_join<T, ENT>), grid_of((rows + kJoinNT / 64 - 1) / (kJoinNT / 64)),
                            dim3(kJoinNT), 0, st, x, rows, (int)vocab, ld, target, sc, pl.splits, parts, o);
@@ -604,12 +616,17 @@ void start_vjp(const void* logits, int64_t rows, int64_t vocab, int64_t ld, cons
     const int chunk = kVjpU * kVjpNT * Wide<T>::N;
     const int splits = (int)((vocab + chunk - 1) / chunk);
     const dim3 grid = grid_of(rows * splits), nt(kVjpNT);
-    if (g_ent)
-        hipLaunchKernelGGL((k_logp_vjp<T, true>), grid, nt, 0, st, x, rows, (int)vocab, ld, target, sc.inv_t,
-                           temperature, sc.near, splits, chunk, lse, ent, g_logp, g_ent, o, ldg);
-    else
-        hipLaunchKernelGGL((k_logp_vjp<T, false>), grid, nt, 0, st, x, rows, (int)vocab, ld, target, sc.inv_t,
-                           temperature, sc.near, splits, chunk, lse, ent, g_logp, g_ent, o, ldg);
+    auto start = [&](auto ent_on, auto stream) {
+        hipLaunchKernelGGL((k_logp_vjp<T, decltype(ent_on)::value, decltype(stream)::value>), grid, nt, 0, st, x, rows,
+                           (int)vocab, ld, target, sc.inv_t, temperature, sc.near, splits, chunk, lse, ent, g_logp,
+                           g_ent, o, ldg);
+    };
+    auto by_ent = [&](auto stream) {
+        if (g_ent) start(std::true_type{}, stream);
+        else start(std::false_type{}, stream);
+    };
+    if (streamed<T>(rows, vocab)) by_ent(std::true_type{});
+    else by_ent(std::false_type{});
 }
 
 // f called with a value of the logits' type.
