@@ -93,6 +93,28 @@ def test_rows_and_their_terms(torch, rows, seqs, seq_mean, token_adv, norm):
         head_case(torch, logits, target, x, 5, (np.arange(6) * (rows // 5)).astype(np.int32), rows, seq_mean, token_adv=token_adv)
 
 
+@pytest.mark.parametrize("name,rows,vocab", [("f32", 700, 50021), ("bf16", 1100, 65536), ("f16", 9000, 9001)])
+def test_more_logits_than_the_cache_holds(torch, name, rows, vocab):
+    """More than 128 MB: every row agrees with the calls on its own block of rows, and some with the oracle."""
+    say(f"[losses] large {name} {rows}x{vocab}")
+    dtype = dtype_of(torch, name)
+    gen = torch.Generator(device="cuda").manual_seed(vocab)
+    logits = (torch.randn(rows, vocab, generator=gen, device="cuda") * 2).to(dtype)
+    target = torch.randint(0, vocab, (rows,), generator=gen, device="cuda").to(torch.int32)
+    target[rows // 3] = -1
+    g = torch.randn(rows, generator=gen, device="cuda")
+    lp, lse, ent = iso.token_logp(logits, target, entropy=True)
+    grad = iso.token_logp_vjp(g, logits, target, lse, entropy=ent, g_entropy=g)
+    pick = torch.tensor([0, 1, rows // 3, rows // 2, rows - 2, rows - 1], device="cuda")
+    x, t = logits[pick], target[pick]
+    xn = x.double().cpu().numpy()
+    check_logp(torch, (lp[pick], lse[pick], ent[pick]), xn, t.cpu(), 1.0)
+    check_vjp(torch, grad[pick], xn, t.cpu(), lse[pick], g[pick], ent[pick], g[pick], 1.0, dtype)
+    part = slice(rows // 4, rows // 4 + 100)  # a small call's gradient is the same elements' arithmetic
+    small = iso.token_logp_vjp(g[part], logits[part], target[part], lse[part], entropy=ent[part], g_entropy=g[part])
+    assert torch.equal(small, grad[part])
+
+
 def piles(rng, seqs, tokens, places):
     """Offsets that fall on few places: many sequences are empty, hundreds begin at one token."""
     at = np.sort(rng.integers(0, tokens + 1, places))
