@@ -441,7 +441,7 @@ __global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t 
     __shared__ Stat part[NT / 64];
     __shared__ double of_row[2];  // log-sum, gradient of the token's logp
     __shared__ PolicySums total;  // thread 0's
-    constexpr bool kKeep = NT * U >= 4096;
+    constexpr bool kKeep = NT * U >= 1024;
     __shared__ typename Wide<T>::A keep[kKeep ? NT * U : 1];
     if (threadIdx.x == 0) total = PolicySums{0.0, 0.0, 0, 0};
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
@@ -645,7 +645,17 @@ void by_dtype(int dtype, F f) {
 // Workspace and grid of iso_policy_loss_logits.
 constexpr int64_t kHeadGrid = 8192;
 constexpr int64_t kOwnTerms = 256;  // rows and sequences up to which a row's workgroup finds its term itself
-constexpr int64_t kHeadWide = 232 << 10, kHeadMid = 40 << 10, kHeadNarrow = 8 << 10;  // bytes of a row
+// A row's workgroup, by the bytes of a row.  A workgroup holds two chunks on
+// chip (registers and LDS); the fewer threads it has, the more rows a CU has in
+// flight, one reading while another writes.
+//   1024 x 8 vectors (2 x 128 KB, one row a CU): 4096 x 131072 bf16 370 us, 385 with 512
+//   512 x 8 (2 x 64 KB, two rows): 3000 x 101574 f16 253 us, 288 with 1024, 286 with 256
+//   256 x 8 (2 x 32 KB, four rows), many rows: 2000 x 25000 bf16 51 us, 57 with 512
+//     (37 x 32003 f16: 14.7 us, 12.9 with 512)
+//   256 x 4 (2 x 16 KB): 4096 x 16384 bf16 61 us, 72 with 512 x 8
+//   64 x 4: 4000 x 1500 bf16 19 us, 30 with 256 x 4
+constexpr int64_t kHeadWide = 232 << 10, kHeadFull = 96 << 10, kHeadMid = 40 << 10, kHeadNarrow = 8 << 10;
+constexpr int64_t kHeadRows = 512;  // many rows: two a CU
 struct HeadPlan {
     int grid;
     size_t off_terms, off_sums, off_weights, bytes;
@@ -676,7 +686,8 @@ void start_rows(const void* logits, int64_t rows, int64_t vocab, int64_t ld, con
     typedef std::integral_constant<int, 4> Four;
     typedef std::integral_constant<int, 8> Eight;
     if (bytes > kHeadWide) start(std::integral_constant<int, 1024>{}, Eight{});
-    else if (bytes > kHeadMid) start(std::integral_constant<int, 512>{}, Eight{});
+    else if (bytes > kHeadFull || (bytes > kHeadMid && rows <= kHeadRows)) start(std::integral_constant<int, 512>{}, Eight{});
+    else if (bytes > kHeadMid) start(std::integral_constant<int, 256>{}, Eight{});
     else if (bytes > kHeadNarrow) start(std::integral_constant<int, 256>{}, Four{});
     else start(std::integral_constant<int, 64>{}, Four{});
 }
