@@ -10,15 +10,23 @@
 namespace iso {
 namespace {
 
-constexpr int kLossNT = 256;        // threads of a workgroup over many tokens: four waves, a span each
-constexpr int kSpanG = 1;           // a wave's span: groups of 256 tokens, 4 a lane in each
-constexpr int kTermG = 2;           // the same where the policy's terms are computed, which take more registers
-constexpr int64_t kGrid = 2048;      // workgroups over spans: eight a CU
-constexpr int64_t kTermGrid = 1024;  // four a CU where they take more registers
-constexpr int kTermWaves = 4;       // waves a SIMD holds of them
-constexpr int64_t kWideSeqs = 256;  // pairs or sequences up to which each has a workgroup for its spans
-constexpr int kOneNT = 1024;        // the one workgroup of a small call, whose spans are one group
-constexpr int64_t kOneMax = 8192;  // tokens (and sequences) up to which one workgroup takes the whole call
+constexpr int kLossNT = 256;  // threads of a workgroup over many tokens: four waves
+// A wave's span, in groups of 256 tokens (4 a lane in each): 1 for the sums and
+// the preference gradient (64 pairs of 20000 tokens: 12.0 us, 13.1 with 2), 2 for the
+// policy's terms, whose registers leave no room for more.
+constexpr int kSpanG = 1, kTermG = 2;
+// Workgroups over spans, eight a CU, four where they take more registers
+// (policy loss of 8e6 tokens: 58 us, 60 with four throughout, 66 with one span a wave).
+constexpr int64_t kGrid = 2048, kTermGrid = 1024;
+constexpr int kTermWaves = 4;  // waves a SIMD holds of them
+// Pairs or sequences up to which each has a workgroup for its spans, else a wave:
+// few can be long (2 pairs of 2e6 tokens: 17 us, 22 with waves).
+constexpr int64_t kWideSeqs = 256;
+// Up to this many tokens and sequences one workgroup takes the whole call, in
+// spans of one group (6000 tokens in 16 pairs: 10.1 us, 12.1 in three launches; at
+// 12000 13.1 and 12.3).
+constexpr int kOneNT = 1024;
+constexpr int64_t kOneMax = 8192;
 
 // A span of G groups and a lane's tokens of it: group g holds tokens at(g) .. at(g)+3.
 template <int G>
@@ -500,6 +508,8 @@ __global__ __launch_bounds__(kLossNT) void k_pref_sums(Pref p, uint32_t spans) {
     Cursor cur;
     w.each(spans, [&](uint32_t s) { pref_sums<kSpanG>(p, s, maps.mine(), cur); });
 }
+// 4e6 tokens in 1000 pairs: sums 11 us (28 MB read), pairs 5, gradient 7 (16 MB
+// written), each launch about 3 of them.
 // A wave a pair, or (WIDE) a workgroup: few pairs can be long.
 template <bool WIDE>
 __global__ __launch_bounds__(kLossNT) void k_pref_pairs(Pref p) {
@@ -770,6 +780,11 @@ __device__ __forceinline__ void policy_out(double kl_coef, const PolicySums& s, 
     counts[1] = s.over;
 }
 
+// Bound by its f64 instructions: 8e6 tokens take 10.9e6 wave instructions (18 of
+// 35 us of every SIMD's issue at 2.4 GHz; two thirds of the time that waves live)
+// for 103 MB read and 32 MB written.  More waves (5, 6, 8 a SIMD) spill, spans
+// of 256 or 1024 tokens were 12 and 30 % slower, and loads issued a span ahead
+// brought nothing.
 template <typename K>
 __global__ __launch_bounds__(kLossNT, kTermWaves) void k_policy_tokens(PolicyCall f, uint32_t spans) {
     __shared__ Maps<kLossNT, kTermG> maps;
