@@ -1,7 +1,7 @@
 // Token log-probabilities from logits, their backward pass, and the policy loss
 // taken from the logits (formulas in iso.h).  A row of logits is one token's;
-// logits are f32, f16 or bf16 and everything is computed in f32 from the
-// difference to the row's maximum (exact, or nearly, in f32), joined in f64.
+// logits are f32, f16 or bf16; terms are computed in f32 from the difference to
+// the maximum (exact, or nearly, in f32), and summed in f64.
 #include "../../include/iso.h"
 #include "iso_losses.hpp"
 
@@ -37,11 +37,7 @@ __device__ __forceinline__ typename Wide<T>::V load_wide(const T* p) {
 // term counts, the largest term is exactly 1, and no finite logit overflows.
 struct Scale {
     double inv_t, c;
-    float cf, rest;  // c rounded down to f32, and what that leaves off (> 0: -infinity stays -infinity)
-    float near;      // c in f32, for single terms
-    // An exponent.  All terms of a sum carry the rounding of c alike, so it is
-    // taken back: 1.5e-7 of lse at 32768 logits.
-    __device__ __forceinline__ float times(float d) const { return fmaf(d, rest, d * cf); }
+    float cf;  // c in f32
 };
 
 // The maximum that differences are taken to: 0 where everything so far is
@@ -151,9 +147,11 @@ struct Chunk {
     }
 };
 
-// A thread's running statistics.  A chunk adds its maximum first, then its sums
-// in f32 (U*8 terms at most), joined in f64 to the sums so far, which are
-// scaled when the maximum rises.
+// A thread's running statistics.  A chunk adds its maximum first, then its sums,
+// to those so far, which are scaled when the maximum rises.  Terms are f32, their
+// sum f64: where one term is nearly all, logp is what the small ones add to its
+// 1, and f32 additions to 1 lost up to 2e-5 of it (3e-7 is left).  The extra
+// instruction an element costs 2 % where rows stay on chip and nothing elsewhere.
 // LEAN: the chunk's values are kept on (a row's gradient takes them again), and
 // their f32 forms are made twice rather than held; else held (8192 x 65536 bf16:
 // 127 us, 132 lean).
@@ -170,25 +168,26 @@ struct Running {
             for (int i = 0; i < N; ++i) bm = fmaxf(bm, (float)c.v[u][i]);
         if (bm > m) {
             if (m != -INFINITY) {
-                const float d = held(sc.times(m - bm)), f = __builtin_amdgcn_exp2f(d);
+                const float d = held((m - bm) * sc.cf), f = __builtin_amdgcn_exp2f(d);
                 if (ENT) h = (h + s * (double)d) * (double)f;
                 s *= (double)f;
             }
             m = bm;
         }
         const float base = base_of(m);
-        float fs = 0.0f, fh = 0.0f;
+        double fs = 0.0;
+        float fh = 0.0f;
         if (LEAN) c.forget();
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float a = sc.times((float)c.v[u][i] - base);
+                const float a = ((float)c.v[u][i] - base) * sc.cf;
                 const float e = __builtin_amdgcn_exp2f(a);
-                fs += e;
+                fs += (double)e;
                 if (ENT) fh = fmaf(e, held(a), fh);
             }
-        s += (double)fs;
+        s += fs;
         if (ENT) h += (double)fh;
     }
     // One more value, of those that whole vectors leave over.
@@ -198,7 +197,7 @@ struct Running {
             rebase<ENT>(a, (double)x, sc);
             m = x;
         }
-        const float d = sc.times(x - base_of(m)), e = __builtin_amdgcn_exp2f(d);
+        const float d = (x - base_of(m)) * sc.cf, e = __builtin_amdgcn_exp2f(d);
         s = a.s + (double)e;
         if (ENT) h = a.h + (double)(e * held(d));
     }
@@ -504,11 +503,11 @@ __global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t 
         __syncthreads();
         if (grad && j < vocab) {
             const RowGrad q = row_grad(of_row[0], of_row[1], 0.0, 0.0, sc.inv_t, temperature);
-            store_edge<T, false>(x, o, edge, j, q, sc.near);
+            store_edge<T, false>(x, o, edge, j, q, sc.cf);
             // the last chunk is still in registers, the others follow backwards
             for (e = w.to;;) {
                 k = max(e - C::kSize, w.from);
-                store_grads<T, false>(c, o, k, e, j, q, sc.near);
+                store_grads<T, false>(c, o, k, e, j, q, sc.cf);
                 if (k == w.from) break;
                 e = k;
                 if (kKeep && e + C::kSize == w.to) c.take(keep);
@@ -588,10 +587,7 @@ bool streamed(int64_t rows, int64_t vocab) { return rows * vocab * (int64_t)size
 
 Scale scale_of(double temperature) {
     const double c = kLog2e / temperature;
-    const float near = (float)c;
-    float cf = near;
-    if ((double)cf > c) cf = nextafterf(cf, 0.0f);
-    return Scale{1.0 / temperature, c, cf, fmaxf((float)(c - (double)cf), 1e-30f), near};
+    return Scale{1.0 / temperature, c, (float)c};
 }
 
 template <typename T, bool ENT>
@@ -635,7 +631,7 @@ void start_vjp(const void* logits, int64_t rows, int64_t vocab, int64_t ld, cons
     const dim3 grid = grid_of(rows * splits), nt(kVjpNT);
     auto start = [&](auto ent_on, auto stream) {
         hipLaunchKernelGGL((k_logp_vjp<T, decltype(ent_on)::value, decltype(stream)::value>), grid, nt, 0, st, x, rows,
-                           (int)vocab, ld, target, sc.inv_t, temperature, sc.near, splits, chunk, lse, ent, g_logp,
+                           (int)vocab, ld, target, sc.inv_t, temperature, sc.cf, splits, chunk, lse, ent, g_logp,
                            g_ent, o, ldg);
     };
     auto by_ent = [&](auto stream) {

@@ -115,6 +115,31 @@ def test_more_logits_than_the_cache_holds(torch, name, rows, vocab):
     assert torch.equal(small, grad[part])
 
 
+@pytest.mark.parametrize("vocab", [1000, 16385, 131072])
+@pytest.mark.parametrize("rows", [1, 40, 300])
+def test_confident_tokens(torch, rows, vocab):
+    """A target that takes nearly all: logp = -log(1 + r) keeps its relative accuracy.  The largest term is exactly 1 and
+    the sums are f64, so each other term's own roundings (its exponent's three, its exp's two half steps) and the output's
+    are all that is left."""
+    gen = torch.Generator().manual_seed(rows + vocab)
+    x = torch.randn(rows, vocab, generator=gen)
+    target = torch.randint(0, vocab, (rows,), generator=gen, dtype=torch.int32)
+    lift = math.log(vocab) + torch.linspace(2.0, 14.0, rows)
+    x[torch.arange(rows), target.long()] = lift
+    old = torch.zeros(rows, device="cuda")
+    got = iso.token_logp(x.cuda(), target.cuda())[0]
+    head = iso.policy_loss_logits(x.cuda(), target.cuda(), old, torch.ones(1, device="cuda"))[2]
+    for r in range(rows):
+        z = x[r].double().numpy()
+        z = z - z.max()
+        e = np.exp(z)
+        e[target[r]] = 0.0
+        want = -np.log1p(e.sum())
+        tol = U * (abs(want) + (e * (3 * np.abs(z) + 2)).sum())
+        for name, v in (("logp", got), ("head", head)):
+            assert abs(float(v[r]) - want) <= tol, (name, r, float(v[r]), want, tol)
+
+
 def piles(rng, seqs, tokens, places):
     """Offsets that fall on few places: many sequences are empty, hundreds begin at one token."""
     at = np.sort(rng.integers(0, tokens + 1, places))
