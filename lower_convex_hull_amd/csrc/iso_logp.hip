@@ -436,8 +436,8 @@ __global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t ro
 // statistics, its token's terms, and its gradient.  The last chunk of the row
 // stays in registers and the one before in LDS between the two; what a longer
 // row has before them is read again while the last-level cache may still have
-// it.  Bound by HBM: 4096 x 131072 bf16 reads each logit once (842 MB by the
-// counters) and writes 1.07 GB in 364 us, 5.3 TB/s, with half of the issue cycles
+// it.  Bound by HBM: 4096 x 131072 bf16 reads each logit once (862 MB by the
+// counters) and writes 1.07 GB in 373 us, 5.2 TB/s, with 60 % of the issue cycles
 // spent on VALU instructions; three passes over the logits took 596.  Every
 // row's weight and advantage depend on the targets alone and are known before
 // (terms), or (NULL; few rows) are found here, which saves a launch.
@@ -656,7 +656,7 @@ constexpr int64_t kOwnTerms = 256;  // rows and sequences up to which a row's wo
 // A row's workgroup, by the bytes of a row.  A workgroup holds two chunks on
 // chip (registers and LDS); the fewer threads it has, the more rows a CU has in
 // flight, one reading while another writes.
-//   1024 x 8 vectors (2 x 128 KB, one row a CU): 4096 x 131072 bf16 370 us, 385 with 512
+//   1024 x 8 vectors (2 x 128 KB, one row a CU): 4096 x 131072 bf16 375 us, 390 with 512
 //   512 x 8 (2 x 64 KB, two rows): 3000 x 101574 f16 253 us, 288 with 1024, 286 with 256
 //   256 x 8 (2 x 32 KB, four rows), many rows: 2000 x 25000 bf16 51 us, 57 with 512
 //     (37 x 32003 f16: 14.7 us, 12.9 with 512)

@@ -781,8 +781,8 @@ __device__ __forceinline__ void policy_out(double kl_coef, const PolicySums& s, 
 }
 
 // Bound by its f64 instructions: 8e6 tokens take 10.9e6 wave instructions (18 of
-// 35 us of every SIMD's issue at 2.4 GHz; two thirds of the time that waves live)
-// for 103 MB read and 32 MB written.  More waves (5, 6, 8 a SIMD) spill, spans
+// 36 us of every SIMD's issue at 2.4 GHz; two thirds of the time that waves live)
+// for 105 MB read and 32 MB written.  More waves (5, 6, 8 a SIMD) spill, spans
 // of 256 or 1024 tokens were 12 and 30 % slower, and loads issued a span ahead
 // brought nothing.
 template <typename K>
