@@ -159,11 +159,17 @@ struct MaxStep {
     template <int CTRL, int RM>
     __device__ __forceinline__ void step() { v = max(v, dpp<CTRL, RM>(0, v)); }
 };
-// A wave takes spans that follow each other, and looks for a span's first
-// sequence from the last one of the span before: 64 sequences in one load,
-// which mostly holds all that begin inside the span too.
+// A wave takes spans that follow each other.  Its lanes hold where the 64
+// sequences after q begin, in which a span's first sequence and those that begin
+// inside it are looked up; the window moves on when the spans have passed it.
 struct Cursor {
     uint32_t q = 0xffffffffu;  // one that begins at or before the next span, or none known
+    uint32_t b = 0;            // where sequence q + 1 + lane begins (none: 2^32 - 1)
+    __device__ __forceinline__ void look(const Seqs& sq, uint32_t at) {
+        q = at;
+        const uint32_t k = q + 1 + (threadIdx.x & 63);
+        b = k < sq.n ? sq.begin(k) : 0xffffffffu;
+    }
 };
 // Each sequence that begins inside the span marks its first token in `map`
 // (G * 256 words of the wave's own in LDS; the last one where some are empty);
@@ -172,33 +178,31 @@ struct Cursor {
 // sequences below n.
 template <int G>
 __device__ __forceinline__ Ids<G> seq_ids(const Seqs& sq, const Place<G>& w, int* map, Cursor& cur) {
-    auto begin_of = [&](uint32_t k) { return k < sq.n ? sq.begin(k) : 0xffffffffu; };
-    if (!sq.off) cur.q = w.p0 / sq.len;
-    else if (cur.q == 0xffffffffu) cur.q = sq.n <= 64 ? 0u : find_seq(sq, w.p0);
-    uint32_t k = cur.q + 1 + w.lane, b = begin_of(k);
-    uint32_t passed = (uint32_t)__popcll(__ballot(b <= w.p0));
+    if (!sq.off) cur.look(sq, w.p0 / sq.len);
+    else if (cur.q == 0xffffffffu) cur.look(sq, sq.n <= 64 ? 0u : find_seq(sq, w.p0));
+    uint32_t passed = (uint32_t)__popcll(__ballot(cur.b <= w.p0));
     if (passed == 64) {
-        cur.q = find_seq(sq, w.p0);
-        k = cur.q + 1 + w.lane;
-        b = begin_of(k);
-        passed = (uint32_t)__popcll(__ballot(b <= w.p0));
+        cur.look(sq, cur.q + 64);
+        passed = (uint32_t)__popcll(__ballot(cur.b <= w.p0));
+        if (passed == 64) {
+            cur.look(sq, find_seq(sq, w.p0));
+            passed = (uint32_t)__popcll(__ballot(cur.b <= w.p0));
+        }
     }
     Ids<G> s;
     s.q0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(cur.q + passed));
-    cur.q = s.q0;
 #pragma unroll
     for (int i = 0; i < 4 * G; ++i) s.id[i] = 0;
-    s.one = !__any(b > w.p0 && b < w.p1);
+    s.one = !__any(cur.b > w.p0 && cur.b < w.p1) && !__all(cur.b < w.p1);
     if (s.one) return s;
     int4* m = reinterpret_cast<int4*>(map);
 #pragma unroll
     for (int g = 0; g < G; ++g) m[g * 64 + w.lane] = make_int4(0, 0, 0, 0);
     wave_order();
     for (;;) {
-        if (b > w.p0 && b < w.p1) atomicMax(map + (b - w.p0), (int)(k - s.q0));
-        if (!__all(b < w.p1)) break;
-        k += 64;
-        b = begin_of(k);
+        if (cur.b > w.p0 && cur.b < w.p1) atomicMax(map + (cur.b - w.p0), (int)(cur.q + 1 + w.lane - s.q0));
+        if (!__all(cur.b < w.p1)) break;
+        cur.look(sq, cur.q + 64);
     }
     wave_order();
     int before = 0;
@@ -217,7 +221,6 @@ __device__ __forceinline__ Ids<G> seq_ids(const Seqs& sq, const Place<G>& w, int
         for (int i = 0; i < 4; ++i) id[i] = max(id[i], low);
         before = max(before, lane_value(x.v, 63));
     }
-    cur.q = s.q0 + (uint32_t)before;
     return s;
 }
 
