@@ -380,7 +380,8 @@ int iso_token_logp_vjp(const void* logits, int dtype, int64_t rows, int64_t voca
  *   the count of tokens, or of seqs (for sums over several calls).
  *   adv       [seqs] f32, or [tokens] with ISO_POLICY_ADV_TOKEN.
  *   clip_lo in [0, 1], clip_hi >= 0 (may be infinite), kl_coef finite (0
- *   without ref_logp).
+ *   without ref_logp; 0 with it: the reference is only watched, kl is summed into
+ *   loss[2] and reaches neither the loss nor its gradient, whatever it is).
  *   loss      [3] f32, written: the loss, its part sum w pg, and sum w kl.
  *   counts    [2] int32, written: unmasked tokens, and those the clip holds
  *             (A > 0 and d > log(1 + clip_hi), or A < 0 and

@@ -191,13 +191,17 @@ __device__ __forceinline__ void policy_terms(const Policy& p, const ExpSeries& e
     for (int i = 0; i < N; ++i) {
         r[i] = ex(d[i]);
         k[i] = REF ? ex(u[i]) : ExpTerms{1.0, 0.0, 0.0};
-        far |= (REF ? fmax(fabs(d[i]), fabs(u[i])) : fabs(d[i])) > ExpSeries::kFar;
+        far |= !((REF ? fabs(d[i]) + fabs(u[i]) : fabs(d[i])) <= ExpSeries::kFar);  // NaN too
     }
     if (far) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             ExpSeries::far(d[i], r[i]);
-            if (REF) ExpSeries::far(u[i], k[i]);
+            if (REF) {
+                ExpSeries::far(u[i], k[i]);
+                // a reference that is only watched: no infinity or NaN times 0 into the slope
+                if (p.kl_coef == 0.0) k[i].m1 = 0.0;
+            }
         }
     }
 #pragma unroll

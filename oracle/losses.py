@@ -132,8 +132,9 @@ def policy_loss(logp, old, ref, adv, mask, off, seqs, lo=0.2, hi=0.2, kl_coef=0.
             if ref is not None:
                 u = ref[at] - logp[at]
                 kl = np.expm1(u) - u
-                slope = slope - kl_coef * np.expm1(u)
-                move = move + abs(kl_coef) * np.exp(u)
+                if kl_coef:  # else the loss has no KL term, whatever u is
+                    slope = slope - kl_coef * np.expm1(u)
+                    move = move + abs(kl_coef) * np.exp(u)
         total += w * pg.sum(), w * kl.sum()
         over += int(held.sum())
         grad[at] = grad_scale * w * slope

@@ -1,0 +1,62 @@
+"""The losses where a product of 0 and infinity, a cancellation or a range decides:
+references that are only watched, advantages of 0, rows of one value, confident
+targets, temperatures and gradients at the ends of their range; and what tests of
+values do not show: streams, memory beside the outputs, arrays that begin anywhere.
+
+Tolerances are derived at each test; U is half a step of f32.
+"""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+
+from lower_convex_hull_amd import iso
+from oracle import losses
+from tests.test_gpu_losses import U, check_logp, check_vjp, dtype_of, floor_of, half, make, near, offsets, put, say, torch  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def far_reference(rng, logp):
+    """References whose u = ref - logp is beyond exp's range, infinite or NaN at some tokens."""
+    ref = (logp + rng.normal(0, 0.2, logp.size)).astype(np.float32)
+    at = rng.choice(logp.size, max(1, logp.size // 3), replace=False)
+    ref[at] = rng.choice([750.0, 1e30, np.inf, -np.inf, np.nan], at.size).astype(np.float32)
+    return ref
+
+
+@pytest.mark.parametrize("seqs,tokens", [(2, 7), (6, 777), (40, 20011)])
+@pytest.mark.parametrize("seq_mean", [False, True])
+def test_a_reference_that_is_only_watched(torch, seqs, tokens, seq_mean):
+    """kl_coef 0: the loss has no KL term, so the reference, whatever it holds,
+    leaves the loss and its gradient as they are without it, bit by bit."""
+    say(f"[losses] watched {seqs}x{tokens}")
+    rng = np.random.default_rng(tokens)
+    logp = -rng.exponential(1.0, tokens).astype(np.float32)
+    old = (logp + rng.normal(0, 0.25, tokens)).astype(np.float32)
+    logp[rng.choice(tokens, tokens // 5, replace=False)] = -np.inf  # a live token that the model cannot say
+    off, adv = put(torch, offsets(rng, seqs, tokens)), put(torch, rng.normal(size=seqs).astype(np.float32))
+    kw = dict(seq_off=off, seq_mean=seq_mean)
+    want = iso.policy_loss(put(torch, logp), put(torch, old), adv, **kw)
+    for ref in (far_reference(rng, logp), np.full(tokens, -1.0, np.float32)):
+        got = iso.policy_loss(put(torch, logp), put(torch, old), adv, ref_logp=put(torch, ref), **kw)
+        assert torch.equal(got[0][:2], want[0][:2]) and torch.equal(got[1], want[1])
+        assert not bool(torch.isnan(got[2]).any()) and torch.equal(got[2], want[2])
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+def test_a_reference_that_is_only_watched_from_logits(torch, name):
+    rng = np.random.default_rng(5)
+    logits, target, _, _ = make(torch, dtype_of(torch, name), 300, 517, 8)
+    rows = torch.arange(0, 300, 7, device="cuda")
+    at = target.cuda()
+    logits[rows[::2], at[rows[::2]].long()] = -math.inf
+    logits[rows[1::2], at[rows[1::2]].long()] = torch.finfo(logits.dtype).min
+    old, adv = put(torch, np.full(300, -4.0, np.float32)), put(torch, rng.normal(size=1).astype(np.float32))
+    want = iso.policy_loss_logits(logits, at, old, adv)
+    ref = put(torch, far_reference(rng, np.full(300, -4.0, np.float32)))
+    got = iso.policy_loss_logits(logits, at, old, adv, ref_logp=ref)
+    assert torch.equal(got[0][:2], want[0][:2]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    assert not bool(torch.isnan(got[3]).any()) and torch.equal(got[3], want[3])
