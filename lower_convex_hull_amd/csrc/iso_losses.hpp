@@ -197,6 +197,7 @@ __device__ __forceinline__ void policy_terms(const Policy& p, const ExpSeries& e
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             ExpSeries::far(d[i], r[i]);
+            if (a[i] == 0.0f && fabs(d[i]) < INFINITY) r[i].e = 1.0;  // r A is 0, also where r is beyond f64
             if (REF) {
                 ExpSeries::far(u[i], k[i]);
                 // a reference that is only watched: no infinity or NaN times 0 into the slope

@@ -122,6 +122,7 @@ def policy_loss(logp, old, ref, adv, mask, off, seqs, lo=0.2, hi=0.2, kl_coef=0.
         with np.errstate(over="ignore", invalid="ignore"):
             d = logp[at] - old[at]
             r = np.exp(d)
+            r = np.where((adv_q == 0) & np.isfinite(d), 1.0, r)  # r A is 0, also where r is beyond f64
             clipped = np.clip(r, 1 - lo, 1 + hi)
             pg = -np.where(r * adv_q <= clipped * adv_q, r * adv_q, clipped * adv_q)
             pg = np.where(np.isnan(r * adv_q), np.nan, pg)

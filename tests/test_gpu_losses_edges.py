@@ -60,3 +60,24 @@ def test_a_reference_that_is_only_watched_from_logits(torch, name):
     got = iso.policy_loss_logits(logits, at, old, adv, ref_logp=ref)
     assert torch.equal(got[0][:2], want[0][:2]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
     assert not bool(torch.isnan(got[3]).any()) and torch.equal(got[3], want[3])
+
+
+@pytest.mark.parametrize("seqs,tokens", [(4, 40), (40, 20011)])
+@pytest.mark.parametrize("clip_hi", [0.2, math.inf])
+def test_an_advantage_of_zero(torch, seqs, tokens, clip_hi):
+    """r A is 0 at A = 0 for every finite difference, also where r is beyond f64."""
+    rng = np.random.default_rng(tokens)
+    off, adv = offsets(rng, seqs, tokens), rng.normal(size=seqs).astype(np.float32)
+    adv[::2] = 0.0
+    logp = -rng.exponential(1.0, tokens).astype(np.float32)
+    old = (logp + rng.normal(0, 0.25, tokens)).astype(np.float32)
+    zero = np.repeat(adv == 0, np.diff(off))
+    old[zero] = rng.choice([-800.0, -705.0, -3e38, 3e38, -1.0], zero.sum()).astype(np.float32)
+    loss, counts, grad = iso.policy_loss(put(torch, logp), put(torch, old), put(torch, adv), seq_off=put(torch, off),
+                                         clip_hi=clip_hi)
+    f = lambda a: a.astype(np.float64)  # noqa: E731
+    w = losses.policy_loss(f(logp), f(old), None, f(adv), None, off, seqs, hi=clip_hi)
+    assert np.all(np.isfinite(w[0])) and np.all(w[2][zero] == 0)
+    near(loss, w[0], 100.0 * (1 + seqs))
+    near(grad, w[2], w[3] + 1e-3)
+    assert np.array_equal(counts.cpu().numpy(), w[1])

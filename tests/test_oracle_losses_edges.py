@@ -18,3 +18,13 @@ def test_a_reference_that_is_only_watched():
         assert np.all(np.isfinite(got[2]))
     with_term = losses.policy_loss(logp[1:2], old[1:2], np.array([-0.5]), adv[:1], None, None, 1, kl_coef=0.25)
     assert np.isclose(with_term[2][0], -0.5 - 0.25 * np.expm1(0.5), rtol=1e-14)
+
+
+def test_an_advantage_of_zero():
+    """r A is 0 at A = 0 for every finite difference, also where r is beyond f64."""
+    logp, old = np.full(5, -1.0), np.array([-800.0, -1e30, 1e30, -1.0, -1.5])
+    for hi in (0.2, np.inf):
+        loss, counts, grad, size = losses.policy_loss(logp, old, None, np.zeros(1), None, None, 1, hi=hi)
+        assert np.all(loss == 0) and np.all(grad == 0) and np.all(size == 0) and counts.tolist() == [5, 0]
+    loss, _, grad, _ = losses.policy_loss(logp, np.array([np.nan] * 5), None, np.zeros(1), None, None, 1)
+    assert np.isnan(loss[0]) and np.all(np.isnan(grad))
