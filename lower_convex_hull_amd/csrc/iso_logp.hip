@@ -315,11 +315,12 @@ __global__ __launch_bounds__(kJoinNT) void k_token_logp_join(const T* __restrict
 }
 
 // What a row's gradient takes: p = exp(x/T - lse) as exp2((x - mh) c) times a
-// factor of the row, mh = lse T rounded to f32 (the factor is what that
-// rounding leaves off), folded into a, b: gradient p (a + b (x - mh)).
+// factor of the row, folded into a, b: gradient p (a + b (x - mh)).
 struct RowGrad {
     float mh, a, b, hot;
 };
+// From a given log-sum: mh = lse T rounded to f32, the factor is what that
+// rounding leaves off.
 __device__ __forceinline__ RowGrad row_grad(double lse, double g, double ent, double g_ent, double inv_t,
                                             double temperature) {
     RowGrad o;
@@ -330,6 +331,12 @@ __device__ __forceinline__ RowGrad row_grad(double lse, double g, double ent, do
     o.b = (float)(-g_ent * inv_t * f);
     o.hot = (float)(g * inv_t);
     return o;
+}
+
+// From the row's own maximum and sum: 1/sum is the factor.  A log-sum of a row
+// of one huge value (a mask's lowest one) does not show log V any more.
+__device__ __forceinline__ RowGrad row_grad(const Stat& st, double g, double inv_t) {
+    return RowGrad{(float)st.m, (float)(-g * inv_t / st.s), 0.0f, (float)(g * inv_t)};
 }
 
 // An element's gradient (but for the target's own g/T).
@@ -443,14 +450,13 @@ __global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t ro
 // (terms), or (NULL; few rows) are found here, which saves a launch.
 template <typename T, int NT, int U>
 __global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t rows, int vocab, int64_t ld,
-                                                       const int32_t* __restrict__ target, Scale sc,
-                                                       double temperature, Policy p,
+                                                       const int32_t* __restrict__ target, Scale sc, Policy p,
                                                        const RowTerm* __restrict__ terms, Seqs sq,
                                                        float* __restrict__ logp, T* grad, int64_t ldg,
                                                        PolicySums* __restrict__ sums) {
     typedef Chunk<T, NT, U> C;
     __shared__ Stat part[NT / 64];
-    __shared__ double of_row[2];  // log-sum, gradient of the token's logp
+    __shared__ RowGrad of_row;
     __shared__ PolicySums total;  // thread 0's
     constexpr bool kKeep = NT * U >= 1024;
     __shared__ typename Wide<T>::A keep[kKeep ? NT * U : 1];
@@ -497,12 +503,11 @@ __global__ __launch_bounds__(NT, 4) void k_policy_rows(const T* logits, int64_t 
             total.kl += t.w * k1.kl;
             total.live += 1;
             total.over += k1.over ? 1 : 0;
-            of_row[0] = v.lse;
-            of_row[1] = k1.slope * (t.w * p.grad_scale);
+            of_row = row_grad(a, k1.slope * (t.w * p.grad_scale), sc.inv_t);
         }
         __syncthreads();
         if (grad && j < vocab) {
-            const RowGrad q = row_grad(of_row[0], of_row[1], 0.0, 0.0, sc.inv_t, temperature);
+            const RowGrad q = of_row;
             store_edge<T, false>(x, o, edge, j, q, sc.cf);
             // the last chunk is still in registers, the others follow backwards
             for (e = w.to;;) {
@@ -688,8 +693,8 @@ void start_rows(const void* logits, int64_t rows, int64_t vocab, int64_t ld, con
     const int64_t bytes = vocab * (int64_t)sizeof(T);
     auto start = [&](auto nt, auto u) {
         constexpr int NT = decltype(nt)::value, U = decltype(u)::value;
-        hipLaunchKernelGGL((k_policy_rows<T, NT, U>), dim3(grid), dim3(NT), 0, st, x, rows, (int)vocab, ld, target, sc,
-                           temperature, p, terms, sq, logp, o, ldg, sums);
+        hipLaunchKernelGGL((k_policy_rows<T, NT, U>), dim3(grid), dim3(NT), 0, st, x, rows, (int)vocab, ld, target, sc, p,
+                           terms, sq, logp, o, ldg, sums);
     };
     typedef std::integral_constant<int, 4> Four;
     typedef std::integral_constant<int, 8> Eight;

@@ -81,3 +81,27 @@ def test_an_advantage_of_zero(torch, seqs, tokens, clip_hi):
     near(loss, w[0], 100.0 * (1 + seqs))
     near(grad, w[2], w[3] + 1e-3)
     assert np.array_equal(counts.cpu().numpy(), w[1])
+
+
+@pytest.mark.parametrize("name", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("vocab", [7, 1000, 70001])
+def test_live_rows_of_one_value(torch, name, vocab):
+    """A live row that a mask of the type's lowest value (or any one value) fills is
+    the uniform distribution: logp = -log V, gradient g ([k = j] - 1/V).  Every
+    term and factor is 1 or 1/V, so that log V, the coefficient g and the product
+    g/V are rounded once each to f32, and the output once."""
+    dtype = dtype_of(torch, name)
+    low = torch.finfo(dtype).min
+    values = [low, low / 2, -1e4, 0.0, 5.0]
+    logits = torch.stack([torch.full((vocab,), v, dtype=dtype, device="cuda") for v in values])
+    target = torch.tensor([0, vocab - 1, vocab // 2, 3, 1], dtype=torch.int32, device="cuda")
+    old = torch.full((5,), -math.log(vocab), device="cuda")
+    for temperature in (1.0, 0.7):
+        _, _, logp, grad = iso.policy_loss_logits(logits, target, old, torch.ones(1, device="cuda"), temperature=temperature)
+        assert np.all(np.abs(logp.double().cpu().numpy() + math.log(vocab)) <= 2 * U * math.log(vocab))
+        # d = logp - old is off by old's rounding, and r = exp(d) with it
+        g = -np.exp(-math.log(vocab) - old.double().cpu().numpy())[:, None] / 5 / temperature
+        want = np.repeat(g * -1.0 / vocab, vocab, 1)
+        want[np.arange(5), target.cpu().numpy()] = g[:, 0] * (1 - 1.0 / vocab)
+        bad = np.abs(grad.double().cpu().numpy() - want) - (half(torch, dtype) + 4 * U) * np.abs(want) - floor_of(torch, dtype)
+        assert bad.max() <= 0, bad.max()
