@@ -165,6 +165,12 @@ struct ExpSeries {
         o.m1 = o.m2 + x;
         return o;
     }
+    // for any x
+    __device__ __forceinline__ ExpTerms any(double x) const {
+        ExpTerms o = (*this)(x);
+        far(x, o);
+        return o;
+    }
     // Beyond kFar: infinity or 0, which is what f32 outputs make of it.
     __device__ __forceinline__ static void far(double x, ExpTerms& o) {
         if (fabs(x) > kFar) {

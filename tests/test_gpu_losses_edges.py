@@ -105,3 +105,83 @@ def test_live_rows_of_one_value(torch, name, vocab):
         want[np.arange(5), target.cpu().numpy()] = g[:, 0] * (1 - 1.0 / vocab)
         bad = np.abs(grad.double().cpu().numpy() - want) - (half(torch, dtype) + 4 * U) * np.abs(want) - floor_of(torch, dtype)
         assert bad.max() <= 0, bad.max()
+
+
+def confident(torch, dtype, rows, vocab, seed, pad, temperature):
+    """Rows whose target leaves 1e-2 to 1e-7 to the others, the targets at the rows' ends and anywhere."""
+    logits, target, _, _ = make(torch, dtype, rows, vocab, seed, pad=pad, shift=seed % 3, scale=1.0)
+    target[0], target[1] = 0, vocab - 1
+    tg = target.cuda()
+    x = logits.double().cpu().numpy()
+    x[np.arange(rows), target.numpy()] = -np.inf
+    rest = np.log(np.exp(x / temperature).sum(1))
+    lift = torch.from_numpy((rest + np.linspace(math.log(1e2), math.log(1e7), rows)) * temperature)
+    logits[torch.arange(rows, device="cuda"), tg.long()] = lift.to(dtype).cuda()
+    return logits, target, logits.double().cpu().numpy()
+
+
+CONFIDENT = [(24, 11), (24, 1000), (140, 4099), (24, 32003), (12, 70001), (6, 131075)]
+
+
+@pytest.mark.parametrize("name", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,vocab", CONFIDENT)
+def test_confident_targets_vjp(torch, name, rows, vocab):
+    """The target's entry g (1 - p) / T keeps its relative accuracy, p at the given
+    log-sum: f64 up to one rounding to f32 and one to the type; z = x/T - lse and the
+    entropy's z + H are off by a few of f64's steps of their parts."""
+    dtype = dtype_of(torch, name)
+    say(f"[losses] confident vjp {name} {rows}x{vocab}")
+    for temperature in (1.0, 0.7):
+        logits, target, x = confident(torch, dtype, rows, vocab, rows + vocab, vocab % 4, temperature)
+        tg = target.cuda()
+        _, lse, ent = iso.token_logp(logits, tg, temperature=temperature, entropy=True)
+        gen = torch.Generator().manual_seed(rows)
+        g, gent = torch.randn(rows, generator=gen).cuda(), torch.randn(rows, generator=gen).cuda()
+        n = lambda t: t.double().cpu().numpy()  # noqa: E731
+        at = np.arange(rows), target.numpy()
+        xt = x[at] / temperature
+        z = xt - n(lse)
+        step = 2.0 ** -50 * (np.abs(xt) + np.abs(n(lse)))
+        for entropies in (False, True):
+            kw = dict(entropy=ent, g_entropy=gent) if entropies else {}
+            for out in (None, logits.clone()):  # in place too
+                src = logits if out is None else out
+                grad = n(iso.token_logp_vjp(g, src, tg, lse, temperature=temperature, out=out, **kw))[at]
+                want = -n(g) * np.expm1(z)
+                moved = np.abs(n(g)) * step
+                if entropies:
+                    want = want - n(gent) * np.exp(z) * (z + n(ent))
+                    moved = moved + np.abs(n(gent)) * (step + 2.0 ** -50 * np.abs(n(ent)))
+                tol = (half(torch, dtype) + 2 * U) * np.abs(want) + moved
+                bad = np.abs(grad - want / temperature) - tol / temperature - floor_of(torch, dtype)
+                assert bad.max() <= 0, (temperature, entropies, bad.max())
+
+
+@pytest.mark.parametrize("name", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,vocab", CONFIDENT)
+def test_confident_targets_from_logits(torch, name, rows, vocab):
+    """The same in the loss from logits.  1 - p is the sum of the other entries'
+    p, each off by its exponent's three roundings, its exp's two half steps and two a
+    rescaling of the running sums (one a chunk, 16 at most here, and three joins);
+    r = exp(logp - old) = 1 moves by what logp moves."""
+    dtype = dtype_of(torch, name)
+    say(f"[losses] confident head {name} {rows}x{vocab}")
+    for temperature in (1.0, 0.7):
+        logits, target, x = confident(torch, dtype, rows, vocab, rows + vocab, vocab % 4, temperature)
+        at = np.arange(rows), target.numpy()
+        z = (x - x[at][:, None]) / temperature
+        others = np.exp(z)
+        others[at] = 0.0
+        s = others.sum(1)
+        lp = -np.log1p(s)
+        adv = torch.full((1,), 2.0, device="cuda")
+        old = lp.astype(np.float32)
+        for out in (None, logits.clone()):
+            src = logits if out is None else out
+            _, _, logp, grad = iso.policy_loss_logits(src, target.cuda(), put(torch, old), adv, temperature=temperature, out=out)
+            off = U * ((others * (3 * np.abs(z) + 2)).sum(1) / s + 2 * 19) + 2.0 ** -50 / s
+            assert np.all(np.abs(logp.double().cpu().numpy() - lp) <= (U + off) * np.abs(lp))
+            want = -2.0 / rows * np.exp(lp - old.astype(np.float64)) * (s / (1 + s)) / temperature
+            got = grad.double().cpu().numpy()[at]
+            tol = (half(torch, dtype) + 2 * U + 2 * off) * np.abs(want) + floor_of(torch, dtype)
+            assert np.all(np.abs(got - want) <= tol), (temperature, (np.abs(got - want) - tol).max())
