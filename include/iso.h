@@ -319,7 +319,7 @@ size_t iso_calib_workspace_bytes(int64_t n);
  *           row is not read and its outputs are 0.  A target >= vocab gives
  *           NaN logp.
  *   logp, lse [rows] f32, written.  entropy [rows] f32, written, or NULL.
- *   temperature > 0, finite.
+ *   temperature from 1e-28 to 1e28.
  * A logit of -infinity (or far below the row's maximum) is a masked entry and
  * adds nothing.  A row with a NaN or +infinity, or of -infinity alone, has no
  * distribution: its outputs are NaN.
@@ -328,7 +328,9 @@ size_t iso_calib_workspace_bytes(int64_t n);
  * logp and g_entropy of the entropy (NULL: none):
  *     grad_k = ( g_logp ([k = j] - p_k) - g_entropy p_k (x_k - lse + entropy) ) / temperature .
  *   lse     [rows] f32: the forward call's.  entropy [rows] f32: the forward
- *           call's (needed with g_entropy only).
+ *           call's (needed with g_entropy only).  p is taken at this lse: its
+ *           rounding to f32 is a relative |lse| 2^-24 of p, much at a small
+ *           temperature (iso_policy_loss_logits does not round it).
  *   grad    [rows][vocab] of `dtype`, row r at r*ld_grad, written.  It may be
  *           the logits themselves (same pointer and ld): the gradient then
  *           takes the logits' place; any other overlap is an error.  Columns

@@ -571,11 +571,14 @@ size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t size_of(int dtype) { return dtype == ISO_DT_F32 ? 4 : 2; }
 
+// log2(e)/T and lse T (up to 21 T past the largest logit) stay inside f32.
+constexpr double kTempMin = 1e-28, kTempMax = 1e28;
+
 bool logits_ok(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld, double temperature) {
     if (dtype != ISO_DT_F32 && dtype != ISO_DT_F16 && dtype != ISO_DT_BF16) return false;
     if (rows < 0 || rows > 0x7fffffffLL || vocab < 1 || vocab > (1LL << 30) || ld < vocab) return false;
     if (rows && ld > INT64_MAX / 16 / rows) return false;
-    if (!(temperature > 0.0) || !isfinite(temperature)) return false;
+    if (!(temperature >= kTempMin && temperature <= kTempMax)) return false;
     return aligned(logits, size_of(dtype));
 }
 

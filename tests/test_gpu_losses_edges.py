@@ -185,3 +185,32 @@ def test_confident_targets_from_logits(torch, name, rows, vocab):
             got = grad.double().cpu().numpy()[at]
             tol = (half(torch, dtype) + 2 * U + 2 * off) * np.abs(want) + floor_of(torch, dtype)
             assert np.all(np.abs(got - want) <= tol), (temperature, (np.abs(got - want) - tol).max())
+
+
+@pytest.mark.parametrize("name", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("vocab", [9, 5000, 50021])
+def test_temperatures_at_the_ends(torch, name, vocab):
+    """1e-28: the largest logit takes all; 1e28: every distribution is uniform."""
+    dtype = dtype_of(torch, name)
+    logits, target, x, _ = make(torch, dtype, 6, vocab, vocab)
+    logits[2, ::2] = -math.inf
+    logits[3, 1:] = torch.finfo(dtype).min
+    target[2], target[4] = 1, int(x[4].argmax())
+    x = logits.double().cpu().numpy()
+    tg, g = target.cuda(), torch.linspace(-1, 1, 6).cuda()
+    for temperature in (1e-28, 1e28):
+        got = iso.token_logp(logits, tg, temperature=temperature, entropy=True)
+        lp, lse, ent, err = losses.token_logp(x, target.numpy(), temperature)
+        for v, w in ((got[0], lp), (got[1], lse), (got[2], ent)):
+            v = v.double().cpu().numpy()
+            with np.errstate(over="ignore"):
+                w32 = w.astype(np.float32).astype(np.float64)
+            same = np.isinf(w32)
+            assert np.array_equal(v[same], w32[same])
+            assert np.all(np.abs(v - w)[~same] <= (U * (np.abs(w) + err))[~same])
+        if temperature > 1:
+            grad = iso.token_logp_vjp(g, logits, tg, got[1], temperature=temperature)
+            check_vjp(torch, grad, x, target, got[1], g, None, None, temperature, dtype)
+        old = put(torch, np.maximum(lp, -3e38).astype(np.float32))
+        out = iso.policy_loss_logits(logits, tg, old, torch.ones(1, device="cuda"), temperature=temperature)
+        assert torch.equal(out[2], got[0]) and not bool(torch.isnan(out[3]).any())
