@@ -335,7 +335,9 @@ size_t iso_calib_workspace_bytes(int64_t n);
  *           the logits themselves (same pointer and ld): the gradient then
  *           takes the logits' place; any other overlap is an error.  Columns
  *           past vocab are not touched.
- * Ignored rows get zeros.  A row whose target is >= vocab gets NaN.
+ * Ignored rows get zeros.  A row whose target is >= vocab gets NaN.  A masked
+ * entry's gradient is 0 while g_logp and 200 g_entropy over temperature are
+ * inside f32.
  */
 enum { ISO_DT_F32 = 0, ISO_DT_F16 = 1, ISO_DT_BF16 = 2 };
 size_t iso_token_logp_workspace_bytes(int64_t rows, int64_t vocab, int dtype);

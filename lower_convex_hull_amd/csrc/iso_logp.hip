@@ -320,9 +320,11 @@ __global__ __launch_bounds__(kJoinNT) void k_token_logp_join(const T* __restrict
 }
 
 // What a row's gradient takes: p = exp(x/T - lse) as exp2((x - mh) c) times a
-// factor of the row, folded into a, b: gradient p (a + b (x - mh)).  The target's
-// entry, g (1 - p)/T and the entropy's part, is formed apart in f64: in f32 the
-// difference kept nothing of 1 - p below 1e-7, and lost bf16's half step at 1e-5.
+// factor of the row, folded into a, b: gradient p (a + b y), y = (x - mh) c.  y is
+// held at -200, where p is 0: a masked entry's, -infinity or huge, times b would
+// be infinite, and its gradient 0 times that.  The target's entry, g (1 - p)/T and
+// the entropy's part, is formed apart in f64: in f32 the difference kept nothing
+// of 1 - p below 1e-7, and lost bf16's half step at 1e-5.
 struct RowGrad {
     float mh, a, b;
 };
@@ -335,7 +337,7 @@ __device__ __forceinline__ RowGrad row_grad(double lse, double g, double ent, do
     const double off = (double)o.mh * inv_t - lse;  // x/T - lse = (x - mh)/T + off
     const double f = (double)__builtin_amdgcn_exp2f((float)(off * kLog2e)) * inv_t;
     o.a = (float)(-(g + g_ent * (ent + off)) * f);
-    o.b = (float)(-g_ent * inv_t * f);
+    o.b = (float)(-g_ent * kLn2 * f);
     return o;
 }
 // The target's entry at the given log-sum, xj its logit.
@@ -366,9 +368,9 @@ struct RowShare {
 // An element's gradient (not the target's).
 template <bool ENT>
 __device__ __forceinline__ float grad_one(float x, const RowGrad& q, float cf) {
-    const float d = x - q.mh;
-    const float p = __builtin_amdgcn_exp2f(d * cf);
-    return ENT ? p * fmaf(q.b, held(d), q.a) : p * q.a;
+    const float y = (x - q.mh) * cf;
+    const float p = __builtin_amdgcn_exp2f(y);
+    return ENT ? p * fmaf(q.b, fmaxf(y, -200.0f), q.a) : p * q.a;
 }
 // The target's place in a row and its entry.  Put into its vector before that is
 // stored, or (Later) stored over it at the end by the same thread: the loss from

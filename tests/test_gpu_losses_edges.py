@@ -214,3 +214,22 @@ def test_temperatures_at_the_ends(torch, name, vocab):
         old = put(torch, np.maximum(lp, -3e38).astype(np.float32))
         out = iso.policy_loss_logits(logits, tg, old, torch.ones(1, device="cuda"), temperature=temperature)
         assert torch.equal(out[2], got[0]) and not bool(torch.isnan(out[3]).any())
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("scale,temperature", [(1e9, 1.0), (1e20, 1.0), (1.0, 1e-10), (1e12, 0.7)])
+def test_large_entropy_gradients_of_masked_entries(torch, name, scale, temperature):
+    """A masked entry's gradient is 0 whatever g_entropy / T is."""
+    dtype = dtype_of(torch, name)
+    logits, target, _, _ = make(torch, dtype, 8, 1003, 3)
+    logits *= temperature
+    logits[:, 1::3] = -math.inf
+    logits[:, 2::3] = torch.finfo(dtype).min
+    target = target // 3 * 3
+    x = logits.double().cpu().numpy()
+    tg = target.cuda()
+    _, lse, ent = iso.token_logp(logits, tg, temperature=temperature, entropy=True)
+    g, gent = torch.linspace(-1, 1, 8).cuda(), torch.linspace(1, -1, 8).cuda() * scale
+    grad = iso.token_logp_vjp(g, logits, tg, lse, temperature=temperature, entropy=ent, g_entropy=gent)
+    check_vjp(torch, grad, x, target, lse, g, ent, gent, temperature, dtype)
+    assert bool((grad[:, 1::3] == 0).all()) and bool((grad[:, 2::3] == 0).all())
