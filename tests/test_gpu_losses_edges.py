@@ -233,3 +233,21 @@ def test_large_entropy_gradients_of_masked_entries(torch, name, scale, temperatu
     grad = iso.token_logp_vjp(g, logits, tg, lse, temperature=temperature, entropy=ent, g_entropy=gent)
     check_vjp(torch, grad, x, target, lse, g, ent, gent, temperature, dtype)
     assert bool((grad[:, 1::3] == 0).all()) and bool((grad[:, 2::3] == 0).all())
+
+
+@pytest.mark.parametrize("name", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [(1, 1000003), (3, 300007), (2, 131075), (140, 70001), (200, 50021), (260, 24577), (700, 16391),
+                                        (40, 8195), (2000, 2051), (300, 1025)])
+def test_every_entry_counts_once(torch, name, rows, vocab):
+    """In a row of one value every term and factor is exactly 1: the sum is V, and
+    log V is rounded once.  An entry left out or taken twice is 1 / V."""
+    logits = torch.full((rows, vocab), 1.5, dtype=dtype_of(torch, name), device="cuda")
+    target = torch.arange(rows, dtype=torch.int32, device="cuda")
+    logp, lse, ent = iso.token_logp(logits, target, entropy=True)
+    old = torch.full((rows,), -math.log(vocab), device="cuda")
+    head = iso.policy_loss_logits(logits, target, old, torch.ones(1, device="cuda"))[2]
+    tol = U * math.log(vocab) + 1e-12
+    assert tol < 0.9 / vocab
+    for v, w in ((logp, -math.log(vocab)), (ent, math.log(vocab)), (head, -math.log(vocab))):
+        assert np.all(np.abs(v.double().cpu().numpy() - w) <= tol)
+    assert np.all(np.abs(lse.double().cpu().numpy() - 1.5 - math.log(vocab)) <= U * (1.5 + math.log(vocab)) + 1e-12)
