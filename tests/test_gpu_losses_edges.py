@@ -251,3 +251,104 @@ def test_every_entry_counts_once(torch, name, rows, vocab):
     for v, w in ((logp, -math.log(vocab)), (ent, math.log(vocab)), (head, -math.log(vocab))):
         assert np.all(np.abs(v.double().cpu().numpy() - w) <= tol)
     assert np.all(np.abs(lse.double().cpu().numpy() - 1.5 - math.log(vocab)) <= U * (1.5 + math.log(vocab)) + 1e-12)
+
+
+class Arena:
+    """Device memory filled with a pattern, of which pieces are handed out with guards around them."""
+
+    GUARD = 8192
+
+    def __init__(self, torch, nbytes):
+        self.torch = torch
+        self.mem = torch.full((nbytes,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.end, self.used = self.GUARD, []
+
+    def take(self, nbytes):
+        at = self.end
+        assert at + nbytes + self.GUARD <= self.mem.numel()
+        self.used.append((at, at + nbytes))
+        self.end = (at + nbytes + 255) // 256 * 256 + self.GUARD
+        return self.mem.data_ptr() + at
+
+    def untouched(self):
+        """Every byte outside the pieces still holds the pattern."""
+        keep = self.mem.clone()
+        for a, b in self.used:
+            keep[a:b] = 0xA5
+        return bool((keep == 0xA5).all())
+
+
+def broken_offsets(rng, seqs, n):
+    yield rng.integers(-2 * n, 3 * n, seqs + 1)
+    yield rng.integers(-2 ** 31, 2 ** 31, seqs + 1)
+    yield np.sort(rng.integers(-n, 2 * n, seqs + 1))
+    yield np.sort(rng.integers(0, n + 1, seqs + 1))[::-1]
+    yield np.full(seqs + 1, n // 2)
+    yield np.full(seqs + 1, n)
+    yield np.full(seqs + 1, -1)
+    yield np.full(seqs + 1, 2 ** 31 - 1)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("seqs,n", [(2, 100), (300, 5000), (2, 40000), (300, 40001), (9000, 20011)])
+def test_nothing_beside_the_outputs_is_written(torch, seqs, n, masked):
+    """Outputs and workspaces of exactly the sizes asked for, between guards, in calls with broken offsets."""
+    say(f"[losses] guards {seqs}x{n} masked={masked}")
+    rng = np.random.default_rng(seqs + n)
+    lp = torch.full((n,), -1.0, device="cuda")
+    mask = put(torch, rng.random(n) < 0.7) if masked else None
+    adv = torch.ones(seqs, device="cuda")
+    vocab = 9
+    logits = torch.zeros(n, vocab, dtype=torch.bfloat16, device="cuda")
+    target = torch.zeros(n, dtype=torch.int32, device="cuda")
+    if masked:
+        target[~mask] = -1
+    m = None if mask is None else mask.data_ptr()
+    stream = torch.cuda.current_stream().cuda_stream
+    sizes = [iso.iso_pref_loss_workspace_bytes(n, seqs // 2), iso.iso_policy_loss_workspace_bytes(n, seqs),
+             iso.iso_policy_loss_logits_workspace_bytes(n, vocab, seqs, iso.ISO_DT_BF16)]
+    for off in broken_offsets(rng, seqs, n):
+        o = put(torch, off.astype(np.int32))
+        for flags in (0, 1):
+            a = Arena(torch, 2 * sum(sizes) + 40 * (n + seqs) + 20 * (Arena.GUARD + 256))
+            st = iso.iso_pref_loss(lp.data_ptr(), None, m, o.data_ptr(), seqs // 2, n, 0.1, 0.0, a.take(4), a.take(2 * seqs),
+                                   a.take(4 * seqs), a.take(4 * n), 1.0, a.take(sizes[0]), sizes[0], stream, flags)
+            assert st == iso.ISO_OK
+            for token_adv in (0, iso.ISO_POLICY_ADV_TOKEN):
+                av = lp.data_ptr() if token_adv else adv.data_ptr()
+                st = iso.iso_policy_loss(lp.data_ptr(), lp.data_ptr(), lp.data_ptr(), av, m, o.data_ptr(), seqs, n, 0.2, 0.2, 0.1,
+                                         0.0, a.take(12), a.take(8), a.take(4 * n), 1.0, a.take(sizes[1]), sizes[1], stream,
+                                         flags | token_adv)
+                assert st == iso.ISO_OK
+            st = iso.iso_policy_loss_logits(logits.data_ptr(), iso.ISO_DT_BF16, n, vocab, vocab, target.data_ptr(), 1.0,
+                                            lp.data_ptr(), None, adv.data_ptr(), o.data_ptr(), seqs, 0.2, 0.2, 0.0, 0.0,
+                                            a.take(12), a.take(8), a.take(4 * n), a.take(2 * n * vocab), vocab, 1.0,
+                                            a.take(sizes[2]), sizes[2], stream, flags)
+            assert st == iso.ISO_OK
+            torch.cuda.synchronize()
+            assert a.untouched(), (off[:4], flags)
+
+
+@pytest.mark.parametrize("rows,vocab", [(1, 1), (3, 257), (5, 16385), (3, 131075), (130, 50021), (700, 2049)])
+def test_nothing_beside_the_logits_outputs_is_written(torch, rows, vocab):
+    code, ld = iso.ISO_DT_BF16, vocab + 3
+    size = iso.iso_token_logp_workspace_bytes(rows, vocab, code)
+    logits = torch.randn(rows, vocab, device="cuda").bfloat16()
+    target = torch.arange(rows, dtype=torch.int32, device="cuda") % (vocab + 2) - 1  # ignored, in the vocabulary, past it
+    g = torch.ones(rows, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    for shift in (0, 1, 3):
+        a = Arena(torch, size + 2 * rows * ld + 12 * rows + 6 * (Arena.GUARD + 512))
+        logp, lse, ent = a.take(4 * rows), a.take(4 * rows), a.take(4 * rows)
+        st = iso.iso_token_logp(logits.data_ptr(), code, rows, vocab, vocab, target.data_ptr(), 1.0, logp, lse, ent, a.take(size),
+                                size, stream)
+        assert st == iso.ISO_OK
+        grad = a.take(2 * shift + 2 * rows * ld) + 2 * shift
+        a.used.pop()
+        base = grad - a.mem.data_ptr()
+        a.used += [(base + 2 * ld * r, base + 2 * ld * r + 2 * vocab) for r in range(rows)]  # without the padding
+        st = iso.iso_token_logp_vjp(logits.data_ptr(), code, rows, vocab, vocab, target.data_ptr(), 1.0, lse, ent, g.data_ptr(),
+                                    g.data_ptr(), grad, ld, stream)
+        assert st == iso.ISO_OK
+        torch.cuda.synchronize()
+        assert a.untouched(), shift
