@@ -352,3 +352,78 @@ def test_nothing_beside_the_logits_outputs_is_written(torch, rows, vocab):
         assert st == iso.ISO_OK
         torch.cuda.synchronize()
         assert a.untouched(), shift
+
+
+def stream_calls(s, **kw):
+    lp, lse, ent = iso.token_logp(s["x"], s["t"], entropy=True, **kw)
+    return [lp, lse, ent, iso.token_logp_vjp(s["g"], s["x"], s["t"], s["lse"], entropy=s["ent"], g_entropy=s["g"], **kw),
+            *iso.pref_loss(s["lp"], s["ref"], s["off"], mask=s["mask"], **kw),
+            *iso.policy_loss(s["lp"], s["ref"], s["adv"], ref_logp=s["ref"], mask=s["mask"], seq_off=s["off"], kl_coef=0.1,
+                             seq_mean=True, **kw),
+            *iso.policy_loss_logits(s["x"], s["t"], s["old"], s["adv"], ref_logp=s["lse"], seq_off=s["off64"], kl_coef=0.1,
+                                    seq_mean=True, **kw)]
+
+
+def stream_inputs(torch, seed):
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(64, 5003, generator=gen) * 2
+    s = {"x": x.bfloat16(), "t": torch.randint(-1, 5003, (64,), generator=gen, dtype=torch.int32), "g": torch.randn(64, generator=gen),
+         "lse": torch.logsumexp(x, 1), "ent": torch.rand(64, generator=gen) + 5, "lp": -torch.rand(30000, generator=gen),
+         "ref": -torch.rand(30000, generator=gen), "old": -torch.rand(64, generator=gen) - 8,
+         "mask": torch.rand(30000, generator=gen) < 0.7, "adv": torch.randn(4, generator=gen),
+         "off": torch.tensor([0, 100 + seed, 9000, 9000, 30000], dtype=torch.int32),
+         "off64": torch.tensor([0, 10 + seed, 20, 40, 64], dtype=torch.int32)}
+    return {k: v.cuda() for k, v in s.items()}
+
+
+def busy(torch, block):
+    """Some tens of milliseconds of copies on the current stream."""
+    for _ in range(200):
+        block[1].copy_(block[0])
+
+
+def test_calls_run_on_the_stream_they_are_given(torch):
+    """New inputs are copied in on the other stream, behind other work there: a call
+    that ran anywhere else would take the old ones."""
+    s, new = stream_inputs(torch, 1), stream_inputs(torch, 2)
+    block = torch.empty(2, 1 << 28, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    stream_calls(s)
+    before = stream_calls(s)
+    want = stream_calls(new)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        busy(torch, block)
+        for k in s:
+            s[k].copy_(new[k])
+    got = stream_calls(s, stream=side)
+    side.synchronize()
+    for k, (a, b, c) in enumerate(zip(got, want, before)):
+        assert torch.equal(a, b), k
+        assert b.dtype == torch.int32 or not torch.equal(b, c), k  # the old inputs would have shown
+
+
+def test_inputs_dropped_after_a_call_on_another_stream(torch):
+    """The call still waits behind other work when its inputs are dropped and their sizes taken again and overwritten."""
+    keep = stream_inputs(torch, 3)
+    block = torch.empty(2, 1 << 28, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    want = stream_calls(keep)
+    for v in keep.values():
+        torch.empty_like(v).fill_(1)  # its kernels are loaded by now
+    torch.cuda.synchronize()
+    mine = {k: v.clone() for k, v in keep.items()}
+    places = {v.data_ptr() for v in mine.values()}
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        busy(torch, block)
+    got = stream_calls(mine, stream=side)
+    mine.clear()
+    again = [torch.empty_like(v) for v in keep.values()]
+    assert not side.query()  # the calls have not run yet
+    for v in again:
+        v.fill_(1)  # on the current stream, at once
+    assert not places & {v.data_ptr() for v in again}
+    side.synchronize()
+    for k, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a, b), k
