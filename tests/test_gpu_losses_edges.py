@@ -427,3 +427,61 @@ def test_inputs_dropped_after_a_call_on_another_stream(torch):
     side.synchronize()
     for k, (a, b) in enumerate(zip(got, want)):
         assert torch.equal(a, b), k
+
+
+def placed(torch, a, shift):
+    """A copy of a that begins `shift` elements into a buffer."""
+    store = torch.empty(a.numel() + shift + 8, dtype=a.dtype, device="cuda")
+    view = store[shift:shift + a.numel()]
+    view.copy_(a)
+    return view
+
+
+@pytest.mark.parametrize("seqs,tokens", [(4, 777), (6, 8192), (40, 20011), (2, 70002), (3000, 90001)])
+@pytest.mark.parametrize("shifts", [(1, 2, 3, 1), (2, 3, 1, 2), (3, 1, 2, 3)])
+def test_token_arrays_that_begin_anywhere(torch, seqs, tokens, shifts):
+    """Tokens' arrays at every multiple of their element and masks at every byte: the
+    values do not depend on where they lie."""
+    say(f"[losses] places {seqs}x{tokens} {shifts}")
+    rng = np.random.default_rng(tokens)
+    torch.manual_seed(tokens)
+    logp = put(torch, -rng.exponential(1.0, tokens).astype(np.float32))
+    old, ref = logp + 0.2 * torch.randn(tokens, device="cuda"), logp + 0.2 * torch.randn(tokens, device="cuda")
+    mask = put(torch, rng.random(tokens) < 0.7)
+    off = put(torch, offsets(rng, seqs, tokens))
+    adv, per = torch.randn(seqs, device="cuda"), torch.randn(tokens, device="cuda")
+    a, b, c, d = shifts
+    p = lambda t, k: placed(torch, t, k)  # noqa: E731
+    for m in (None, mask):
+        pm = None if m is None else p(m, d)
+        for mean in (False, True):
+            want = iso.pref_loss(logp, ref, off, mask=m, mean=mean)
+            got = iso.pref_loss(p(logp, a), p(ref, b), p(off, c), mask=pm, mean=mean)
+            assert all(torch.equal(x, y) for x, y in zip(got, want))
+            for token_adv in (False, True):
+                kw = dict(kl_coef=0.1, seq_mean=mean, token_adv=token_adv)
+                av = per if token_adv else adv
+                want = iso.policy_loss(logp, old, av, ref_logp=ref, mask=m, seq_off=off, **kw)
+                got = iso.policy_loss(p(logp, a), p(old, b), p(av, c), ref_logp=p(ref, d), mask=pm, seq_off=p(off, a), **kw)
+                assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("rows,seqs", [(40, 3), (300, 5), (9001, 7)])
+def test_rows_arrays_that_begin_anywhere(torch, rows, seqs):
+    rng = np.random.default_rng(rows)
+    torch.manual_seed(rows)
+    logits = torch.randn(rows, 67, device="cuda").half()
+    target = put(torch, rng.integers(-1, 67, rows).astype(np.int32))
+    old, ref = put(torch, -rng.random(rows).astype(np.float32) - 3), put(torch, -rng.random(rows).astype(np.float32) - 3)
+    off, adv = put(torch, offsets(rng, seqs, rows)), torch.randn(seqs, device="cuda")
+    p = lambda t, k: placed(torch, t, k)  # noqa: E731
+    logp, lse, ent = iso.token_logp(logits, target, entropy=True)
+    grad = iso.token_logp_vjp(old, logits, target, lse, entropy=ent, g_entropy=ref)
+    head = iso.policy_loss_logits(logits, target, old, adv, ref_logp=ref, seq_off=off, kl_coef=0.1, seq_mean=True)
+    for k in (1, 2, 3):
+        got = iso.token_logp(logits, p(target, k), entropy=True)
+        assert all(torch.equal(x, y) for x, y in zip(got, (logp, lse, ent)))
+        assert torch.equal(iso.token_logp_vjp(p(old, k), logits, p(target, k), p(lse, k), entropy=p(ent, k), g_entropy=p(ref, k)), grad)
+        got = iso.policy_loss_logits(logits, p(target, k), p(old, k), p(adv, k), ref_logp=p(ref, k), seq_off=p(off, k), kl_coef=0.1,
+                                     seq_mean=True)
+        assert all(torch.equal(x, y) for x, y in zip(got, head))
