@@ -23,8 +23,10 @@ struct Wide {
 };
 
 // STREAM: without a place in the caches, for logits that do not fit them anyway
-// (8192 x 65536 bf16 forward 145 -> 133 us); smaller ones may still be there
-// from the call before (300 x 30000 f32 backward: 12.3 us, streamed 13.8).
+// (8192 x 65536 bf16 forward 145 -> 133 us; in workgroups of 64 threads 40000 x 2000
+// f32 56.4 -> 55.5, of 512 515 x 99991 f32 48.3 -> 39.4, of 1024 200 x 200000 f32
+// 30.3 -> 28.3); smaller ones may still be there from the call before (300 x 30000
+// f32 backward: 12.3 us, streamed 13.8).
 template <bool STREAM, typename T>
 __device__ __forceinline__ typename Wide<T>::V load_wide(const T* p) {
     const auto* v = reinterpret_cast<const typename Wide<T>::V*>(p);
@@ -651,12 +653,14 @@ void start_logp_t(const T* x, int64_t rows, int64_t vocab, int64_t ld, const int
         hipLaunchKernelGGL((k_token_logp<T, ENT, NT, decltype(stream)::value>), grid_of(rows * pl.splits), dim3(NT), 0, st, x, rows, (int)vocab,
                            ld, target, sc, pl.splits, (int)pl.chunk, o, parts);
     };
-    // so many logits have workgroups of 256
-    if (pl.threads == 64) start(std::integral_constant<int, 64>{}, std::false_type{});
-    else if (pl.threads == 256 && streamed<T>(rows, vocab)) start(std::integral_constant<int, 256>{}, std::true_type{});
-    else if (pl.threads == 256) start(std::integral_constant<int, 256>{}, std::false_type{});
-    else if (pl.threads == 512) start(std::integral_constant<int, 512>{}, std::false_type{});
-    else start(std::integral_constant<int, 1024>{}, std::false_type{});
+    auto by_threads = [&](auto stream) {
+        if (pl.threads == 64) start(std::integral_constant<int, 64>{}, stream);
+        else if (pl.threads == 256) start(std::integral_constant<int, 256>{}, stream);
+        else if (pl.threads == 512) start(std::integral_constant<int, 512>{}, stream);
+        else start(std::integral_constant<int, 1024>{}, stream);
+    };
+    if (streamed<T>(rows, vocab)) by_threads(std::true_type{});
+    else by_threads(std::false_type{});
     if (pl.splits > 1)
         hipLaunchKernelGGL((k_token_logp_join<T, ENT>), grid_of((rows + kJoinNT / 64 - 1) / (kJoinNT / 64)),
                            dim3(kJoinNT), 0, st, x, rows, (int)vocab, ld, target, sc, pl.splits, parts, o);

@@ -485,3 +485,22 @@ def test_rows_arrays_that_begin_anywhere(torch, rows, seqs):
         got = iso.policy_loss_logits(logits, p(target, k), p(old, k), p(adv, k), ref_logp=p(ref, k), seq_off=p(off, k), kl_coef=0.1,
                                      seq_mean=True)
         assert all(torch.equal(x, y) for x, y in zip(got, head))
+
+
+@pytest.mark.parametrize("rows,vocab,name", [(36000, 1000, "f32"), (70000, 1003, "bf16"), (800, 50021, "f32"), (400, 99991, "f32"),
+                                             (200, 180001, "f32"), (150, 500009, "f16"), (100, 700001, "bf16")])
+def test_streamed_logits_in_every_workgroup_shape(torch, rows, vocab, name):
+    """Calls past 128 MB, which read past the caches, by 64, 256, 512 and 1024 threads, whole rows and pieces."""
+    dtype = dtype_of(torch, name)
+    say(f"[losses] streamed {rows}x{vocab} {name}")
+    assert rows * vocab * torch.finfo(dtype).bits // 8 > 128 << 20
+    torch.manual_seed(rows)
+    logits = (2 * torch.randn(rows, vocab, device="cuda")).to(dtype)
+    target = torch.randint(0, vocab, (rows,), device="cuda").to(torch.int32)
+    target[rows // 3] = -1
+    got = iso.token_logp(logits, target, entropy=True)
+    short = iso.token_logp(logits, target)
+    pick = torch.tensor([0, 1, rows // 3, rows // 2, rows - 2, rows - 1], device="cuda")
+    x, t = logits[pick].double().cpu().numpy(), target[pick].cpu()
+    check_logp(torch, [v[pick] for v in got], x, t, 1.0)
+    check_logp(torch, [v[pick] for v in short], x, t, 1.0, entropy=False)
