@@ -301,9 +301,9 @@ size_t iso_calib_workspace_bytes(int64_t n);
  * preference loss, a clipped policy loss with a KL term, and the policy loss
  * taken from the logits.  Logits are f32, f16 or bf16 (ISO_DT_*); every other
  * real array is f32.  The terms of softmax sums are f32, the sums f64 (an
- * entropy's are f32 over at most 64 terms of a thread, f64 beyond); the losses'
- * sums are f64; each output is rounded once.  No atomics: results do not depend on
- * scheduling.  The calls only enqueue work on `stream` (they may be captured
+ * entropy's are f32 over at most 32 terms of a thread, f64 beyond); the losses'
+ * sums are f64; each output is rounded once.  No atomics on values: results do
+ * not depend on scheduling.  The calls only enqueue work on `stream` (they may be captured
  * into a graph), allocate nothing, and use a caller workspace (256-byte
  * aligned, no initialisation) of the size the matching *_workspace_bytes
  * gives.  Statuses: ISO_OK, ISO_ERR_ARG, ISO_ERR_WORKSPACE, ISO_ERR_HIP;

@@ -267,8 +267,11 @@ __device__ __forceinline__ void write_row(const LogpOut& o, int64_t r, const T* 
 constexpr int64_t kMaxGrid = 1 << 20;
 inline dim3 grid_of(int64_t items) { return dim3((unsigned)(items < kMaxGrid ? items : kMaxGrid)); }
 
-// Vectors of a thread at a time: 4, but 2 of streamed f32 logits (1111 x 50021:
-// 35.3 us, 38.4 with 4; 8192 x 65536 bf16: 132 us with 4, 135 with 2).
+// Vectors of a thread at a time: 4, but 2 of streamed f32 logits.  16 bits: 8192 x
+// 65536 bf16 166 us with 4, 168 with 2; 2000 x 131072 92 and 98.  f32 goes by how a
+// call's rows fill the CUs: 2 is faster at 515 x 99991 (38.6 us, 42.6 with 4), 1111 x
+// 50021 (39.5, 42.0) and 1500 x 99991 (95, 99), 4 at 700 x 131072 (57, 62 with 2), 2000 x
+// 50021 (67, 74) and 2000 x 131072 (162, 185); from 3000 rows on they are within 2 %.
 template <typename T, bool STREAM>
 constexpr int kLogpU = STREAM && sizeof(T) == 4 ? 2 : 4;
 
@@ -443,9 +446,9 @@ __device__ __forceinline__ void fill_row(T* o, const Piece<T>& w, T v) {
 
 constexpr int kVjpNT = 256, kVjpU = 2;
 
-// Bound by HBM: 4096 x 65536 bf16 moves 0.94 GB in 154 us, 6.1 TB/s.  One chunk a
+// Bound by HBM: 4096 x 65536 bf16 moves 0.94 GB in 151 us, 6.2 TB/s.  One chunk a
 // workgroup (a second, read after the first is written, cost 7 %), of two
-// vectors a thread (156 us; 1: 184, 4: 158, 8: 170).
+// vectors a thread (151 us; 1: 176, 3: 159, 4: 156, 8: 165).
 // Item = (row, chunk of it).
 template <typename T, bool ENT, bool STREAM>
 __global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t rows, int vocab, int64_t ld,
@@ -483,7 +486,7 @@ __global__ __launch_bounds__(kVjpNT) void k_logp_vjp(const T* logits, int64_t ro
 // stays in registers and the one before in LDS between the two; what a longer
 // row has before them is read again while the last-level cache may still have
 // it.  Bound by HBM: 4096 x 131072 bf16 reads each logit once (862 MB by the
-// counters) and writes 1.07 GB in 373 us, 5.2 TB/s, with 60 % of the issue cycles
+// counters) and writes 1.07 GB in 375 us, 5.2 TB/s, with 60 % of the issue cycles
 // spent on VALU instructions; three passes over the logits took 596.  Every
 // row's weight and advantage depend on the targets alone and are known before
 // (terms), or (NULL; few rows) are found here, which saves a launch.
@@ -711,8 +714,14 @@ constexpr int64_t kOwnTerms = 256;  // rows and sequences up to which a row's wo
 // A row's workgroup, by the bytes of a row.  A workgroup holds two chunks on
 // chip (registers and LDS); the fewer threads it has, the more rows a CU has in
 // flight, one reading while another writes.
-//   1024 x 8 vectors (2 x 128 KB, one row a CU): 4096 x 131072 bf16 375 us, 390 with 512
-//   512 x 8 (2 x 64 KB, two rows): 3000 x 101574 f16 253 us, 288 with 1024, 286 with 256
+//   1024 x 8 vectors (2 x 128 KB, one row a CU): 4096 x 131072 bf16, a fifth of the rows
+//     ignored, 375 us, 385 with 512; 256 x 131072 33 and 38; 2000 x 65536 f32 204 and 213
+//   512 x 8 (2 x 64 KB, two rows): 3000 x 101574 f16 253 us, 288 with 1024, 286 with 256;
+//     2000 x 118000 bf16 206 and 217
+//     Where they meet goes by more than the bytes, from 160 to 340 KB: f32 is faster
+//     with 1024 below the border (2000 x 58001, 227 KB: 199 us, 212 with 512), 16 bits with
+//     512 above it where no row is ignored (4096 x 131072, 256 KB: 417 us, 436 with 1024; at
+//     2000 x 170003, 332 KB, 312 and 305).
 //   256 x 8 (2 x 32 KB, four rows), many rows: 2000 x 25000 bf16 51 us, 57 with 512
 //     (37 x 32003 f16: 14.7 us, 12.9 with 512)
 //   256 x 4 (2 x 16 KB): 4096 x 16384 bf16 61 us, 72 with 512 x 8

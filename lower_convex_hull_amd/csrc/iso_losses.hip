@@ -1,7 +1,8 @@
 // Losses over tokens' log-probabilities, with their gradients: the paired
 // preference loss and the clipped policy loss with a KL term (formulas in
 // iso.h).  Both are sums over sequences of tokens followed by one value per
-// token; every sum of values is f64, in a fixed order, without atomics.
+// token; every sum of values is f64, in a fixed order, without atomics (the one
+// atomic is a maximum of whole numbers in LDS, whose order does not matter).
 #include "../../include/iso.h"
 #include "iso_losses.hpp"
 
@@ -786,7 +787,7 @@ __device__ __forceinline__ void policy_out(double kl_coef, const PolicySums& s, 
 // Bound by its f64 instructions: 8e6 tokens take 10.9e6 wave instructions (18 of
 // 36 us of every SIMD's issue at 2.4 GHz; two thirds of the time that waves live)
 // for 105 MB read and 32 MB written.  More waves (5, 6, 8 a SIMD) spill, spans
-// of 256 or 1024 tokens were 12 and 30 % slower, and loads issued a span ahead
+// of 256 or 1024 tokens were 7 and 12 % slower, and loads issued a span ahead
 // brought nothing.
 template <typename K>
 __global__ __launch_bounds__(kLossNT, kTermWaves) void k_policy_tokens(PolicyCall f, uint32_t spans) {

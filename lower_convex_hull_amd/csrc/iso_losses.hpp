@@ -121,7 +121,7 @@ struct Policy {
 };
 // exp(x), exp(x) - 1 and exp(x) - 1 - x in f64.  Cody and Waite's reduction
 // x = k ln 2 + r with |r| <= ln(2)/2, then Taylor's series q of exp(r) - 1 - r
-// to r^11 (the rest is below 6e-15 of 1).  With s = 2^k the small differences
+// to r^11 (the rest is below 7e-15 of 1).  With s = 2^k the small differences
 // are s q + (s r + (s - 1) - x): for k = 0 that is q, with its relative
 // accuracy.  A third of the instructions of the library's exp and expm1, whose
 // last bits an f32 output does not show.  The coefficients are held in scalar
