@@ -176,7 +176,7 @@ struct ExpSeries {
         if (fabs(x) > kFar) {
             o.e = x > 0.0 ? INFINITY : 0.0;
             o.m1 = o.e - 1.0;
-            o.m2 = o.m1 - x;
+            o.m2 = x > 0.0 ? INFINITY : o.m1 - x;  // also at x = infinity
         }
     }
 };

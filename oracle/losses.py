@@ -136,7 +136,7 @@ def policy_loss(logp, old, ref, adv, mask, off, seqs, lo=0.2, hi=0.2, kl_coef=0.
             move = np.abs(slope)
             if ref is not None:
                 u = ref[at] - logp[at]
-                kl = np.expm1(u) - u
+                kl = np.where(u == np.inf, np.inf, np.expm1(u) - u)  # its limit
                 if kl_coef:  # else the loss has no KL term, whatever u is
                     slope = slope - kl_coef * np.expm1(u)
                     move = move + abs(kl_coef) * np.exp(u)

@@ -504,3 +504,22 @@ def test_streamed_logits_in_every_workgroup_shape(torch, rows, vocab, name):
     x, t = logits[pick].double().cpu().numpy(), target[pick].cpu()
     check_logp(torch, [v[pick] for v in got], x, t, 1.0)
     check_logp(torch, [v[pick] for v in short], x, t, 1.0, entropy=False)
+
+
+@pytest.mark.parametrize("tokens", [5, 20011])
+@pytest.mark.parametrize("place", [0, 4])
+def test_an_infinite_difference_to_the_reference(torch, tokens, place):
+    """exp(u) - u - 1 is infinite at both infinities of u, and so is its sum, beside a finite loss."""
+    logp, ref = torch.full((tokens,), -1.0, device="cuda"), torch.full((tokens,), -1.1, device="cuda")
+    old, adv = logp.clone(), torch.ones(1, device="cuda")
+    for a in (logp, ref):
+        b = a.clone()
+        b[place] = -math.inf
+        args = (b, ref) if a is logp else (logp, b)
+        loss, _, grad = iso.policy_loss(args[0], old, adv, ref_logp=args[1])
+        assert float(loss[2]) == math.inf and math.isfinite(float(loss[0])) and bool(torch.isfinite(grad).all())
+        loss, _, grad = iso.policy_loss(args[0], old, adv, ref_logp=args[1], kl_coef=0.5)
+        assert float(loss[2]) == math.inf and float(loss[0]) == math.inf
+        want = -math.inf if a is logp else -1.0 / tokens + 0.5 / tokens  # -r A + kl_coef (1 - exp(u))
+        got = float(grad[place])
+        assert got == want or abs(got - want) <= 4 * U * abs(want)

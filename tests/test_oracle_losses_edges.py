@@ -28,3 +28,10 @@ def test_an_advantage_of_zero():
         assert np.all(loss == 0) and np.all(grad == 0) and np.all(size == 0) and counts.tolist() == [5, 0]
     loss, _, grad, _ = losses.policy_loss(logp, np.array([np.nan] * 5), None, np.zeros(1), None, None, 1)
     assert np.isnan(loss[0]) and np.all(np.isnan(grad))
+
+
+def test_an_infinite_difference_to_the_reference():
+    """exp(u) - u - 1 is infinite at both infinities of u."""
+    for ref, logp in ((-1.0, -np.inf), (-np.inf, -1.0)):
+        loss, _, _, _ = losses.policy_loss(np.array([logp]), np.array([-1.0]), np.array([ref]), np.ones(1), None, None, 1)
+        assert loss[2] == np.inf and np.isfinite(loss[0])
