@@ -422,6 +422,120 @@ int iso_policy_loss_logits(const void* logits, int dtype, int64_t rows, int64_t 
                            double grad_scale, void* workspace, size_t workspace_bytes, void* stream,
                            uint32_t flags);
 
+/*
+ * Decoding steps: what makes the answers that the losses above compare, and
+ * keeps their states apart while they are made.  Beam search's selection from
+ * logits, the states of beams brought into the order of their parents, a paged
+ * cache's sequences forked, grown and freed, and its live pages moved together.
+ * The calls only enqueue work on `stream` (they may be captured into a graph),
+ * allocate nothing, and results do not depend on scheduling.  Statuses: ISO_OK,
+ * ISO_ERR_ARG, ISO_ERR_WORKSPACE, ISO_ERR_HIP; nothing is launched on an error.
+ * Workspaces as for the losses (256-byte aligned, no initialisation).
+ *
+ * iso_beam_select - the best continuations of each batch item's beams.  Row
+ * r = b * beams + k of logits is beam k of item b.  With z = logits[r] /
+ * temperature and lse = log sum_v exp(z_v), the candidates of a beam are
+ *     token v:   logp = z_v - lse ,   s = score[r] + logp      (logits[r][v] > -infinity) ,
+ * and of an ended beam (ended[r] != 0) itself alone: end_token, logp = 0,
+ * s = score[r].  They are ranked by s * weight[r], rounded to f32; equal ranks
+ * by the lower beam, then the higher logit, then the lower token.  The first
+ * `take` of each item are written in this order.
+ *   logits   as for iso_token_logp, batch * beams rows.  The rows of ended
+ *            beams are not read.
+ *   score    [batch*beams] f32.  A beam whose score is not finite has no
+ *            candidates and is not read (-infinity for all beams but one: the
+ *            first step, where all are alike).
+ *   weight   [batch*beams] f32, or NULL (1): the rank's factor, as 1 / length^a.
+ *            A beam whose weight is not positive and finite has no candidates.
+ *   ended    [batch*beams] bytes, or NULL.
+ *   beams, take  from 1 to 128.
+ *   out_score, out_logp [batch*take] f32, written: s and logp.  out_parent
+ *            [batch*take] int32: the candidate's row, b * beams + k (what
+ *            iso_beam_reorder and iso_pages_fork take).  out_token
+ *            [batch*take] int32.  Places past an item's last candidate hold
+ *            -infinity, -infinity, -1 and -1.
+ * A row with a NaN or +infinity, or of -infinity alone, has no candidates, nor
+ * has what ranks at -infinity (below f32).  Sums are as in iso_token_logp, the
+ * score and the rank f64 until they are rounded.
+ *
+ * Arrays of states.  An iso_blocks describes, for rows (beams) or pages, the
+ * blocks row r holds: `inner` bytes each, block (o, m) at
+ *     base + o * outer_stride + r * row_stride + m * mid_stride ,
+ * o < outer, m < mid, strides in bytes (not negative; of a count of 1 they are
+ * not used).  A cache [layers][rows][heads][room][dim] whose first t tokens
+ * count has outer = layers, mid = heads, inner = t * dim * element size.
+ * Blocks may not overlap; arrays of one call may not either, from the first to
+ * the last byte each (two interleaved arrays are one, with a larger outer or
+ * mid).  At most ISO_MAX_BLOCKS arrays a call; any element type and alignment.
+ *
+ * iso_beam_reorder - row r of every array becomes what row parent[r] was, in
+ * place.  parent [batch*beams] int32: a row of the same item (r / beams); any
+ * other value, and r itself, leaves the row as it is.  beams from 1 to 128.
+ * Rows that stay are not written, those nobody comes from not read.
+ *
+ * iso_pages_fork - one step of a paged cache.  A page holds page_size tokens.
+ * Sequence s has length[s] tokens, in the pages table[s][0 ..
+ * ceil(length[s] / page_size)); refs[p] counts the entries, in this table or
+ * outside it, that hold page p; a page of 0 is free.  Child i goes on from
+ * sequence parent[i] (any value outside [0, seqs): a new sequence of length 0)
+ * and has room for grow[i] more tokens:
+ *     new_length[i] = length[parent[i]] + grow[i]
+ * (a negative grow counts as 0).  A sequence with several children is forked,
+ * one with none is freed.  Pages are shared, but for the one that a growing
+ * child goes on to write, where its parent's tokens end inside a page: the
+ * first such child (in order) keeps it if nobody but such children holds it,
+ * the others have copies of its tokens.  Pages for copies and growth are the
+ * lowest free ones (pages this call frees among them), in the children's order.
+ *   table [seqs][max_pages] int32, length [seqs] int32, refs [pages] int32: the
+ *            cache before the step, left as they are.
+ *   parent [children] int32.  grow [children] int32, or NULL: grow_all each.
+ *   pools    the arrays that hold the pages' tokens: rows are pages, a block's
+ *            inner bytes are page_size tokens (inner a multiple of page_size).
+ *            Copied tokens are written, nothing else.  May be NULL with count 0.
+ *   new_table [children][max_pages], new_length [children], new_refs [pages],
+ *            written: the cache after the step (entries without a page: -1).
+ *   status [5] int32, written: pages lacking, children longer than max_pages
+ *            allow, pages copied, pages taken, pages left free.
+ * If one of the first two is not 0 nothing is done: new_length is 0, new_table
+ * -1, new_refs is refs, no token is copied, and the old cache stands.
+ * What breaks the above is held inside the arrays: lengths to [0, max_pages *
+ * page_size], negative refs to 0, an entry outside [0, pages) holds no page.
+ * seqs and children at most 2^20.
+ *
+ * iso_pages_compact - the live pages (refs > 0) moved together: with n of them,
+ * those at n and beyond go, in order, to the free ones below n.
+ *   table [entries] int32, any shape; entries outside [0, pages) become -1.
+ *   new_table [entries], new_refs [pages], written.  moved [pages] int32,
+ *            written: where each page is now, -1 for the free ones.
+ *   pools    as above; whole pages are moved, in place.
+ *   status [2] int32, written: live pages, pages moved.
+ */
+#define ISO_MAX_BLOCKS 16
+typedef struct iso_blocks {
+    void* base;
+    int64_t outer, outer_stride, row_stride, mid, mid_stride, inner;
+} iso_blocks;
+size_t iso_beam_select_workspace_bytes(int64_t batch, int64_t beams, int64_t vocab, int64_t take,
+                                       int dtype);
+int iso_beam_select(const void* logits, int dtype, int64_t batch, int64_t beams, int64_t vocab,
+                    int64_t ld, const float* score, const float* weight, const uint8_t* ended,
+                    int32_t end_token, double temperature, int64_t take, float* out_score,
+                    float* out_logp, int32_t* out_parent, int32_t* out_token, void* workspace,
+                    size_t workspace_bytes, void* stream);
+int iso_beam_reorder(const iso_blocks* states, int count, const int32_t* parent, int64_t batch,
+                     int64_t beams, void* stream);
+size_t iso_pages_fork_workspace_bytes(int64_t seqs, int64_t children, int64_t pages);
+int iso_pages_fork(const int32_t* table, const int32_t* length, int64_t seqs, int64_t max_pages,
+                   const int32_t* refs, int64_t pages, int64_t page_size, const int32_t* parent,
+                   const int32_t* grow, int32_t grow_all, int64_t children, const iso_blocks* pools,
+                   int count, int32_t* new_table, int32_t* new_length, int32_t* new_refs,
+                   int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+size_t iso_pages_compact_workspace_bytes(int64_t pages);
+int iso_pages_compact(const int32_t* table, int64_t entries, const int32_t* refs, int64_t pages,
+                      const iso_blocks* pools, int count, int32_t* new_table, int32_t* new_refs,
+                      int32_t* moved, int32_t* status, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
 /* Bytes of device workspace iso_fit_ex needs for this shape and these flags
  * (weighted or not is part of the shape: pass ISO_F_WEIGHTED_HINT in flags
  * when w will be non-NULL).  Returns 0 for an empty or invalid shape. */

@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libiso.so")
 SOURCES = ["iso_api.hip", "iso_kernels.hip", "iso_merge.hip", "iso_copy.hip", "iso_vjp.hip",
-           "iso_calib.hip", "iso_logp.hip", "iso_losses.hip"]
+           "iso_calib.hip", "iso_logp.hip", "iso_losses.hip", "iso_beams.hip", "iso_pages.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

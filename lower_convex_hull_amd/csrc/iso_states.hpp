@@ -1,0 +1,74 @@
+// Arrays of states (iso_blocks in iso.h) as the kernels take them, their checks,
+// and bytes moved between blocks of any alignment.
+#pragma once
+
+#include "../../include/iso.h"
+#include "iso_losses.hpp"
+
+namespace iso {
+
+struct States {
+    iso_blocks b[ISO_MAX_BLOCKS];
+    int count;
+};
+
+// Bytes from the first to the last of `rows` rows' blocks, 0 for none, or -1:
+// counts or strides that are negative or too large, or blocks that overlap.
+inline int64_t blocks_extent(const iso_blocks& b, int64_t rows) {
+    if (b.outer < 0 || b.mid < 0 || b.inner < 0 || rows < 0) return -1;
+    if (b.outer > 0x7fffffffLL || b.mid > 0x7fffffffLL || b.inner > (1LL << 40)) return -1;
+    struct Dim {
+        int64_t n, stride;
+    } d[3] = {{b.outer, b.outer_stride}, {rows, b.row_stride}, {b.mid, b.mid_stride}};
+    for (const Dim& x : d)
+        if (x.n > 1 && x.stride < 0) return -1;
+    if (!b.outer || !b.mid || !b.inner || !rows) return 0;
+    // from the smallest stride on, each holds what is inside it
+    for (int i = 0; i < 2; ++i)
+        for (int k = 0; k < 2; ++k)
+            if (d[k].stride > d[k + 1].stride) {
+                const Dim t = d[k];
+                d[k] = d[k + 1];
+                d[k + 1] = t;
+            }
+    int64_t extent = b.inner;
+    for (const Dim& x : d) {
+        if (x.n <= 1) continue;
+        int64_t far;
+        if (x.stride < extent || __builtin_mul_overflow(x.stride, x.n - 1, &far) ||
+            __builtin_add_overflow(far, extent, &extent))
+            return -1;
+    }
+    return extent < (1LL << 62) ? extent : -1;
+}
+
+// The arrays of a call, those without bytes left out; false if one is not
+// right, or two overlap, or one overlaps one of `other`.
+template <int N>
+bool take_states(const iso_blocks* from, int count, int64_t rows, const Span (&other)[N], States& to) {
+    if (count < 0 || count > ISO_MAX_BLOCKS || (count && !from)) return false;
+    to = States{};
+    Span at[ISO_MAX_BLOCKS];
+    for (int i = 0; i < count; ++i) {
+        const int64_t bytes = blocks_extent(from[i], rows);
+        if (bytes < 0) return false;
+        if (!bytes) continue;
+        const Span s{from[i].base, (size_t)bytes};
+        if (!s.p) return false;
+        for (int k = 0; k < to.count; ++k)
+            if (overlap(s, at[k])) return false;
+        for (int k = 0; k < N; ++k)
+            if (overlap(s, other[k])) return false;
+        at[to.count] = s;
+        to.b[to.count++] = from[i];
+    }
+    return true;
+}
+
+// 16 bytes at any address: global loads and stores need no alignment.
+typedef uint32_t Wide16 __attribute__((ext_vector_type(4), aligned(1), may_alias));
+typedef uint64_t Wide8 __attribute__((aligned(1), may_alias));
+typedef uint32_t Wide4 __attribute__((aligned(1), may_alias));
+typedef uint16_t Wide2 __attribute__((aligned(1), may_alias));
+
+}  // namespace iso

@@ -6,9 +6,10 @@ library is missing: there is no fallback.
 
 Functions with the C names take raw device pointers (ints); ``fit``, ``vjp``,
 ``calib_curve`` and the loss operators ``token_logp``, ``token_logp_vjp``,
-``pref_loss``, ``policy_loss`` and ``policy_loss_logits`` are convenience
-wrappers over torch CUDA tensors that allocate the outputs and the workspace
-with torch.
+``pref_loss``, ``policy_loss`` and ``policy_loss_logits`` and the decoding steps
+``beam_select``, ``beam_reorder``, ``pages_fork`` and ``pages_compact`` are
+convenience wrappers over torch CUDA tensors that allocate the outputs and the
+workspace with torch.
 """
 from __future__ import annotations
 
@@ -59,7 +60,20 @@ EXPORTS = ("iso_fit", "iso_fit_ex", "iso_fit_noalloc", "iso_workspace_bytes", "i
            "iso_copy_probe", "iso_token_logp", "iso_token_logp_vjp", "iso_token_logp_workspace_bytes",
            "iso_pref_loss", "iso_pref_loss_workspace_bytes", "iso_policy_loss",
            "iso_policy_loss_workspace_bytes", "iso_policy_loss_logits",
-           "iso_policy_loss_logits_workspace_bytes")
+           "iso_policy_loss_logits_workspace_bytes", "iso_beam_select", "iso_beam_select_workspace_bytes",
+           "iso_beam_reorder", "iso_pages_fork", "iso_pages_fork_workspace_bytes", "iso_pages_compact",
+           "iso_pages_compact_workspace_bytes")
+
+ISO_MAX_BLOCKS = 16
+
+
+class Blocks(ctypes.Structure):
+    """iso_blocks: the blocks of an array that its rows (or pages) hold; strides in bytes."""
+
+    _fields_ = [("base", ctypes.c_void_p), ("outer", ctypes.c_int64), ("outer_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("mid", ctypes.c_int64), ("mid_stride", ctypes.c_int64),
+                ("inner", ctypes.c_int64)]
+
 
 _lib = None
 
@@ -124,6 +138,22 @@ def lib() -> ctypes.CDLL:
         L.iso_policy_loss_logits.restype = ctypes.c_int
         L.iso_policy_loss_logits_workspace_bytes.argtypes = [i64, i64, i64, i32]
         L.iso_policy_loss_logits_workspace_bytes.restype = sz
+        L.iso_beam_select.argtypes = [p, i32, i64, i64, i64, i64, p, p, p, ctypes.c_int32, f64, i64, p, p, p, p, p,
+                                      sz, p]
+        L.iso_beam_select.restype = ctypes.c_int
+        L.iso_beam_select_workspace_bytes.argtypes = [i64, i64, i64, i64, i32]
+        L.iso_beam_select_workspace_bytes.restype = sz
+        L.iso_beam_reorder.argtypes = [p, i32, p, i64, i64, p]
+        L.iso_beam_reorder.restype = ctypes.c_int
+        L.iso_pages_fork.argtypes = [p, p, i64, i64, p, i64, i64, p, p, ctypes.c_int32, i64, p, i32, p, p, p, p, p, sz,
+                                     p]
+        L.iso_pages_fork.restype = ctypes.c_int
+        L.iso_pages_fork_workspace_bytes.argtypes = [i64, i64, i64]
+        L.iso_pages_fork_workspace_bytes.restype = sz
+        L.iso_pages_compact.argtypes = [p, i64, p, i64, p, i32, p, p, p, p, p, sz, p]
+        L.iso_pages_compact.restype = ctypes.c_int
+        L.iso_pages_compact_workspace_bytes.argtypes = [i64]
+        L.iso_pages_compact_workspace_bytes.restype = sz
         L.iso_status_str.argtypes = [ctypes.c_int]
         L.iso_status_str.restype = ctypes.c_char_p
         L.iso_release.argtypes = []
@@ -248,6 +278,45 @@ def iso_policy_loss_logits(logits_ptr, dtype, rows, vocab, ld, target_ptr, tempe
 
 def iso_policy_loss_logits_workspace_bytes(rows, vocab, seqs, dtype) -> int:
     return lib().iso_policy_loss_logits_workspace_bytes(rows, vocab, seqs, dtype)
+
+
+def iso_beam_select(logits_ptr, dtype, batch, beams, vocab, ld, score_ptr, weight_ptr, ended_ptr, end_token,
+                    temperature, take, out_score_ptr, out_logp_ptr, out_parent_ptr, out_token_ptr, ws_ptr, ws_bytes,
+                    stream) -> int:
+    return lib().iso_beam_select(logits_ptr, dtype, batch, beams, vocab, ld, score_ptr, weight_ptr, ended_ptr,
+                                 end_token, temperature, take, out_score_ptr, out_logp_ptr, out_parent_ptr,
+                                 out_token_ptr, ws_ptr, ws_bytes, stream)
+
+
+def iso_beam_select_workspace_bytes(batch, beams, vocab, take, dtype) -> int:
+    return lib().iso_beam_select_workspace_bytes(batch, beams, vocab, take, dtype)
+
+
+def iso_beam_reorder(states, count, parent_ptr, batch, beams, stream) -> int:
+    """states: a ctypes array of Blocks (here and below)."""
+    return lib().iso_beam_reorder(states, count, parent_ptr, batch, beams, stream)
+
+
+def iso_pages_fork(table_ptr, length_ptr, seqs, max_pages, refs_ptr, pages, page_size, parent_ptr, grow_ptr, grow_all,
+                   children, pools, count, new_table_ptr, new_length_ptr, new_refs_ptr, status_ptr, ws_ptr, ws_bytes,
+                   stream) -> int:
+    return lib().iso_pages_fork(table_ptr, length_ptr, seqs, max_pages, refs_ptr, pages, page_size, parent_ptr,
+                                grow_ptr, grow_all, children, pools, count, new_table_ptr, new_length_ptr,
+                                new_refs_ptr, status_ptr, ws_ptr, ws_bytes, stream)
+
+
+def iso_pages_fork_workspace_bytes(seqs, children, pages) -> int:
+    return lib().iso_pages_fork_workspace_bytes(seqs, children, pages)
+
+
+def iso_pages_compact(table_ptr, entries, refs_ptr, pages, pools, count, new_table_ptr, new_refs_ptr, moved_ptr,
+                      status_ptr, ws_ptr, ws_bytes, stream) -> int:
+    return lib().iso_pages_compact(table_ptr, entries, refs_ptr, pages, pools, count, new_table_ptr, new_refs_ptr,
+                                   moved_ptr, status_ptr, ws_ptr, ws_bytes, stream)
+
+
+def iso_pages_compact_workspace_bytes(pages) -> int:
+    return lib().iso_pages_compact_workspace_bytes(pages)
 
 
 def iso_workspace_bytes(rows, n, flags=0) -> int:
@@ -605,3 +674,160 @@ def policy_loss_logits(logits, target, old_logp, adv, *, ref_logp=None, seq_off=
                                        logp.data_ptr(), gptr, gld, grad_scale, wptr, nb, c.handle,
                                        _policy_flags(seq_mean, token_adv)))
     return loss, counts, logp, g
+
+
+def beam_select(logits, score, *, take=None, weight=None, ended=None, end_token: int = -1,
+                temperature: float = 1.0, stream=None):
+    """The best continuations of each batch item's beams: (scores, log-probabilities,
+    parents, tokens), each (batch, take) and in order; parents are rows of logits.
+    logits: 2-D f32, f16 or bf16, row b * beams + k the beam k of item b; score:
+    (batch, beams) f32; weight: its rank's factor, shaped like score; ended: bool
+    or uint8, shaped like score; take: as many as beams, if not given."""
+    c = _Launch(logits, stream)
+    t = c.torch
+    ptr, code, rows, vocab, ld = c.logits(logits, "logits")
+    if score.dim() != 2 or score.shape[0] * score.shape[1] != rows:
+        raise ValueError("score must have the shape (batch, beams), logits batch * beams rows")
+    batch, beams = score.shape
+    take = beams if take is None else take
+    sc, wt = c.use(score, "score", score.shape, (t.float32,)), c.use(weight, "weight", score.shape, (t.float32,))
+    en = c.use(ended, "ended", score.shape, (t.bool, t.uint8))
+    if not 1 <= take <= 128:
+        raise ValueError("take must be from 1 to 128")
+    out, logp = c.new(t.float32, batch, take), c.new(t.float32, batch, take)
+    parent, token = c.new(t.int32, batch, take), c.new(t.int32, batch, take)
+    nb = c.lib.iso_beam_select_workspace_bytes(batch, beams, vocab, take, code)
+    ws, wptr = c.workspace(nb)
+    _done(c.lib.iso_beam_select(ptr, code, batch, beams, vocab, ld, sc, wt, en, end_token, temperature, take,
+                                out.data_ptr(), logp.data_ptr(), parent.data_ptr(), token.data_ptr(), wptr, nb,
+                                c.handle))
+    return out, logp, parent, token
+
+
+def _joined(shape, stride):
+    """(count, stride) of dimensions taken as one, None if they are not one; those of size 1 do not count."""
+    n, step = 1, 0
+    for size, by in zip(shape, stride):
+        if size == 1:
+            continue
+        if n > 1 and step != size * by:
+            return None
+        n, step = n * size, by
+    return n, step
+
+
+def _blocks(launch, tensors, dims, token_dim=None):
+    """(array of Blocks, count) of tensors whose rows (or pages) are dimension
+    `dim`, with the sizes of those dimensions.  What lies behind a row is blocks
+    of adjacent elements at one stride: from `token_dim` on, or as long as they get."""
+    tensors = (tensors,) if hasattr(tensors, "data_ptr") else tuple(tensors)
+    dims = (dims,) * len(tensors) if isinstance(dims, int) else tuple(dims)
+    if len(dims) != len(tensors):
+        raise ValueError("one dimension for each tensor")
+    if len(tensors) > ISO_MAX_BLOCKS:
+        raise ValueError(f"at most {ISO_MAX_BLOCKS} tensors a call")
+    out, sizes = (Blocks * max(1, len(tensors)))(), []
+    for i, (t, dim) in enumerate(zip(tensors, dims)):
+        if t.get_device() != launch.index:
+            raise TypeError(f"every tensor must be on {launch.dev}")
+        if not 0 <= dim < t.dim():
+            raise ValueError(f"a tensor of shape {tuple(t.shape)} has no dimension {dim}")
+        shape, stride, size = t.shape, t.stride(), t.element_size()
+        at, inner = len(shape), 1
+        if token_dim is None:
+            while at > dim + 1 and (shape[at - 1] == 1 or stride[at - 1] == inner):
+                at -= 1
+                inner *= shape[at]
+        else:
+            if not dim < token_dim < len(shape):
+                raise ValueError("token_dim must be behind page_dim")
+            while at > token_dim:
+                at -= 1
+                if shape[at] != 1 and stride[at] != inner:
+                    raise ValueError("a page's tokens must be adjacent from token_dim on")
+                inner *= shape[at]
+        outer, mid = _joined(shape[:dim], stride[:dim]), _joined(shape[dim + 1:at], stride[dim + 1:at])
+        if outer is None or mid is None:
+            raise ValueError("the dimensions before the rows, and those behind them, must have one stride")
+        sizes.append(shape[dim])
+        b = out[i]
+        b.base, b.inner, b.row_stride = t.data_ptr(), inner * size, stride[dim] * size
+        (b.outer, b.outer_stride), (b.mid, b.mid_stride) = (outer[0], outer[1] * size), (mid[0], mid[1] * size)
+        if launch.other is not None:
+            t.record_stream(launch.other)
+    return out, len(tensors), sizes
+
+
+def beam_reorder(states, parent, *, dim=0, stream=None):
+    """States of beams in the order of their parents, in place: row r of each
+    becomes what row parent[r] was.  states: a tensor or several, of any type,
+    whose dimension `dim` (one for all, or one each) holds the rows; parent:
+    (batch, beams) int32 as beam_select gives, rows of the same item (any other
+    value: the row stays).  Returns states."""
+    c = _Launch(parent, stream)
+    if parent.dim() != 2:
+        raise ValueError("parent must have the shape (batch, beams)")
+    pr = c.use(parent, "parent", parent.shape, (c.torch.int32,))
+    batch, beams = parent.shape
+    blocks, count, sizes = _blocks(c, states, dim)
+    if any(n != batch * beams for n in sizes):
+        raise ValueError("each state must have batch * beams rows")
+    _done(c.lib.iso_beam_reorder(blocks, count, pr, batch, beams, c.handle))
+    return states
+
+
+def pages_fork(table, length, refs, parent, *, page_size: int, grow=1, pools=(), page_dim: int = 0,
+               token_dim: int = 1, stream=None):
+    """One step of a paged cache: (table, length, refs, status), the cache after
+    it.  Child i goes on from sequence parent[i] (none: -1) with room for grow
+    more tokens (an int, or int32 shaped like parent); sequences without a child
+    are freed.  table: (sequences, max_pages) int32; length, refs, parent: 1-D
+    int32.  pools: the tensors of the pages' tokens, pages at dimension page_dim,
+    a page's tokens at token_dim.  status (int32): pages lacking, children too
+    long (nothing is done if either is not 0), pages copied, taken, left free."""
+    c = _Launch(table, stream)
+    t = c.torch
+    i32 = (t.int32,)
+    if table.dim() != 2 or refs.dim() != 1 or parent.dim() != 1:
+        raise ValueError("table must be 2-D, refs and parent 1-D")
+    seqs, most = table.shape
+    tb, ln = c.use(table, "table", table.shape, i32), c.use(length, "length", (seqs,), i32)
+    rf, pr = c.use(refs, "refs", refs.shape, i32), c.use(parent, "parent", parent.shape, i32)
+    pages, children = refs.shape[0], parent.shape[0]
+    each, gr = (grow, None) if isinstance(grow, int) else (0, c.use(grow, "grow", parent.shape, i32))
+    blocks, count, sizes = _blocks(c, pools, page_dim, token_dim)
+    if any(n != pages for n in sizes):
+        raise ValueError("each pool must have as many pages as refs")
+    for p in ((pools,) if hasattr(pools, "data_ptr") else pools):
+        if p.shape[token_dim] != page_size:
+            raise ValueError("each pool must have page_size tokens a page")
+    new_table, new_length = c.new(t.int32, children, most), c.new(t.int32, children)
+    new_refs, status = c.new(t.int32, pages), c.new(t.int32, 5)
+    nb = c.lib.iso_pages_fork_workspace_bytes(seqs, children, pages)
+    ws, wptr = c.workspace(nb)
+    _done(c.lib.iso_pages_fork(tb, ln, seqs, most, rf, pages, page_size, pr, gr, each, children, blocks, count,
+                               new_table.data_ptr(), new_length.data_ptr(), new_refs.data_ptr(), status.data_ptr(),
+                               wptr, nb, c.handle))
+    return new_table, new_length, new_refs, status
+
+
+def pages_compact(table, refs, *, pools=(), page_dim: int = 0, stream=None):
+    """The live pages (refs > 0) of a paged cache moved together, in place in
+    the pools: (table, refs, moved, status), the cache after it; moved: where
+    each page is now (-1: free); status (int32): live pages, pages moved."""
+    c = _Launch(table, stream)
+    t = c.torch
+    if refs.dim() != 1:
+        raise ValueError("refs must be 1-D")
+    tb, rf = c.use(table, "table", table.shape, (t.int32,)), c.use(refs, "refs", refs.shape, (t.int32,))
+    pages = refs.shape[0]
+    blocks, count, sizes = _blocks(c, pools, page_dim)
+    if any(n != pages for n in sizes):
+        raise ValueError("each pool must have as many pages as refs")
+    new_table, new_refs = c.new(t.int32, *table.shape), c.new(t.int32, pages)
+    moved, status = c.new(t.int32, pages), c.new(t.int32, 2)
+    nb = c.lib.iso_pages_compact_workspace_bytes(pages)
+    ws, wptr = c.workspace(nb)
+    _done(c.lib.iso_pages_compact(tb, table.numel(), rf, pages, blocks, count, new_table.data_ptr(),
+                                  new_refs.data_ptr(), moved.data_ptr(), status.data_ptr(), wptr, nb, c.handle))
+    return new_table, new_refs, moved, status
