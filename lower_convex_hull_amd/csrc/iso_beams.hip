@@ -52,60 +52,138 @@ struct Beams {
     __device__ __forceinline__ bool has_ended(int64_t r) const { return ended && ended[r]; }
 };
 
+// A value t >= 1 that at least n of a wave's values (V a lane) reach, and few
+// more; 1 if less than n of them are not 0.
+template <int V>
+__device__ __forceinline__ uint32_t reached_by(const uint32_t (&v)[V], int n) {
+    uint32_t t = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t c = t | (1u << bit);
+        int count = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) count += __popcll(__ballot(v[i] >= c));
+        if (count >= n) {
+            t = c;
+            if (count <= n + n / 8) break;
+        }
+    }
+    return t ? t : 1u;
+}
+
+// Room for the values that reach a threshold; where more do, a round of a
+// maximum each finds the best.
+constexpr int kRoom = 1024;
+
 // Item = (row, piece of it), held in the registers of a workgroup: the piece's
-// maximum and sum, and its `take` best tokens, one round of a maximum each.
-template <typename T, int NT, int U>
+// maximum and sum, and its `take` best tokens.  A value that `take` threads'
+// maxima reach bounds the take-th best token from below; the few tokens that
+// reach it are brought into order by counting.
+template <typename T, int NT, int U, bool STREAM>
 __global__ __launch_bounds__(NT) void k_beam_pieces(const T* __restrict__ logits, int64_t rows, int vocab, int64_t ld,
                                                     Beams b, Scale sc, int splits, uint64_t* __restrict__ keys,
                                                     PieceSum* __restrict__ sums) {
     constexpr int N = Wide<T>::N, kWaves = NT / 64;
-    __shared__ uint64_t red[kWaves];
+    __shared__ uint64_t room[kRoom];
+    __shared__ uint32_t most[NT];
     __shared__ double red_sum[kWaves];
-    const int wave = threadIdx.x >> 6;
+    __shared__ float red[kWaves];
+    __shared__ uint32_t bound;
+    __shared__ int count;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     for (int64_t item = blockIdx.x; item < rows * splits; item += gridDim.x) {
         const int64_t r = item / splits;
         if (!b.counts(r) || b.has_ended(r)) continue;
         const T* x = logits + r * ld;
         const Piece<T> w(x, (int)(item - r * splits), Chunk<T, NT, U>::kSize, vocab);
         Chunk<T, NT, U> c;
-        c.load(x, w.from, w.to);
+        c.template load<STREAM>(x, w.from, w.to);
         const int ke = w.edge();
         const float xe = ke >= 0 ? (float)x[ke] : -INFINITY;
-        uint64_t last = ~0ull;
-        float m = -INFINITY;
-        for (int i = 0; i < b.take; ++i) {
-            uint64_t best = token_key(xe, ke);
-            if (best >= last) best = 0;
+        float top[U], m = xe;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            top[u] = (float)c.v[u][0];
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const uint64_t k = token_key((float)c.v[u][j], c.at(w.from, u) + j);
-                    best = k < last && k > best ? k : best;
-                }
-            best = wave_max(best);
-            if ((threadIdx.x & 63) == 0) red[wave] = best;
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < kWaves; ++k) best = red[k] > best ? red[k] : best;
-            __syncthreads();
-            if (i == 0 && best) m = key_logit(best);
-            if (threadIdx.x == 0) keys[item * b.take + i] = best;
-            last = best;  // 0: nothing is below it
+            for (int j = 1; j < N; ++j) top[u] = fmaxf(top[u], (float)c.v[u][j]);
+            m = fmaxf(m, top[u]);
         }
-        const float base = m == -INFINITY ? 0.0f : m;
+        most[threadIdx.x] = m > -INFINITY ? ordered(m) : 0;
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+        if (lane == 0) red[wave] = m;
+        if (threadIdx.x == 0) count = 0;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kWaves; ++k) m = fmaxf(m, red[k]);
+        if (wave == 0) {
+            uint32_t v[kWaves];
+#pragma unroll
+            for (int k = 0; k < kWaves; ++k) v[k] = most[k * 64 + lane];
+            const uint32_t t = reached_by(v, b.take);
+            if (lane == 0) bound = t;
+        }
+        const float base = base_of(m);
+        c.forget();
         double s = (double)__builtin_amdgcn_exp2f((xe - base) * sc.cf);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < N; ++j) s += (double)__builtin_amdgcn_exp2f(((float)c.v[u][j] - base) * sc.cf);
+        c.forget();
         s = wg_sum<NT>(s, red_sum);
         if (threadIdx.x == 0) sums[item] = PieceSum{(double)m, s};
+        // every number reaches the lowest one
+        const float low = bound == 1u ? -3.402823466e38f : unordered(bound);
+        auto put = [&](float v, int at) {
+            if (v >= low) {
+                const int p = atomicAdd(&count, 1);
+                if (p < kRoom) room[p] = token_key(v, at);
+            }
+        };
+        put(xe, ke);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (top[u] >= low) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) put((float)c.v[u][j], c.at(w.from, u) + j);
+            }
+        __syncthreads();
+        const int found = count;
+        uint64_t* out = keys + item * b.take;
+        if (found <= kRoom) {
+            for (int i = threadIdx.x; i < found; i += NT) {
+                const uint64_t k = room[i];
+                int rank = 0;
+                for (int j = 0; j < found; ++j) rank += room[j] > k;
+                if (rank < b.take) out[rank] = k;
+            }
+            for (int i = found + threadIdx.x; i < b.take; i += NT) out[i] = 0;
+        } else {
+            uint64_t last = ~0ull;
+            for (int i = 0; i < b.take; ++i) {
+                uint64_t best = token_key(xe, ke);
+                if (best >= last) best = 0;
+#pragma unroll 1
+                for (int k = w.from + (int)threadIdx.x; k < w.to; k += NT) {
+                    const uint64_t y = token_key((float)x[k], k);
+                    best = y < last && y > best ? y : best;
+                }
+                best = wave_max(best);
+                __syncthreads();
+                if (lane == 0) room[wave] = best;
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < kWaves; ++k) best = room[k] > best ? room[k] : best;
+                if (threadIdx.x == 0) out[i] = best;
+                last = best;  // 0: nothing is below it
+            }
+        }
+        __syncthreads();  // the shared arrays are used again
     }
 }
 
-// A batch item: its rows' log-sums, then its best candidates, one round of a
-// maximum each, by (rank, lower beam; logit, lower token).
+// A batch item: its rows' log-sums, then its best candidates by (rank, lower
+// beam; logit, lower token), found as in a piece.
 struct Cand {
     uint64_t hi, lo;
     __device__ __forceinline__ bool over(const Cand& o) const { return hi > o.hi || (hi == o.hi && lo > o.lo); }
@@ -113,21 +191,30 @@ struct Cand {
 struct RowSum {
     double m, log_s, score, weight;
     int state;  // 0: no candidates, 1: its tokens, 2: itself
+    __device__ __forceinline__ double logp(uint64_t key, double inv_t) const {
+        return state == 2 ? 0.0 : ((double)key_logit(key) - m) * inv_t - log_s;
+    }
+};
+struct SelectOut {
+    float *score, *logp;
+    int32_t *parent, *token;
 };
 constexpr int kJoinNT = 256;
 __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, Scale sc, int splits,
                                                        const uint64_t* __restrict__ keys,
-                                                       const PieceSum* __restrict__ sums, float* __restrict__ out_score,
-                                                       float* __restrict__ out_logp, int32_t* __restrict__ out_parent,
-                                                       int32_t* __restrict__ out_token) {
+                                                       const PieceSum* __restrict__ sums, SelectOut o) {
+    constexpr int kWaves = kJoinNT / 64;
     __shared__ RowSum row[kMaxBeams];
-    __shared__ Cand red[kJoinNT / 64];
+    __shared__ Cand room[kRoom];
+    __shared__ uint32_t most[kJoinNT];
+    __shared__ uint32_t bound;
+    __shared__ int count;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int64_t item = blockIdx.x; item < batch; item += gridDim.x) {
-        for (int k = wave; k < b.beams; k += kJoinNT / 64) {
+        for (int k = wave; k < b.beams; k += kWaves) {
             const int64_t r = item * b.beams + k;
-            RowSum o{0.0, 0.0, (double)b.score[r], b.weight ? (double)b.weight[r] : 1.0, 0};
-            if (b.counts(r) && b.has_ended(r)) o.state = 2;
+            RowSum a{0.0, 0.0, (double)b.score[r], b.weight ? (double)b.weight[r] : 1.0, 0};
+            if (b.counts(r) && b.has_ended(r)) a.state = 2;
             else if (b.counts(r)) {
                 double m = -INFINITY;
                 for (int p = lane; p < splits; p += 64) m = fmax(m, sums[r * splits + p].m);
@@ -135,69 +222,105 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
                 for (int d = 32; d > 0; d >>= 1) m = fmax(m, __shfl_xor(m, d));
                 double s = 0.0;
                 for (int p = lane; p < splits; p += 64) {
-                    const PieceSum a = sums[r * splits + p];
-                    s += a.m == -INFINITY ? a.s : a.s * exp((a.m - m) * sc.inv_t);
+                    const PieceSum q = sums[r * splits + p];
+                    s += q.m == -INFINITY ? q.s : q.s * exp((q.m - m) * sc.inv_t);
                 }
                 s = wave_sum(s);
                 if (s > 0.0 && s < INFINITY) {
-                    o.m = m;
-                    o.log_s = log(s);
-                    o.state = 1;
+                    a.m = m;
+                    a.log_s = log(s);
+                    a.state = 1;
                 }
             }
-            if (lane == 0) row[k] = o;
+            if (lane == 0) row[k] = a;
+        }
+        if (threadIdx.x == 0) count = 0;
+        __syncthreads();
+        const int each = splits * b.take;
+        const int64_t all = (int64_t)b.beams * each;
+        const uint64_t* key = keys + item * all;
+        // candidate e; hi is 0 where there is none
+        auto cand = [&](int64_t e) {
+            const int k = (int)((uint32_t)e / (uint32_t)each);
+            const RowSum& a = row[k];
+            if (a.state == 0 || (a.state == 2 && e != (int64_t)k * each)) return Cand{0, 0};
+            const uint64_t x = a.state == 2 ? 0 : key[e];
+            if (a.state == 1 && !x) return Cand{0, 0};
+            const float rank = (float)((a.score + a.logp(x, sc.inv_t)) * a.weight);
+            if (!(rank > -INFINITY)) return Cand{0, 0};
+            return Cand{((uint64_t)ordered(rank) << 32) | (uint32_t)(kMaxBeams - k), x};
+        };
+        auto write = [&](int i, const Cand& c) {
+            const int64_t at = item * b.take + i;
+            const bool none = !c.hi;
+            const int k = none ? 0 : kMaxBeams - (int)(uint32_t)c.hi;
+            const RowSum& a = row[k];
+            const double logp = a.logp(c.lo, sc.inv_t);
+            o.score[at] = none ? -INFINITY : (float)(a.score + logp);
+            o.logp[at] = none ? -INFINITY : (float)logp;
+            o.parent[at] = none ? -1 : (int32_t)(item * b.beams + k);
+            o.token[at] = none ? -1 : a.state == 2 ? b.end_token : key_token(c.lo);
+        };
+        uint32_t mine = 0;
+        for (int64_t e = threadIdx.x; e < all; e += kJoinNT) mine = max(mine, (uint32_t)(cand(e).hi >> 32));
+        most[threadIdx.x] = mine;
+        __syncthreads();
+        if (wave == 0) {
+            uint32_t v[kWaves];
+#pragma unroll
+            for (int k = 0; k < kWaves; ++k) v[k] = most[k * 64 + lane];
+            const uint32_t t = reached_by(v, b.take);
+            if (lane == 0) bound = t;
         }
         __syncthreads();
-        Cand last{~0ull, ~0ull};
-        const int each = splits * b.take;
-        for (int i = 0; i < b.take; ++i) {
-            Cand best{0, 0};
-            for (int64_t e = threadIdx.x; e < (int64_t)b.beams * each; e += kJoinNT) {
-                const int k = (int)(e / each);
-                const RowSum& o = row[k];
-                if (o.state == 0 || (o.state == 2 && e - (int64_t)k * each)) continue;
-                const uint64_t key = o.state == 2 ? 0 : keys[item * b.beams * each + e];
-                if (o.state == 1 && !key) continue;
-                const double logp = o.state == 2 ? 0.0 : ((double)key_logit(key) - o.m) * sc.inv_t - o.log_s;
-                const float rank = (float)((o.score + logp) * o.weight);
-                if (!(rank > -INFINITY)) continue;
-                const Cand c{((uint64_t)ordered(rank) << 32) | (uint32_t)(kMaxBeams - k), key};
-                if (last.over(c) && c.over(best)) best = c;
-            }
-#pragma unroll
-            for (int d = 32; d > 0; d >>= 1) {
-                const Cand o{(uint64_t)__shfl_xor((unsigned long long)best.hi, d),
-                             (uint64_t)__shfl_xor((unsigned long long)best.lo, d)};
-                if (o.over(best)) best = o;
-            }
-            if (lane == 0) red[wave] = best;
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < kJoinNT / 64; ++k)
-                if (red[k].over(best)) best = red[k];
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                const int64_t at = item * b.take + i;
-                if (best.hi) {
-                    const int k = kMaxBeams - (int)(uint32_t)best.hi;
-                    const RowSum& o = row[k];
-                    const double logp = o.state == 2 ? 0.0 : ((double)key_logit(best.lo) - o.m) * sc.inv_t - o.log_s;
-                    out_score[at] = (float)(o.score + logp);
-                    out_logp[at] = (float)logp;
-                    out_parent[at] = (int32_t)(item * b.beams + k);
-                    out_token[at] = o.state == 2 ? b.end_token : key_token(best.lo);
-                } else {
-                    out_score[at] = out_logp[at] = -INFINITY;
-                    out_parent[at] = out_token[at] = -1;
+        if (mine >= bound) {
+            for (int64_t e = threadIdx.x; e < all; e += kJoinNT) {
+                const Cand c = cand(e);
+                if ((uint32_t)(c.hi >> 32) >= bound) {
+                    const int p = atomicAdd(&count, 1);
+                    if (p < kRoom) room[p] = c;
                 }
             }
-            last = best;
         }
-        __syncthreads();  // row is used again
+        __syncthreads();
+        const int found = count;
+        if (found <= kRoom) {
+            for (int i = threadIdx.x; i < found; i += kJoinNT) {
+                const Cand c = room[i];
+                int rank = 0;
+                for (int j = 0; j < found; ++j) rank += room[j].over(c);
+                if (rank < b.take) write(rank, c);
+            }
+            for (int i = found + threadIdx.x; i < b.take; i += kJoinNT) write(i, Cand{0, 0});
+        } else {
+            Cand last{~0ull, ~0ull};
+            for (int i = 0; i < b.take; ++i) {
+                Cand best{0, 0};
+                for (int64_t e = threadIdx.x; e < all; e += kJoinNT) {
+                    const Cand c = cand(e);
+                    if (last.over(c) && c.over(best)) best = c;
+                }
+#pragma unroll
+                for (int d = 32; d > 0; d >>= 1) {
+                    const Cand c{(uint64_t)__shfl_xor((unsigned long long)best.hi, d),
+                                 (uint64_t)__shfl_xor((unsigned long long)best.lo, d)};
+                    if (c.over(best)) best = c;
+                }
+                __syncthreads();
+                if (lane == 0) room[wave] = best;
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < kWaves; ++k)
+                    if (room[k].over(best)) best = room[k];
+                if (threadIdx.x == 0) write(i, best);
+                last = best;
+            }
+        }
+        __syncthreads();  // the shared arrays are used again
     }
 }
 
-constexpr int kPieceNT = 256, kPieceU = 4;
+constexpr int kPieceNT = 256, kPieceU = 8;
 struct SelectPlan {
     int splits;
     size_t off_sums, bytes;
@@ -217,46 +340,77 @@ bool select_sizes_ok(int64_t batch, int64_t beams, int64_t vocab, int64_t take, 
            vocab <= (1LL << 30) && batch <= 0x7fffffffLL / beams && dtype >= ISO_DT_F32 && dtype <= ISO_DT_BF16;
 }
 
-// Item = (array, batch item, outer, 256 vectors of 16 bytes): a thread has one
-// column of them through all rows of the item, and reads what rows come from
-// before it writes any.
-constexpr int kReorderNT = 256;
-template <typename V>
-__device__ void reorder_column(char* at, int64_t row_stride, const int32_t* from, int beams) {
-    V v[kMaxBeams];
-    for (int k = 0; k < beams; ++k)
-        if (from[k] >= 0) v[k] = *reinterpret_cast<const V*>(at + from[k] * row_stride);
-    for (int k = 0; k < beams; ++k)
-        if (from[k] >= 0) *reinterpret_cast<V*>(at + k * row_stride) = v[k];
+// A workgroup takes 2^`shift` columns of 16 bytes through all rows of a batch
+// item: it reads what the moved rows come from, waits until all of it has come,
+// and only then writes.  No other workgroup reads or writes there, so rows may
+// come from each other.  What 16 bytes leave over of each block is a last
+// column, taken apart: its width is the same for all.
+constexpr int kReorderNT = 256, kReorderU = 8;
+struct Moves {
+    int32_t to[kMaxBeams], from[kMaxBeams];
+    int n;
+};
+template <bool TAIL, int U>
+__device__ __forceinline__ void reorder_columns(const iso_blocks& s, char* base, const Moves& mv, int shift) {
+    const uint32_t whole = (uint32_t)(s.inner / 16), cols = TAIL ? 1 : whole, all = (uint32_t)s.mid * cols;
+    const int width = TAIL ? (int)(s.inner % 16) : 16;
+    if (TAIL) base += (int64_t)whole * 16;
+    // col / cols: the product is off by less than 2^-51 of itself, its distance from a
+    // whole number is at least 0.5 / cols; in registers a third of a division's
+    const double part = 1.0 / (double)cols;
+    for (uint32_t first = blockIdx.x << shift; first < all; first += gridDim.x << shift) {
+        Quad v[U];
+        char* put[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t unit = u * kReorderNT + threadIdx.x, k = unit >> shift;
+            const uint32_t col = first + (unit & ((1u << shift) - 1));
+            put[u] = nullptr;
+            if ((int)k < mv.n && col < all) {
+                const uint32_t m = TAIL ? col : (uint32_t)(((double)col + 0.5) * part), c = TAIL ? 0 : col - m * cols;
+                char* at = base + m * s.mid_stride + (int64_t)c * 16;
+                put[u] = at + mv.to[k] * s.row_stride;
+                v[u] = load_bytes(at + mv.from[k] * s.row_stride, width);
+            }
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (put[u]) store_bytes(put[u], width, v[u]);
+    }
 }
 __global__ __launch_bounds__(kReorderNT) void k_beam_reorder(States st, const int32_t* __restrict__ parent,
-                                                             int64_t batch, int beams) {
-    __shared__ int32_t from[kMaxBeams];
+                                                             uint32_t batch, int beams, int shift) {
+    __shared__ Moves mv;
+    __shared__ int count[2];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int i = 0; i < st.count; ++i) {
-        const iso_blocks& s = st.b[i];
-        const int64_t cols = (s.inner + 15) / 16, tiles = (s.mid * cols + kReorderNT - 1) / kReorderNT;
-        const int64_t items = batch * s.outer * tiles;
-        for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-            const int64_t b = item / (s.outer * tiles), o = item / tiles % s.outer, t = item % tiles;
+        const iso_blocks s = st.b[i];
+        const uint32_t outer = (uint32_t)s.outer, all = (uint32_t)s.mid * (uint32_t)((s.inner + 15) / 16);
+        if (blockIdx.x << (shift - 3) >= all) continue;  // no column of either kind
+        for (uint32_t item = blockIdx.y; item < batch * outer; item += gridDim.y) {
+            const uint32_t b = item / outer, o = item - b * outer;
+            // the rows that move
+            int64_t p = -1;
+            if ((int)threadIdx.x < beams) p = (int64_t)parent[b * (uint32_t)beams + threadIdx.x] - (int64_t)b * beams;
+            const bool moves = p >= 0 && p < beams && p != (int)threadIdx.x;
+            const uint64_t mask = __ballot(moves);
+            if (lane == 0 && wave < 2) count[wave] = __popcll(mask);
             __syncthreads();
-            if (threadIdx.x < beams) {
-                const int64_t p = (int64_t)parent[b * beams + threadIdx.x] - b * beams;
-                from[threadIdx.x] = p >= 0 && p < beams && p != (int)threadIdx.x ? (int32_t)p : -1;
+            if (moves) {
+                const int at = (wave ? count[0] : 0) + __popcll(mask & ((1ull << lane) - 1));
+                mv.to[at] = (int32_t)threadIdx.x;
+                mv.from[at] = (int32_t)p;
             }
+            if (threadIdx.x == 0) mv.n = count[0] + count[1];
             __syncthreads();
-            const int64_t col = t * kReorderNT + threadIdx.x;
-            if (col >= s.mid * cols) continue;
-            const int64_t m = col / cols, c = col % cols;
-            char* at = static_cast<char*>(s.base) + o * s.outer_stride + b * beams * s.row_stride + m * s.mid_stride + c * 16;
-            const int left = (int)(s.inner - c * 16 < 16 ? s.inner - c * 16 : 16);
-            if (left == 16) {
-                reorder_column<Wide16>(at, s.row_stride, from, beams);
-                continue;
+            if (mv.n) {
+                char* base = static_cast<char*>(s.base) + o * s.outer_stride + (int64_t)b * beams * s.row_stride;
+                reorder_columns<false, kReorderU>(s, base, mv, shift);
+                if (s.inner % 16) reorder_columns<true, 1>(s, base, mv, shift - 3);
             }
-            if (left & 8) reorder_column<Wide8>(at, s.row_stride, from, beams);
-            if (left & 4) reorder_column<Wide4>(at + (left & 8), s.row_stride, from, beams);
-            if (left & 2) reorder_column<Wide2>(at + (left & 12), s.row_stride, from, beams);
-            if (left & 1) reorder_column<uint8_t>(at + (left & 14), s.row_stride, from, beams);
+            __syncthreads();  // the list is used again
         }
     }
 }
@@ -299,12 +453,12 @@ int iso_beam_select(const void* logits, int dtype, int64_t batch, int64_t beams,
     const int64_t items = rows * pl.splits;
     by_dtype(dtype, [&](auto v) {
         typedef decltype(v) T;
-        hipLaunchKernelGGL((k_beam_pieces<T, kPieceNT, kPieceU>), dim3((unsigned)(items < kMaxGrid ? items : kMaxGrid)),
+        hipLaunchKernelGGL((k_beam_pieces<T, kPieceNT, kPieceU, false>), dim3((unsigned)(items < kMaxGrid ? items : kMaxGrid)),
                            dim3(kPieceNT), 0, st, static_cast<const T*>(logits), rows, (int)vocab, ld, b, sc, pl.splits,
                            keys, sums);
     });
     hipLaunchKernelGGL(k_beam_join, dim3((unsigned)(batch < kMaxGrid ? batch : kMaxGrid)), dim3(kJoinNT), 0, st, batch, b,
-                       sc, pl.splits, keys, sums, out_score, out_logp, out_parent, out_token);
+                       sc, pl.splits, keys, sums, SelectOut{out_score, out_logp, out_parent, out_token});
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 
@@ -319,18 +473,21 @@ int iso_beam_reorder(const iso_blocks* states, int count, const int32_t* parent,
     if (rows && !parent) return ISO_ERR_ARG;
     if (!aligned(parent, 4)) return ISO_ERR_ARG;
     if (!st.count) return ISO_OK;
-    int64_t most = 1;
+    int shift = 0;  // a workgroup's loads go over the rows first
+    while (shift < 11 && (beams << (shift + 1)) <= kReorderNT * kReorderU) ++shift;
+    // columns of an array's rows, rows over its outer blocks: 31 bits each
+    int64_t tiles = 1, items = 1;
     for (int i = 0; i < st.count; ++i) {
         const iso_blocks& s = st.b[i];
         const int64_t cols = (s.inner + 15) / 16;
-        if (s.mid > (1LL << 40) / cols) return ISO_ERR_ARG;
-        const int64_t tiles = (s.mid * cols + kReorderNT - 1) / kReorderNT;
-        if (s.outer > (1LL << 40) / tiles || batch > (1LL << 60) / (s.outer * tiles)) return ISO_ERR_ARG;
-        const int64_t items = batch * s.outer * tiles;
-        most = items > most ? items : most;
+        if (cols > 0x7fffffffLL / s.mid || s.outer > 0x7fffffffLL / batch) return ISO_ERR_ARG;
+        const int64_t t = ((s.mid * cols - 1) >> shift) + 1;
+        tiles = t > tiles ? t : tiles;
+        items = batch * s.outer > items ? batch * s.outer : items;
     }
-    hipLaunchKernelGGL(k_beam_reorder, dim3((unsigned)(most < kMaxGrid ? most : kMaxGrid)), dim3(kReorderNT), 0,
-                       static_cast<hipStream_t>(stream), st, parent, batch, (int)beams);
+    const dim3 grid((unsigned)(tiles < 65536 ? tiles : 65536), (unsigned)(items < 16384 ? items : 16384));
+    hipLaunchKernelGGL(k_beam_reorder, grid, dim3(kReorderNT), 0, static_cast<hipStream_t>(stream), st, parent,
+                       (uint32_t)batch, (int)beams, shift);
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 

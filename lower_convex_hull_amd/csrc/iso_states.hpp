@@ -66,9 +66,35 @@ bool take_states(const iso_blocks* from, int count, int64_t rows, const Span (&o
 }
 
 // 16 bytes at any address: global loads and stores need no alignment.
+typedef uint32_t Quad __attribute__((ext_vector_type(4)));
 typedef uint32_t Wide16 __attribute__((ext_vector_type(4), aligned(1), may_alias));
 typedef uint64_t Wide8 __attribute__((aligned(1), may_alias));
 typedef uint32_t Wide4 __attribute__((aligned(1), may_alias));
 typedef uint16_t Wide2 __attribute__((aligned(1), may_alias));
+
+// The first `left` of 16 bytes, fewer than 16 as 8, 4, 2 and 1 of them.
+__device__ __forceinline__ Quad load_bytes(const char* at, int left) {
+    if (left >= 16) return *reinterpret_cast<const Wide16*>(at);
+    Quad v = {0, 0, 0, 0};
+    if (left & 8) {
+        const uint64_t x = *reinterpret_cast<const Wide8*>(at);
+        v.x = (uint32_t)x;
+        v.y = (uint32_t)(x >> 32);
+    }
+    if (left & 4) v.z = *reinterpret_cast<const Wide4*>(at + (left & 8));
+    if (left & 2) v.w = *reinterpret_cast<const Wide2*>(at + (left & 12));
+    if (left & 1) v.w |= (uint32_t) * reinterpret_cast<const uint8_t*>(at + (left & 14)) << 16;
+    return v;
+}
+__device__ __forceinline__ void store_bytes(char* at, int left, const Quad& v) {
+    if (left >= 16) {
+        *reinterpret_cast<Wide16*>(at) = v;
+        return;
+    }
+    if (left & 8) *reinterpret_cast<Wide8*>(at) = (uint64_t)v.y << 32 | v.x;
+    if (left & 4) *reinterpret_cast<Wide4*>(at + (left & 8)) = v.z;
+    if (left & 2) *reinterpret_cast<Wide2*>(at + (left & 12)) = (uint16_t)v.w;
+    if (left & 1) *reinterpret_cast<uint8_t*>(at + (left & 14)) = (uint8_t)(v.w >> 16);
+}
 
 }  // namespace iso
