@@ -3,6 +3,8 @@
 #include "iso_logits.hpp"
 #include "iso_states.hpp"
 
+#include <type_traits>
+
 namespace iso {
 namespace {
 
@@ -53,26 +55,66 @@ struct Beams {
 };
 
 // A value t >= 1 that at least n of a wave's values (V a lane) reach, and few
-// more; 1 if less than n of them are not 0.
-template <int V>
+// more; 1 if less than n of them are not 0.  Bits below LOW tell no two apart.
+template <int LOW, int V>
 __device__ __forceinline__ uint32_t reached_by(const uint32_t (&v)[V], int n) {
     uint32_t t = 0;
-    for (int bit = 31; bit >= 0; --bit) {
+    for (int bit = 31; bit >= LOW; --bit) {
         const uint32_t c = t | (1u << bit);
         int count = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) count += __popcll(__ballot(v[i] >= c));
         if (count >= n) {
             t = c;
-            if (count <= n + n / 8) break;
+            if (count <= n + n / 4) break;
         }
     }
     return t ? t : 1u;
 }
+// The bits of ordered() that a type's values leave alike.
+template <typename T>
+constexpr int kLowBits = std::is_same<T, float>::value ? 0 : std::is_same<T, __bf16>::value ? 16 : 13;
 
 // Room for the values that reach a threshold; where more do, a round of a
 // maximum each finds the best.
 constexpr int kRoom = 1024;
+
+// The terms exp2((x - m) c) of a piece's sum, m its maximum.  Vectors with a term
+// above 1/2 take the difference first, so that the largest term is 1, and are
+// summed in f64: where it is nearly all, logp is what the others add to it.
+// Other vectors take x c - b with b = fl(m c), one instruction for two, and their
+// few terms are summed in f32, which is off by no more than 2^-22 of themselves;
+// what b's rounding leaves is a factor of them all, near 1 while b is below 2^10:
+// two terms of its series do.  Past that every vector goes the first way.
+struct PieceTerms {
+    float base, cf, b, edge;
+    double rest;
+    __device__ __forceinline__ PieceTerms(float m, const Scale& sc) : base(m), cf(sc.cf) {
+        const double exact = (double)m * (double)cf;
+        const bool large = !(fabs(exact) < 0x1p10);
+        b = large ? 0.0f : (float)exact;
+        edge = large ? -INFINITY : -1.0f;
+        const double d = ((double)b - exact) * kLn2;  // below 2^-15
+        rest = large ? 0.0 : fma(0.5 * d, d, d) + 1.0;
+    }
+    __device__ __forceinline__ float near(float x) const { return __builtin_amdgcn_exp2f((x - base) * cf); }
+    template <int N>
+    __device__ __forceinline__ void add(const float (&x)[N], float top, double& s, double& far) const {
+        if ((top - base) * cf >= edge) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) s += (double)near(x[j]);
+        } else {
+            float e[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) e[j] = __builtin_amdgcn_exp2f(fmaf(x[j], cf, -b));
+#pragma unroll
+            for (int d = N / 2; d > 0; d >>= 1)
+#pragma unroll
+                for (int j = 0; j < d; ++j) e[j] += e[j + d];
+            far += (double)e[0];
+        }
+    }
+};
 
 // Item = (row, piece of it), held in the registers of a workgroup: the piece's
 // maximum and sum, and its `take` best tokens.  A value that `take` threads'
@@ -107,6 +149,7 @@ __global__ __launch_bounds__(NT) void k_beam_pieces(const T* __restrict__ logits
             for (int j = 1; j < N; ++j) top[u] = fmaxf(top[u], (float)c.v[u][j]);
             m = fmaxf(m, top[u]);
         }
+        c.forget();
         most[threadIdx.x] = m > -INFINITY ? ordered(m) : 0;
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
@@ -119,16 +162,20 @@ __global__ __launch_bounds__(NT) void k_beam_pieces(const T* __restrict__ logits
             uint32_t v[kWaves];
 #pragma unroll
             for (int k = 0; k < kWaves; ++k) v[k] = most[k * 64 + lane];
-            const uint32_t t = reached_by(v, b.take);
+            const uint32_t t = reached_by<kLowBits<T>>(v, b.take);
             if (lane == 0) bound = t;
         }
         const float base = base_of(m);
-        c.forget();
-        double s = (double)__builtin_amdgcn_exp2f((xe - base) * sc.cf);
+        const PieceTerms terms(base, sc);
+        double s = (double)terms.near(xe), far = 0.0;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            float y[N];
 #pragma unroll
-            for (int j = 0; j < N; ++j) s += (double)__builtin_amdgcn_exp2f(((float)c.v[u][j] - base) * sc.cf);
+            for (int j = 0; j < N; ++j) y[j] = (float)c.v[u][j];
+            terms.add(y, top[u], s, far);
+        }
+        s += far * terms.rest;
         c.forget();
         s = wg_sum<NT>(s, red_sum);
         if (threadIdx.x == 0) sums[item] = PieceSum{(double)m, s};
@@ -149,15 +196,16 @@ __global__ __launch_bounds__(NT) void k_beam_pieces(const T* __restrict__ logits
             }
         __syncthreads();
         const int found = count;
-        uint64_t* out = keys + item * b.take;
+        const int64_t lists = (int64_t)b.beams * splits;  // of a batch item: place i of list l at i * lists + l
+        uint64_t* out = keys + item / lists * lists * b.take + item % lists;
         if (found <= kRoom) {
             for (int i = threadIdx.x; i < found; i += NT) {
                 const uint64_t k = room[i];
                 int rank = 0;
                 for (int j = 0; j < found; ++j) rank += room[j] > k;
-                if (rank < b.take) out[rank] = k;
+                if (rank < b.take) out[rank * lists] = k;
             }
-            for (int i = found + threadIdx.x; i < b.take; i += NT) out[i] = 0;
+            for (int i = found + threadIdx.x; i < b.take; i += NT) out[i * lists] = 0;
         } else {
             uint64_t last = ~0ull;
             for (int i = 0; i < b.take; ++i) {
@@ -174,7 +222,7 @@ __global__ __launch_bounds__(NT) void k_beam_pieces(const T* __restrict__ logits
                 __syncthreads();
 #pragma unroll
                 for (int k = 0; k < kWaves; ++k) best = room[k] > best ? room[k] : best;
-                if (threadIdx.x == 0) out[i] = best;
+                if (threadIdx.x == 0) out[i * lists] = best;
                 last = best;  // 0: nothing is below it
             }
         }
@@ -199,18 +247,29 @@ struct SelectOut {
     float *score, *logp;
     int32_t *parent, *token;
 };
-constexpr int kJoinNT = 256;
+// Bound by the latency of its steps; a few of the threads' keys stay in registers.
+// Keys lie by place in their lists, then by list, so that the best of all are
+// spread over the threads.
+constexpr int kJoinNT = 1024, kJoinKeep = 4;
 __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, Scale sc, int splits,
                                                        const uint64_t* __restrict__ keys,
                                                        const PieceSum* __restrict__ sums, SelectOut o) {
-    constexpr int kWaves = kJoinNT / 64;
+    constexpr int kWaves = kJoinNT / 64, kGroups = kJoinNT / 4;
     __shared__ RowSum row[kMaxBeams];
     __shared__ Cand room[kRoom];
-    __shared__ uint32_t most[kJoinNT];
+    __shared__ uint32_t most[kGroups];
     __shared__ uint32_t bound;
     __shared__ int count;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t lists = (uint32_t)b.beams * (uint32_t)splits, all = lists * (uint32_t)b.take;
     for (int64_t item = blockIdx.x; item < batch; item += gridDim.x) {
+        const uint64_t* key = keys + item * all;
+        uint64_t kept[kJoinKeep];
+#pragma unroll
+        for (int i = 0; i < kJoinKeep; ++i) {
+            const uint32_t e = threadIdx.x + i * kJoinNT;
+            kept[i] = e < all ? key[e] : 0;
+        }
         for (int k = wave; k < b.beams; k += kWaves) {
             const int64_t r = item * b.beams + k;
             RowSum a{0.0, 0.0, (double)b.score[r], b.weight ? (double)b.weight[r] : 1.0, 0};
@@ -236,19 +295,24 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
         }
         if (threadIdx.x == 0) count = 0;
         __syncthreads();
-        const int each = splits * b.take;
-        const int64_t all = (int64_t)b.beams * each;
-        const uint64_t* key = keys + item * all;
-        // candidate e; hi is 0 where there is none
-        auto cand = [&](int64_t e) {
-            const int k = (int)((uint32_t)e / (uint32_t)each);
+        // candidate e with its key; hi is 0 where there is none
+        auto cand = [&](uint32_t e, uint64_t x) {
+            const uint32_t list = e % lists, k = list / (uint32_t)splits;
             const RowSum& a = row[k];
-            if (a.state == 0 || (a.state == 2 && e != (int64_t)k * each)) return Cand{0, 0};
-            const uint64_t x = a.state == 2 ? 0 : key[e];
-            if (a.state == 1 && !x) return Cand{0, 0};
+            const bool none = a.state == 1 ? !x : a.state == 0 || e != k * (uint32_t)splits;
+            if (none) return Cand{0, 0};
+            if (a.state == 2) x = 0;
             const float rank = (float)((a.score + a.logp(x, sc.inv_t)) * a.weight);
             if (!(rank > -INFINITY)) return Cand{0, 0};
             return Cand{((uint64_t)ordered(rank) << 32) | (uint32_t)(kMaxBeams - k), x};
+        };
+        auto each = [&](auto f) {
+#pragma unroll
+            for (int i = 0; i < kJoinKeep; ++i) {
+                const uint32_t e = threadIdx.x + i * kJoinNT;
+                if (e < all) f(cand(e, kept[i]));
+            }
+            for (uint32_t e = threadIdx.x + kJoinKeep * kJoinNT; e < all; e += kJoinNT) f(cand(e, key[e]));
         };
         auto write = [&](int i, const Cand& c) {
             const int64_t at = item * b.take + i;
@@ -262,25 +326,27 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
             o.token[at] = none ? -1 : a.state == 2 ? b.end_token : key_token(c.lo);
         };
         uint32_t mine = 0;
-        for (int64_t e = threadIdx.x; e < all; e += kJoinNT) mine = max(mine, (uint32_t)(cand(e).hi >> 32));
-        most[threadIdx.x] = mine;
+        each([&](const Cand& c) { mine = max(mine, (uint32_t)(c.hi >> 32)); });
+        uint32_t group = max(mine, (uint32_t)__shfl_xor((int)mine, 1));
+        group = max(group, (uint32_t)__shfl_xor((int)group, 2));
+        if ((threadIdx.x & 3) == 0) most[threadIdx.x >> 2] = group;
         __syncthreads();
         if (wave == 0) {
-            uint32_t v[kWaves];
+            uint32_t v[kGroups / 64];
 #pragma unroll
-            for (int k = 0; k < kWaves; ++k) v[k] = most[k * 64 + lane];
-            const uint32_t t = reached_by(v, b.take);
+            for (int k = 0; k < kGroups / 64; ++k) v[k] = most[k * 64 + lane];
+            const uint32_t t = reached_by<0>(v, b.take);
             if (lane == 0) bound = t;
         }
         __syncthreads();
-        if (mine >= bound) {
-            for (int64_t e = threadIdx.x; e < all; e += kJoinNT) {
-                const Cand c = cand(e);
-                if ((uint32_t)(c.hi >> 32) >= bound) {
+        const uint32_t low = bound;
+        if (mine >= low) {
+            each([&](const Cand& c) {
+                if ((uint32_t)(c.hi >> 32) >= low) {
                     const int p = atomicAdd(&count, 1);
                     if (p < kRoom) room[p] = c;
                 }
-            }
+            });
         }
         __syncthreads();
         const int found = count;
@@ -296,8 +362,8 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
             Cand last{~0ull, ~0ull};
             for (int i = 0; i < b.take; ++i) {
                 Cand best{0, 0};
-                for (int64_t e = threadIdx.x; e < all; e += kJoinNT) {
-                    const Cand c = cand(e);
+                for (uint32_t e = threadIdx.x; e < all; e += kJoinNT) {
+                    const Cand c = cand(e, key[e]);
                     if (last.over(c) && c.over(best)) best = c;
                 }
 #pragma unroll
@@ -337,7 +403,7 @@ SelectPlan select_plan(int64_t batch, int64_t beams, int64_t vocab, int64_t take
 
 bool select_sizes_ok(int64_t batch, int64_t beams, int64_t vocab, int64_t take, int dtype) {
     return batch >= 0 && beams >= 1 && beams <= kMaxBeams && take >= 1 && take <= kMaxTake && vocab >= 1 &&
-           vocab <= (1LL << 30) && batch <= 0x7fffffffLL / beams && dtype >= ISO_DT_F32 && dtype <= ISO_DT_BF16;
+           vocab <= (1LL << 30) && batch <= 0x7fffffffLL / beams && dtype >= ISO_DT_F32 && dtype <= ISO_DT_BF16;  // an item's keys: 2^31 at most
 }
 
 // A workgroup takes 2^`shift` columns of 16 bytes through all rows of a batch

@@ -10,8 +10,9 @@ U = 2.0 ** -24  # half a step of f32, relative
 def row_logp(x, temperature=1.0):
     """(logp, err) of a row of f64 logits: None where the row has no candidates.
     err: what the log-sum may be off by in units of U when its terms are f32 and
-    their sum f64: sum p (3 |z - zmax| + 2), a term's exponent rounded three times
-    (difference, constant, product) and its exp by two half steps."""
+    their sum f64: sum p (3 |z - zmax| + 5), a term's exponent rounded three times
+    (difference, constant, product), its exp by two half steps, and up to eight
+    terms summed in f32 first, three roundings in pairs."""
     with np.errstate(invalid="ignore", over="ignore"):
         z = x / temperature
         m = z.max()
@@ -20,7 +21,7 @@ def row_logp(x, temperature=1.0):
         e = np.exp(z - m)
         s = e.sum()
         d = np.where(e > 0, z - m, 0.0)
-        return (z - m) - np.log(s), float((e / s * (3 * np.abs(d) + 2)).sum())
+        return (z - m) - np.log(s), float((e / s * (3 * np.abs(d) + 5)).sum())
 
 
 def beam_select(x, score, take, weight=None, ended=None, end_token=-1, temperature=1.0):
