@@ -75,9 +75,27 @@ __device__ __forceinline__ uint32_t reached_by(const uint32_t (&v)[V], int n) {
 template <typename T>
 constexpr int kLowBits = std::is_same<T, float>::value ? 0 : std::is_same<T, __bf16>::value ? 16 : 13;
 
-// Room for the values that reach a threshold; where more do, a round of a
+// Room for the candidates that reach a bound; where more do, a round of a
 // maximum each finds the best.
 constexpr int kRoom = 1024;
+
+// How many of `found` keys in LDS are above k; the next 7 places hold keys that
+// are above none.
+template <typename K, typename F>
+__device__ __forceinline__ int rank_of(const K* room, int found, F above) {
+    int rank = 0;
+    for (int j = 0; j < found; j += 8)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rank += above(room[j + i]);
+    return rank;
+}
+
+// The larger of three; what it makes of a NaN does not matter here.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+    return d;
+}
 
 // The terms exp2((x - m) c) of a piece's sum, m its maximum.  Vectors with a term
 // above 1/2 take the difference first, so that the largest term is 1, and are
@@ -116,117 +134,148 @@ struct PieceTerms {
     }
 };
 
-// Item = (row, piece of it), held in the registers of a workgroup: the piece's
-// maximum and sum, and its `take` best tokens.  A value that `take` threads'
-// maxima reach bounds the take-th best token from below; the few tokens that
-// reach it are brought into order by counting.
+// A workgroup takes a piece of a row, held in its registers: the piece's maximum
+// and sum, and its `take` best tokens.  A value that `take` threads' maxima reach
+// bounds the take-th best token from below.  The few vectors that reach it go
+// through LDS, where a thread looks at each of their values; the values that
+// reach it are brought into order by counting.  A row with a NaN has no
+// candidates (its sum is NaN), whatever is found in it.
 template <typename T, int NT, int U, bool STREAM>
-__global__ __launch_bounds__(NT) void k_beam_pieces(const T* __restrict__ logits, int64_t rows, int vocab, int64_t ld,
-                                                    Beams b, Scale sc, int splits, uint64_t* __restrict__ keys,
+__global__ __launch_bounds__(NT, 5) void k_beam_pieces(const T* __restrict__ logits, uint32_t rows, int vocab, int64_t ld,
+                                                    Beams b, Scale sc, uint32_t splits, uint64_t* __restrict__ keys,
                                                     PieceSum* __restrict__ sums) {
-    constexpr int N = Wide<T>::N, kWaves = NT / 64;
-    __shared__ uint64_t room[kRoom];
+    typedef typename Wide<T>::A Vec;
+    constexpr int N = Wide<T>::N, kWaves = NT / 64, kVectors = kRoom / 2;
+    __shared__ uint64_t room[kRoom + 8];
+    __shared__ Vec vec[kVectors];
+    __shared__ int at[kVectors];
     __shared__ uint32_t most[NT];
     __shared__ double red_sum[kWaves];
     __shared__ float red[kWaves];
     __shared__ uint32_t bound;
-    __shared__ int count;
+    __shared__ int vectors, count;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    for (int64_t item = blockIdx.x; item < rows * splits; item += gridDim.x) {
-        const int64_t r = item / splits;
+    for (uint32_t r = blockIdx.x; r < rows; r += gridDim.x) {
         if (!b.counts(r) || b.has_ended(r)) continue;
-        const T* x = logits + r * ld;
-        const Piece<T> w(x, (int)(item - r * splits), Chunk<T, NT, U>::kSize, vocab);
-        Chunk<T, NT, U> c;
-        c.template load<STREAM>(x, w.from, w.to);
-        const int ke = w.edge();
-        const float xe = ke >= 0 ? (float)x[ke] : -INFINITY;
-        float top[U], m = xe;
+        for (uint32_t split = blockIdx.y; split < splits; split += gridDim.y) {
+            const T* x = logits + r * ld;
+            const Piece<T> w(x, (int)split, Chunk<T, NT, U>::kSize, vocab);
+            Chunk<T, NT, U> c;
+            c.template load<STREAM>(x, w.from, w.to);
+            const int ke = w.edge();
+            const float xe = ke >= 0 ? (float)x[ke] : -INFINITY;
+            float top[U], m = xe;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            top[u] = (float)c.v[u][0];
-#pragma unroll
-            for (int j = 1; j < N; ++j) top[u] = fmaxf(top[u], (float)c.v[u][j]);
-            m = fmaxf(m, top[u]);
-        }
-        c.forget();
-        most[threadIdx.x] = m > -INFINITY ? ordered(m) : 0;
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-        if (lane == 0) red[wave] = m;
-        if (threadIdx.x == 0) count = 0;
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kWaves; ++k) m = fmaxf(m, red[k]);
-        if (wave == 0) {
-            uint32_t v[kWaves];
-#pragma unroll
-            for (int k = 0; k < kWaves; ++k) v[k] = most[k * 64 + lane];
-            const uint32_t t = reached_by<kLowBits<T>>(v, b.take);
-            if (lane == 0) bound = t;
-        }
-        const float base = base_of(m);
-        const PieceTerms terms(base, sc);
-        double s = (double)terms.near(xe), far = 0.0;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float y[N];
-#pragma unroll
-            for (int j = 0; j < N; ++j) y[j] = (float)c.v[u][j];
-            terms.add(y, top[u], s, far);
-        }
-        s += far * terms.rest;
-        c.forget();
-        s = wg_sum<NT>(s, red_sum);
-        if (threadIdx.x == 0) sums[item] = PieceSum{(double)m, s};
-        // every number reaches the lowest one
-        const float low = bound == 1u ? -3.402823466e38f : unordered(bound);
-        auto put = [&](float v, int at) {
-            if (v >= low) {
-                const int p = atomicAdd(&count, 1);
-                if (p < kRoom) room[p] = token_key(v, at);
+            for (int u = 0; u < U; ++u) {
+                top[u] = max3((float)c.v[u][0], (float)c.v[u][1], (float)c.v[u][2]);
+                if (N == 8) top[u] = max3(top[u], (float)c.v[u][N - 5], (float)c.v[u][N - 4]);
+                if (N == 8) top[u] = max3(top[u], (float)c.v[u][N - 3], (float)c.v[u][N - 2]);
+                top[u] = fmaxf(top[u], (float)c.v[u][N - 1]);
+                m = fmaxf(m, top[u]);
             }
-        };
-        put(xe, ke);
+            c.forget();
+            most[threadIdx.x] = m > -INFINITY ? ordered(m) : 0;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (top[u] >= low) {
+            for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+            if (lane == 0) red[wave] = m;
+            if (threadIdx.x == 0) vectors = count = 0;
+            __syncthreads();
 #pragma unroll
-                for (int j = 0; j < N; ++j) put((float)c.v[u][j], c.at(w.from, u) + j);
+            for (int k = 0; k < kWaves; ++k) m = fmaxf(m, red[k]);
+            if (wave == 0) {
+                uint32_t v[kWaves];
+#pragma unroll
+                for (int k = 0; k < kWaves; ++k) v[k] = most[k * 64 + lane];
+                const uint32_t t = reached_by<kLowBits<T>>(v, b.take);
+                if (lane == 0) bound = t;
             }
-        __syncthreads();
-        const int found = count;
-        const int64_t lists = (int64_t)b.beams * splits;  // of a batch item: place i of list l at i * lists + l
-        uint64_t* out = keys + item / lists * lists * b.take + item % lists;
-        if (found <= kRoom) {
-            for (int i = threadIdx.x; i < found; i += NT) {
-                const uint64_t k = room[i];
-                int rank = 0;
-                for (int j = 0; j < found; ++j) rank += room[j] > k;
-                if (rank < b.take) out[rank * lists] = k;
+            const float base = base_of(m);
+            const PieceTerms terms(base, sc);
+            double s = (double)terms.near(xe), far = 0.0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float y[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) y[j] = (float)c.v[u][j];
+                terms.add(y, top[u], s, far);
             }
-            for (int i = found + threadIdx.x; i < b.take; i += NT) out[i * lists] = 0;
-        } else {
-            uint64_t last = ~0ull;
-            for (int i = 0; i < b.take; ++i) {
-                uint64_t best = token_key(xe, ke);
-                if (best >= last) best = 0;
-#pragma unroll 1
-                for (int k = w.from + (int)threadIdx.x; k < w.to; k += NT) {
-                    const uint64_t y = token_key((float)x[k], k);
-                    best = y < last && y > best ? y : best;
+            s += far * terms.rest;
+            c.forget();
+            s = wg_sum<NT>(s, red_sum);
+            const uint32_t lists = (uint32_t)b.beams * splits, item = r / (uint32_t)b.beams;
+            const uint32_t list = (r - item * (uint32_t)b.beams) * splits + split;
+            if (threadIdx.x == 0) sums[(int64_t)r * splits + split] = PieceSum{(double)m, s};
+            // every number reaches the lowest one
+            const float low = bound == 1u ? -3.402823466e38f : unordered(bound);
+            int n = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) n += __popcll(__ballot(top[u] >= low));
+            n += __popcll(__ballot(xe >= low));
+            if (n) {
+                int p = 0;
+                if (lane == 0) p = atomicAdd(&vectors, n);
+                p = __builtin_amdgcn_readfirstlane(p);
+#pragma unroll
+                for (int u = 0; u <= U; ++u) {
+                    const bool mine = (u < U ? top[u < U ? u : 0] : xe) >= low;
+                    const uint64_t mask = __ballot(mine);
+                    const int place = p + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+                    p += __popcll(mask);
+                    if (mine && place < kVectors) {
+                        if (u < U) vec[place] = c.v[u < U ? u : 0];
+                        at[place] = u < U ? c.at(w.from, u) : -1 - ke;  // a value of its own: its place is kept alone
+                    }
                 }
-                best = wave_max(best);
-                __syncthreads();
-                if (lane == 0) room[wave] = best;
-                __syncthreads();
-#pragma unroll
-                for (int k = 0; k < kWaves; ++k) best = room[k] > best ? room[k] : best;
-                if (threadIdx.x == 0) out[i * lists] = best;
-                last = best;  // 0: nothing is below it
             }
+            __syncthreads();
+            const int held = vectors;
+            if (held <= kVectors) {
+                for (int i = threadIdx.x; i < held * N; i += NT) {
+                    const int first = at[i / N];
+                    const int k = first < 0 ? -1 - first : first + i % N;
+                    // (a value of its own is looked at once)
+                    const float v = first >= 0 ? (float)vec[i / N][i % N] : i % N ? -INFINITY : (float)x[k];
+                    if (v >= low) {
+                        const int p = atomicAdd(&count, 1);
+                        if (p < kRoom) room[p] = token_key(v, k);
+                    }
+                }
+            }
+            __syncthreads();
+            const int found = held <= kVectors ? count : kRoom + 1;
+            // place i of list l of a batch item at i * lists + l
+            uint64_t* out = keys + (int64_t)item * lists * b.take + list;
+            if (found <= kRoom) {
+                if (threadIdx.x < 8) room[found + threadIdx.x] = 0;
+                __syncthreads();
+                for (int i = threadIdx.x; i < found; i += NT) {
+                    const uint64_t k = room[i];
+                    const int rank = rank_of(room, found, [&](uint64_t o) { return o > k; });
+                    if (rank < b.take) out[(int64_t)rank * lists] = k;
+                }
+                for (int i = found + threadIdx.x; i < b.take; i += NT) out[(int64_t)i * lists] = 0;
+            } else {
+                uint64_t last = ~0ull;
+                for (int i = 0; i < b.take; ++i) {
+                    uint64_t best = token_key(xe, ke);
+                    if (best >= last) best = 0;
+#pragma unroll 1
+                    for (int k = w.from + (int)threadIdx.x; k < w.to; k += NT) {
+                        const uint64_t y = token_key((float)x[k], k);
+                        best = y < last && y > best ? y : best;
+                    }
+                    best = wave_max(best);
+                    __syncthreads();
+                    if (lane == 0) room[wave] = best;
+                    __syncthreads();
+#pragma unroll
+                    for (int k = 0; k < kWaves; ++k) best = room[k] > best ? room[k] : best;
+                    if (threadIdx.x == 0) out[(int64_t)i * lists] = best;
+                    last = best;  // 0: nothing is below it
+                }
+            }
+            __syncthreads();  // the shared arrays are used again
         }
-        __syncthreads();  // the shared arrays are used again
     }
 }
 
@@ -256,12 +305,13 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
                                                        const PieceSum* __restrict__ sums, SelectOut o) {
     constexpr int kWaves = kJoinNT / 64, kGroups = kJoinNT / 4;
     __shared__ RowSum row[kMaxBeams];
-    __shared__ Cand room[kRoom];
+    __shared__ Cand room[kRoom + 8];
     __shared__ uint32_t most[kGroups];
     __shared__ uint32_t bound;
     __shared__ int count;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t lists = (uint32_t)b.beams * (uint32_t)splits, all = lists * (uint32_t)b.take;
+    const Divide by_lists(lists), by_splits((uint32_t)splits);
     for (int64_t item = blockIdx.x; item < batch; item += gridDim.x) {
         const uint64_t* key = keys + item * all;
         uint64_t kept[kJoinKeep];
@@ -272,16 +322,19 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
         }
         for (int k = wave; k < b.beams; k += kWaves) {
             const int64_t r = item * b.beams + k;
-            RowSum a{0.0, 0.0, (double)b.score[r], b.weight ? (double)b.weight[r] : 1.0, 0};
-            if (b.counts(r) && b.has_ended(r)) a.state = 2;
-            else if (b.counts(r)) {
-                double m = -INFINITY;
-                for (int p = lane; p < splits; p += 64) m = fmax(m, sums[r * splits + p].m);
+            const PieceSum none{-INFINITY, 0.0};
+            // read whether the row counts or not (what is there is not used then): one latency for all
+            const PieceSum head = lane < splits ? sums[r * splits + lane] : none;
+            const bool ended = b.has_ended(r), counts = b.counts(r);
+            RowSum a{0.0, 0.0, (double)b.score[r], b.weight ? (double)b.weight[r] : 1.0, counts && ended ? 2 : 0};
+            if (counts && !ended) {
+                double m = head.m;
+                for (int p = lane + 64; p < splits; p += 64) m = fmax(m, sums[r * splits + p].m);
 #pragma unroll
                 for (int d = 32; d > 0; d >>= 1) m = fmax(m, __shfl_xor(m, d));
                 double s = 0.0;
                 for (int p = lane; p < splits; p += 64) {
-                    const PieceSum q = sums[r * splits + p];
+                    const PieceSum q = p < 64 ? head : sums[r * splits + p];
                     s += q.m == -INFINITY ? q.s : q.s * exp((q.m - m) * sc.inv_t);
                 }
                 s = wave_sum(s);
@@ -297,7 +350,7 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
         __syncthreads();
         // candidate e with its key; hi is 0 where there is none
         auto cand = [&](uint32_t e, uint64_t x) {
-            const uint32_t list = e % lists, k = list / (uint32_t)splits;
+            const uint32_t list = e - by_lists(e) * lists, k = by_splits(list);
             const RowSum& a = row[k];
             const bool none = a.state == 1 ? !x : a.state == 0 || e != k * (uint32_t)splits;
             if (none) return Cand{0, 0};
@@ -351,10 +404,11 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
         __syncthreads();
         const int found = count;
         if (found <= kRoom) {
+            if (threadIdx.x < 8) room[found + threadIdx.x] = Cand{0, 0};
+            __syncthreads();
             for (int i = threadIdx.x; i < found; i += kJoinNT) {
                 const Cand c = room[i];
-                int rank = 0;
-                for (int j = 0; j < found; ++j) rank += room[j].over(c);
+                const int rank = rank_of(room, found, [&](const Cand& o) { return o.over(c); });
                 if (rank < b.take) write(rank, c);
             }
             for (int i = found + threadIdx.x; i < b.take; i += kJoinNT) write(i, Cand{0, 0});
@@ -421,9 +475,7 @@ __device__ __forceinline__ void reorder_columns(const iso_blocks& s, char* base,
     const uint32_t whole = (uint32_t)(s.inner / 16), cols = TAIL ? 1 : whole, all = (uint32_t)s.mid * cols;
     const int width = TAIL ? (int)(s.inner % 16) : 16;
     if (TAIL) base += (int64_t)whole * 16;
-    // col / cols: the product is off by less than 2^-51 of itself, its distance from a
-    // whole number is at least 0.5 / cols; in registers a third of a division's
-    const double part = 1.0 / (double)cols;
+    const Divide by_cols(cols);
     for (uint32_t first = blockIdx.x << shift; first < all; first += gridDim.x << shift) {
         Quad v[U];
         char* put[U];
@@ -433,7 +485,7 @@ __device__ __forceinline__ void reorder_columns(const iso_blocks& s, char* base,
             const uint32_t col = first + (unit & ((1u << shift) - 1));
             put[u] = nullptr;
             if ((int)k < mv.n && col < all) {
-                const uint32_t m = TAIL ? col : (uint32_t)(((double)col + 0.5) * part), c = TAIL ? 0 : col - m * cols;
+                const uint32_t m = TAIL ? col : by_cols(col), c = TAIL ? 0 : col - m * cols;
                 char* at = base + m * s.mid_stride + (int64_t)c * 16;
                 put[u] = at + mv.to[k] * s.row_stride;
                 v[u] = load_bytes(at + mv.from[k] * s.row_stride, width);
@@ -516,12 +568,12 @@ int iso_beam_select(const void* logits, int dtype, int64_t batch, int64_t beams,
     PieceSum* sums = reinterpret_cast<PieceSum*>(static_cast<char*>(workspace) + pl.off_sums);
     const Beams b{score, weight, ended, (int)beams, (int)take, end_token};
     const Scale sc = scale_of(temperature);
-    const int64_t items = rows * pl.splits;
+    const dim3 grid((unsigned)(rows < kMaxGrid ? rows : kMaxGrid), (unsigned)(pl.splits < 65535 ? pl.splits : 65535));
     by_dtype(dtype, [&](auto v) {
         typedef decltype(v) T;
-        hipLaunchKernelGGL((k_beam_pieces<T, kPieceNT, kPieceU, false>), dim3((unsigned)(items < kMaxGrid ? items : kMaxGrid)),
-                           dim3(kPieceNT), 0, st, static_cast<const T*>(logits), rows, (int)vocab, ld, b, sc, pl.splits,
-                           keys, sums);
+        hipLaunchKernelGGL((k_beam_pieces<T, kPieceNT, kPieceU, false>), grid, dim3(kPieceNT), 0, st,
+                           static_cast<const T*>(logits), (uint32_t)rows, (int)vocab, ld, b, sc, (uint32_t)pl.splits, keys,
+                           sums);
     });
     hipLaunchKernelGGL(k_beam_join, dim3((unsigned)(batch < kMaxGrid ? batch : kMaxGrid)), dim3(kJoinNT), 0, st, batch, b,
                        sc, pl.splits, keys, sums, SelectOut{out_score, out_logp, out_parent, out_token});

@@ -65,6 +65,15 @@ bool take_states(const iso_blocks* from, int count, int64_t rows, const Span (&o
     return true;
 }
 
+// x / n of 32 bits by a product, a sixth of a division's instructions: it is off by
+// less than 2^-51 of itself, and its distance from a whole number is at least
+// 0.5 / n.
+struct Divide {
+    double part;
+    __device__ __forceinline__ explicit Divide(uint32_t n) : part(1.0 / (double)n) {}
+    __device__ __forceinline__ uint32_t operator()(uint32_t x) const { return (uint32_t)(((double)x + 0.5) * part); }
+};
+
 // 16 bytes at any address: global loads and stores need no alignment.
 typedef uint32_t Quad __attribute__((ext_vector_type(4)));
 typedef uint32_t Wide16 __attribute__((ext_vector_type(4), aligned(1), may_alias));
