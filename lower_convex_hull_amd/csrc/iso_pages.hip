@@ -93,6 +93,7 @@ struct Fork {
     int32_t* free_sum;  // [blocks of pages]
     Copy* copies;       // [children]
     int32_t* plan;      // [2]: done or not, copies
+    bool counts_left;   // k_fork_write takes the copied pages' counts down
 
     __device__ __forceinline__ int64_t tokens_of(int64_t s) const {
         const int64_t n = length[s], most = max_pages * page_size;
@@ -252,6 +253,41 @@ __global__ __launch_bounds__(kNT) void k_fork_list(Fork f, Blocks pb, int64_t ch
     }
 }
 
+// 16-byte columns of what one block of an array holds, `bytes` of each of its mid
+// runs, by the workgroup: kCopyU of them a thread are on their way at a time.
+constexpr int kCopyU = 8;
+struct CopyTile {
+    uint32_t cols, all;  // columns of a run, of all of them
+    __device__ __forceinline__ CopyTile(const iso_blocks& s, int64_t bytes)
+        : cols((uint32_t)((bytes + 15) / 16)), all((uint32_t)s.mid * cols) {}
+    __device__ __forceinline__ uint32_t tiles() const { return (all + kNT * kCopyU - 1) / (kNT * kCopyU); }
+};
+__device__ __forceinline__ void copy_tile(const iso_blocks& s, const CopyTile& c, int64_t bytes, const char* from, char* to,
+                                          uint32_t tile) {
+    const Divide by_cols(c.cols);
+    const int rest = (int)(bytes - (int64_t)(c.cols - 1) * 16);
+    Quad v[kCopyU];
+    int64_t at[kCopyU];
+#pragma unroll
+    for (int u = 0; u < kCopyU; ++u) {
+        const uint32_t col = (tile * kCopyU + u) * kNT + threadIdx.x;
+        at[u] = -1;
+        if (col < c.all) {
+            const uint32_t m = by_cols(col), k = col - m * c.cols;
+            at[u] = m * s.mid_stride + (int64_t)k * 16;
+            if (k + 1 < c.cols || rest == 16) {
+                v[u] = *reinterpret_cast<const Wide16*>(from + at[u]);
+            } else {  // the end of a run, taken at once
+                store_bytes(to + at[u], rest, load_bytes(from + at[u], rest));
+                at[u] = -1;
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kCopyU; ++u)
+        if (at[u] >= 0) *reinterpret_cast<Wide16*>(to + at[u]) = v[u];
+}
+
 // The children's tables and lengths, then the copies.
 __global__ __launch_bounds__(kNT) void k_fork_write(Fork f, States st) {
     const bool done = f.plan[0];
@@ -274,20 +310,137 @@ __global__ __launch_bounds__(kNT) void k_fork_write(Fork f, States st) {
         }
         if (threadIdx.x == 0) {
             f.new_length[i] = done ? (int32_t)c.after : 0;
-            if (copy && done) atomicAdd(&f.new_refs[c.edge], -1);
+            if (f.counts_left && copy && done) atomicAdd(&f.new_refs[c.edge], -1);
         }
     }
+    // items are tiles of a whole block; those past a copy's tokens have nothing to do
     const int64_t copies = f.plan[1];
     for (int u = 0; u < st.count; ++u) {
         const iso_blocks& s = st.b[u];
-        const int64_t token = s.inner / f.page_size, items = copies * s.outer * s.mid;
-        for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-            const int64_t n = item / (s.outer * s.mid), o = item / s.mid % s.outer, m = item % s.mid;
+        const int64_t token = s.inner / f.page_size;
+        const uint32_t tiles = CopyTile(s, s.inner).tiles();
+        const int64_t per = s.outer * tiles;
+        for (int64_t item = blockIdx.x; item < copies * per; item += gridDim.x) {
+            const int64_t n = item / per, o = (item - n * per) / tiles;
+            const uint32_t tile = (uint32_t)(item - n * per - o * tiles);
             const Copy c = f.copies[n];
-            const char* from = static_cast<char*>(s.base) + o * s.outer_stride + c.from * s.row_stride + m * s.mid_stride;
-            char* to = static_cast<char*>(s.base) + o * s.outer_stride + f.list[c.to] * s.row_stride + m * s.mid_stride;
-            for (int64_t t = threadIdx.x; t < c.tokens * token; t += kNT) to[t] = from[t];
+            const CopyTile ct(s, c.tokens * token);
+            if (tile >= ct.tiles()) continue;
+            char* base = static_cast<char*>(s.base) + o * s.outer_stride;
+            copy_tile(s, ct, c.tokens * token, base + c.from * s.row_stride, base + f.list[c.to] * s.row_stride, tile);
         }
+    }
+}
+
+// A step in one workgroup but for what k_fork_write does: the counts are in LDS.
+// Up to kOnePages pages, kOneNT children and sequences, kOneEntries entries of
+// tables (their counting is this workgroup's).
+constexpr int kOneNT = 1024, kOnePages = 12288;
+constexpr int64_t kOneEntries = 1 << 16;
+__global__ __launch_bounds__(kOneNT) void k_fork_one(Fork f) {
+    constexpr int kOneWaves = kOneNT / 64, kEach = kOnePages / kOneNT;
+    __shared__ int32_t refs[kOnePages];
+    __shared__ int32_t kids[kOneNT];
+    __shared__ int32_t edges[kOneNT];
+    __shared__ int64_t red[kOneWaves];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    // exclusive prefix over the workgroup of two counts in the halves of 64 bits, and the total
+    auto prefix = [&](int64_t v, int64_t& total) {
+        int64_t s = v;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t o = (int64_t)__shfl_up((long long)s, d);
+            s += lane >= d ? o : 0;
+        }
+        if (lane == 63) red[wave] = s;
+        __syncthreads();
+        int64_t before = 0;
+        total = 0;
+#pragma unroll
+        for (int k = 0; k < kOneWaves; ++k) {
+            before += k < wave ? red[k] : 0;
+            total += red[k];
+        }
+        __syncthreads();
+        return before + s - v;
+    };
+    for (int p = t; p < (int)f.pages; p += kOneNT) {
+        const int32_t n = f.refs[p];
+        refs[p] = n > 0 ? n : 0;
+    }
+    kids[t] = 0;
+    Child c{-1, 0, 0, -1};
+    const bool is_child = t < f.children;
+    if (is_child) c = child_of(f, t);
+    edges[t] = c.edge;
+    __syncthreads();
+    if (c.parent >= 0) atomicAdd(&kids[c.parent], 1);
+    __syncthreads();
+    for (int s = wave; s < (int)f.seqs; s += kOneWaves) {
+        const int32_t more = kids[s] - 1;
+        if (!more) continue;
+        const int held = (int)f.pages_for(f.tokens_of(s));
+        for (int j = lane; j < held; j += 64) {
+            const int32_t q = f.table[s * f.max_pages + j];
+            if (f.is_page(q)) atomicAdd(&refs[q], more);
+        }
+    }
+    __syncthreads();
+    // who goes on to write the same page
+    int writers = 0, earlier = 0;
+    if (c.edge >= 0) {
+        for (int k = 0; k < (int)f.children; ++k) {
+            const int same = edges[k] == c.edge;
+            writers += same;
+            earlier += same && k < t;
+        }
+    }
+    const int copy = c.edge >= 0 && !(refs[c.edge] == writers && !earlier);
+    const int64_t want = f.pages_for(c.after);
+    const bool too_long = want > f.max_pages || c.after > INT32_MAX;
+    const int64_t need = too_long ? 0 : want - f.pages_for(c.before) + copy;
+    int64_t all_need, all_copies, all_free;
+    // a need is below 2^31, the sum of all below 2^41
+    const int64_t start = prefix(need, all_need);
+    const int64_t place = prefix(((int64_t)too_long << 32) | copy, all_copies);
+    int64_t open = 0;
+    const int first = t * kEach;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) open += first + i < f.pages && refs[first + i] <= 0;
+    int64_t at = prefix(open, all_free);
+    const int32_t late = (int32_t)(all_copies >> 32), copies = (int32_t)all_copies;
+    const bool done = all_need <= all_free && !late;
+    if (is_child) {
+        f.need[t] = (int32_t)need | (copy << 31);
+        f.start[t] = start;
+        if (done && copy) f.copies[(int32_t)place] = Copy{c.edge, (int32_t)start, (int32_t)(c.before % f.page_size), 0};
+    }
+    if (t == 0) {
+        const int64_t lack = all_need - all_free;
+        f.status[0] = lack <= 0 ? 0 : lack < INT32_MAX ? (int32_t)lack : INT32_MAX;
+        f.status[1] = late;
+        f.status[2] = f.plan[1] = done ? copies : 0;
+        f.status[3] = done ? (int32_t)all_need : 0;
+        f.status[4] = done ? (int32_t)(all_free - all_need) : 0;
+        f.plan[0] = done;
+    }
+    if (done) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int p = first + i;
+            if (p < f.pages && refs[p] <= 0) {
+                refs[p] = at < all_need;
+                if (at < all_need) f.list[at] = p;
+                ++at;
+            }
+        }
+        __syncthreads();
+        if (copy) atomicAdd(&refs[c.edge], -1);
+    }
+    __syncthreads();
+    for (int p = t; p < (int)f.pages; p += kOneNT) {
+        const int32_t n = f.refs[p];
+        f.new_refs[p] = done ? refs[p] : n > 0 ? n : 0;
     }
 }
 
@@ -392,12 +545,14 @@ __global__ __launch_bounds__(kNT) void k_compact_write(Compact f, States st) {
     for (int64_t k = t; k < moves; k += step) f.new_refs[f.holes[k]] = f.refs[f.movers[k]];
     for (int u = 0; u < st.count; ++u) {
         const iso_blocks& s = st.b[u];
-        const int64_t items = moves * s.outer * s.mid;
-        for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-            const int64_t k = item / (s.outer * s.mid), o = item / s.mid % s.outer, m = item % s.mid;
-            const char* from = static_cast<char*>(s.base) + o * s.outer_stride + f.movers[k] * s.row_stride + m * s.mid_stride;
-            char* to = static_cast<char*>(s.base) + o * s.outer_stride + f.holes[k] * s.row_stride + m * s.mid_stride;
-            for (int64_t i = threadIdx.x; i < s.inner; i += kNT) to[i] = from[i];
+        const CopyTile ct(s, s.inner);
+        const uint32_t tiles = ct.tiles();
+        const int64_t per = s.outer * tiles;
+        for (int64_t item = blockIdx.x; item < moves * per; item += gridDim.x) {
+            const int64_t k = item / per, o = (item - k * per) / tiles;
+            char* base = static_cast<char*>(s.base) + o * s.outer_stride;
+            copy_tile(s, ct, s.inner, base + f.movers[k] * s.row_stride, base + f.holes[k] * s.row_stride,
+                      (uint32_t)(item - k * per - o * tiles));
         }
     }
 }
@@ -427,13 +582,25 @@ CompactPlan compact_plan(int64_t pages) {
 constexpr int kGrid = 2048;
 inline dim3 grid_of(int64_t items) { return dim3((unsigned)(items < 1 ? 1 : items < kGrid ? items : kGrid)); }
 
-// Items of a copy of every page stay inside 64 bits.
+// A block's columns of 16 bytes fit 31 bits, items of a copy of every page 64.
 bool pools_ok(const States& st, int64_t pages, int64_t page_size) {
     for (int i = 0; i < st.count; ++i) {
-        if (st.b[i].inner % page_size) return false;
-        if (st.b[i].outer > (1LL << 60) / st.b[i].mid / pages) return false;
+        const iso_blocks& s = st.b[i];
+        if (s.inner % page_size) return false;
+        if ((s.inner + 15) / 16 > 0x7fffffffLL / s.mid || s.outer > (1LL << 30)) return false;
+        if (s.outer * ((s.inner * s.mid >> 15) + 1) > (1LL << 61) / pages) return false;
     }
     return true;
+}
+// Runs that follow each other without a gap are one.
+void join_runs(States& st) {
+    for (int i = 0; i < st.count; ++i) {
+        iso_blocks& s = st.b[i];
+        if (s.mid > 1 && s.mid_stride == s.inner) {
+            s.inner *= s.mid;
+            s.mid = 1;
+        }
+    }
 }
 
 }  // namespace
@@ -479,10 +646,16 @@ int iso_pages_fork(const int32_t* table, const int32_t* length, int64_t seqs, in
            reinterpret_cast<int64_t*>(ws + pl.start), reinterpret_cast<int64_t*>(ws + pl.need_sum),
            reinterpret_cast<int32_t*>(ws + pl.copy_sum), reinterpret_cast<int32_t*>(ws + pl.long_sum),
            reinterpret_cast<int32_t*>(ws + pl.free_sum), reinterpret_cast<Copy*>(ws + pl.copies),
-           reinterpret_cast<int32_t*>(ws + pl.plan)};
+           reinterpret_cast<int32_t*>(ws + pl.plan), true};
     hipStream_t hs = static_cast<hipStream_t>(stream);
     const int64_t blocks = pl.child_blocks + pl.pb.count;
     const int64_t sweep = (pages > seqs ? pages : seqs) / kNT + 1;
+    if (pages <= kOnePages && children <= kOneNT && seqs <= kOneNT && seqs * max_pages <= kOneEntries) {
+        f.counts_left = false;
+        hipLaunchKernelGGL(k_fork_one, dim3(1), dim3(kOneNT), 0, hs, f);
+        if (children) hipLaunchKernelGGL(k_fork_write, dim3(kGrid), dim3(kNT), 0, hs, f, st);
+        return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
+    }
     hipLaunchKernelGGL(k_fork_begin, grid_of(sweep), dim3(kNT), 0, hs, f);
     if (children) hipLaunchKernelGGL(k_fork_count, grid_of(pl.child_blocks), dim3(kNT), 0, hs, f);
     if (seqs) hipLaunchKernelGGL(k_fork_refs, grid_of(seqs), dim3(kNT), 0, hs, f);
@@ -512,6 +685,7 @@ int iso_pages_compact(const int32_t* table, int64_t entries, const int32_t* refs
         if (!aligned(s.p, 4)) return ISO_ERR_ARG;
     States st;
     if (!take_states(pools, count, pages, all, st) || !pools_ok(st, pages, 1)) return ISO_ERR_ARG;
+    join_runs(st);
     const CompactPlan pl = compact_plan(pages);
     if (!workspace || workspace_bytes < pl.bytes) return ISO_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return ISO_ERR_ARG;

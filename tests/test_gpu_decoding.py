@@ -330,6 +330,35 @@ def test_fork_of_broken_caches(torch):
         run_fork(torch, table, length, refs, parent, page, rng.integers(-2, 2, 6).astype(np.int32), pools, token_dim)
 
 
+@pytest.mark.parametrize("seqs,children,most,pages", [(5, 40, 6, 12288), (5, 40, 6, 12289), (1024, 1024, 3, 5000), (1025, 300, 3, 5000),
+                                                       (20, 1025, 4, 6000), (30, 50, 2200, 9000), (700, 2500, 5, 40000), (3, 7, 9, 300000),
+                                                       (64, 64, 1024, 12288), (3000, 3000, 4, 20000)])
+def test_fork_of_many(torch, seqs, children, most, pages):
+    """Many pages, sequences, children and long tables."""
+    say(f"[decoding] fork {seqs} to {children}, {most} pages each of {pages}")
+    rng = np.random.default_rng(seqs + pages)
+    gen = torch.Generator().manual_seed(pages)
+    page = 2
+    table, length = np.full((seqs, most), -1, np.int32), np.zeros(seqs, np.int32)
+    ids, left = rng.permutation(pages).astype(np.int32), pages // 2
+    at = 0
+    for s in range(seqs):
+        take = int(rng.integers(0, min(most, max(1, left // max(1, seqs - s)) * 2) + 1))
+        take = min(take, left)
+        table[s, :take] = ids[at:at + take]
+        if s % 3 == 1 and take > 1 and table[s - 1, 0] >= 0:
+            table[s, 0] = table[s - 1, 0]  # a shared first page
+        at, left = at + take, left - take
+        length[s] = max(0, take * page - int(rng.integers(0, 2))) if take else 0
+    refs = np.bincount(table[table >= 0], minlength=pages).astype(np.int32)
+    pools = [raw(torch, gen, (1, pages, page, 3), torch.bfloat16), raw(torch, gen, (2, pages, page, 1), torch.float32)]
+    parent = rng.integers(-1, seqs, children).astype(np.int32)
+    run_fork(torch, table, length, refs, parent, page, rng.integers(0, 2, children).astype(np.int32), pools, 2)
+    same = np.arange(children, dtype=np.int32)
+    run_fork(torch, table, length, refs, same, page, 1, pools, 2)
+    run_fork(torch, table, length, refs, parent, page, most * page, pools, 2)  # too long
+
+
 def run_compact(torch, table, refs, pools):
     dev = [p.cuda() for p in pools]
     got = iso.pages_compact(torch.from_numpy(table).cuda(), torch.from_numpy(refs).cuda(), pools=dev, page_dim=1)
@@ -340,7 +369,7 @@ def run_compact(torch, table, refs, pools):
         assert np.array_equal(d.float().cpu().numpy(), w)
 
 
-@pytest.mark.parametrize("pages", [0, 1, 2, 63, 257, 2048, 2049, 5000])
+@pytest.mark.parametrize("pages", [0, 1, 2, 63, 257, 2048, 2049, 5000, 70001])
 def test_compact(torch, pages):
     rng = np.random.default_rng(pages)
     gen = torch.Generator().manual_seed(pages)
