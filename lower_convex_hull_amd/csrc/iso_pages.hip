@@ -28,31 +28,24 @@ __device__ __forceinline__ int wg_prefix(int v, int* red, int& total) {
     return before + s.v - v;
 }
 
-// Sums of the first `upto` and of all n values (below 2^63), by the workgroup.
-struct Prefix {
-    int64_t before, total;
-};
-__device__ __forceinline__ int64_t wg_sum64(int64_t v, int64_t* red) {
+// N sums over the workgroup at once, the same in every thread.
+template <int N>
+__device__ __forceinline__ void wg_sums(int64_t (&v)[N], int64_t (*red)[kWaves]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += (int64_t)__shfl_xor((long long)v, d);
-    if (lane == 0) red[wave] = v;
-    __syncthreads();
-    int64_t s = 0;
+    for (int n = 0; n < N; ++n) {
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) s += red[k];
-    __syncthreads();
-    return s;
-}
-template <typename T>
-__device__ __forceinline__ Prefix prefix_of(const T* v, int64_t n, int64_t upto, int64_t* red) {
-    int64_t a = 0, t = 0;
-    for (int64_t i = threadIdx.x; i < n; i += kNT) {
-        const int64_t x = v[i];
-        t += x;
-        a += i < upto ? x : 0;
+        for (int d = 32; d > 0; d >>= 1) v[n] += (int64_t)__shfl_xor((long long)v[n], d);
+        if (lane == 0) red[n][wave] = v[n];
     }
-    return Prefix{wg_sum64(a, red), wg_sum64(t, red)};
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        v[n] = 0;
+#pragma unroll
+        for (int k = 0; k < kWaves; ++k) v[n] += red[n][k];
+    }
+    __syncthreads();
 }
 
 // Pages are taken in blocks, one a workgroup, children in blocks of kNT.
@@ -60,10 +53,10 @@ struct Blocks {
     int64_t pages, per;  // pages in all, in a block
     int64_t count;
 };
-constexpr int64_t kPageBlock = 2048, kPageBlocks = 1024;
+constexpr int64_t kPageBlock = 4 * kNT, kPageBlocks = 4096;
 Blocks page_blocks(int64_t pages) {
     Blocks b{pages, kPageBlock, 0};
-    if (pages > kPageBlock * kPageBlocks) b.per = ((pages + kPageBlocks - 1) / kPageBlocks + kNT - 1) / kNT * kNT;
+    if (pages > kPageBlock * kPageBlocks) b.per = ((pages + kPageBlocks - 1) / kPageBlocks + kPageBlock - 1) / kPageBlock * kPageBlock;
     b.count = (pages + b.per - 1) / b.per;
     return b;
 }
@@ -80,6 +73,7 @@ struct Fork {
     const int32_t *table, *length, *refs, *parent, *grow;
     int32_t grow_all;
     int64_t seqs, max_pages, pages, page_size, children;
+    double part;  // 1 / page_size
     int32_t *new_table, *new_length, *new_refs, *status;
     // workspace
     Mark* mark;         // [pages]
@@ -92,14 +86,17 @@ struct Fork {
     int32_t* long_sum;  // [blocks of children]
     int32_t* free_sum;  // [blocks of pages]
     Copy* copies;       // [children]
-    int32_t* plan;      // [2]: done or not, copies
-    bool counts_left;   // k_fork_write takes the copied pages' counts down
+    int32_t* plan;      // [3]: done or not, copies, pages taken
+    bool counts_left;   // k_fork_write brings the counts up to date
 
     __device__ __forceinline__ int64_t tokens_of(int64_t s) const {
         const int64_t n = length[s], most = max_pages * page_size;
         return n < 0 ? 0 : n < most ? n : most;
     }
-    __device__ __forceinline__ int64_t pages_for(int64_t n) const { return (n + page_size - 1) / page_size; }
+    // Whole pages of n < 2^32 tokens, and pages that hold them (Divide's product).
+    __device__ __forceinline__ uint32_t whole(int64_t n) const { return (uint32_t)(((double)n + 0.5) * part); }
+    __device__ __forceinline__ int64_t past(int64_t n) const { return n - (int64_t)whole(n) * page_size; }
+    __device__ __forceinline__ int64_t pages_for(int64_t n) const { return (int64_t)whole(n) + (past(n) > 0); }
     __device__ __forceinline__ bool is_page(int32_t q) const { return q >= 0 && q < pages; }
     __device__ __forceinline__ int64_t grown(int64_t i) const {
         const int32_t g = grow ? grow[i] : grow_all;
@@ -118,21 +115,40 @@ __device__ __forceinline__ Child child_of(const Fork& f, int64_t i) {
     c.before = c.parent >= 0 ? f.tokens_of(c.parent) : 0;
     c.after = c.before + g;
     c.edge = -1;
-    if (g > 0 && c.before % f.page_size) {
-        const int32_t q = f.table[c.parent * f.max_pages + c.before / f.page_size];
+    if (g > 0 && f.past(c.before)) {
+        const int32_t q = f.table[c.parent * f.max_pages + f.whole(c.before)];
         if (f.is_page(q)) c.edge = q;
     }
     return c;
 }
 
-__global__ __launch_bounds__(kNT) void k_fork_begin(Fork f) {
+// A step of any size takes six launches: the counts copied and the free pages
+// counted by block; each sequence's children counted, and who goes on to write
+// which page; the counts of the pages of sequences with other than one child;
+// what each child takes; where it begins in the list of the taken pages, and the
+// list; tables and copies.  Where children are few the second and the fourth are
+// done by each workgroup of their neighbours for itself.
+__global__ __launch_bounds__(kNT) void k_fork_begin(Fork f, Blocks pb) {
+    __shared__ int64_t red[1][kWaves];
     const int64_t t = (int64_t)blockIdx.x * kNT + threadIdx.x, step = (int64_t)gridDim.x * kNT;
-    for (int64_t p = t; p < f.pages; p += step) {
-        const int32_t n = f.refs[p];
-        f.new_refs[p] = n > 0 ? n : 0;
-        f.mark[p] = Mark{0, INT32_MAX};
+    for (int64_t b = blockIdx.x; b < pb.count; b += gridDim.x) {
+        const int64_t to = (b + 1) * pb.per < f.pages ? (b + 1) * pb.per : f.pages;
+        int64_t open[1] = {0};
+        for (int64_t p0 = b * pb.per + threadIdx.x; p0 < to; p0 += kPageBlock)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t p = p0 + i * kNT;
+                if (p >= to) break;
+                const int32_t n = f.refs[p];
+                f.new_refs[p] = n > 0 ? n : 0;
+                open[0] += n <= 0;
+                if (f.mark) f.mark[p] = Mark{0, INT32_MAX};
+            }
+        wg_sums(open, red);
+        if (threadIdx.x == 0) f.free_sum[b] = (int32_t)open[0];
     }
-    for (int64_t s = t; s < f.seqs; s += step) f.kids[s] = 0;
+    if (f.kids)
+        for (int64_t s = t; s < f.seqs; s += step) f.kids[s] = 0;
 }
 
 __global__ __launch_bounds__(kNT) void k_fork_count(Fork f) {
@@ -146,111 +162,330 @@ __global__ __launch_bounds__(kNT) void k_fork_count(Fork f) {
     }
 }
 
-// A sequence's pages have a holder less for it and one more for each child.
-__global__ __launch_bounds__(kNT) void k_fork_refs(Fork f) {
+// A sequence's pages have a holder less for it and one more for each child;
+// those that nobody holds any more are free.
+__global__ __launch_bounds__(kNT) void k_fork_refs(Fork f, Blocks pb) {
     for (int64_t s = blockIdx.x; s < f.seqs; s += gridDim.x) {
-        const int32_t more = f.kids[s] - 1;
+        int32_t more = -1;
+        if (f.kids) {
+            more += f.kids[s];
+        } else {
+            for (int64_t i0 = 0; i0 < f.children; i0 += 4 * kNT) {
+                int own = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t k = i0 + i * kNT + threadIdx.x;
+                    own += k < f.children && f.parent[k] == s;
+                }
+                // own is 4 at most: three counts of its bits
+                more += __syncthreads_count(own & 1) + 2 * __syncthreads_count(own & 2) + 4 * __syncthreads_count(own & 4);
+            }
+        }
         if (!more) continue;
         const int64_t held = f.pages_for(f.tokens_of(s));
         for (int64_t j = threadIdx.x; j < held; j += kNT) {
             const int32_t q = f.table[s * f.max_pages + j];
-            if (f.is_page(q)) atomicAdd(&f.new_refs[q], more);
+            if (!f.is_page(q)) continue;
+            const int32_t was = atomicAdd(&f.new_refs[q], more), is = was + more;
+            if ((was <= 0) != (is <= 0)) atomicAdd(&f.free_sum[q / pb.per], is <= 0 ? 1 : -1);
         }
     }
 }
 
-// Blocks of children: the pages each takes.  Blocks of pages: the free ones.
-__global__ __launch_bounds__(kNT) void k_fork_need(Fork f, Blocks pb, int64_t child_blocks) {
-    __shared__ int64_t red[kWaves];
-    for (int64_t b = blockIdx.x; b < child_blocks + pb.count; b += gridDim.x) {
-        if (b < child_blocks) {
-            const int64_t i = b * kNT + threadIdx.x;
-            int64_t need = 0;
-            int copies = 0, too_long = 0;
-            if (i < f.children) {
-                const Child c = child_of(f, i);
-                const int64_t want = f.pages_for(c.after);
-                if (c.edge >= 0) {
-                    const Mark m = f.mark[c.edge];
-                    copies = !(f.new_refs[c.edge] == m.writers && m.first == i);
-                }
-                too_long = want > f.max_pages || c.after > INT32_MAX;
-                need = too_long ? 0 : want - f.pages_for(c.before) + copies;
-                f.need[i] = (int32_t)need | (copies << 31);
+// What the step comes to.
+struct Total {
+    int64_t need, room, late, copies;
+    __device__ __forceinline__ bool done() const { return need <= room && !late; }
+};
+__device__ __forceinline__ void write_status(const Fork& f, const Total& t) {
+    const int64_t lack = t.need - t.room;
+    const bool done = t.done();
+    f.status[0] = lack <= 0 ? 0 : lack < INT32_MAX ? (int32_t)lack : INT32_MAX;
+    f.status[1] = (int32_t)t.late;
+    f.status[2] = f.plan[1] = done ? (int32_t)t.copies : 0;
+    f.status[3] = f.plan[2] = done ? (int32_t)t.need : 0;
+    f.status[4] = done ? (int32_t)(t.room - t.need) : 0;
+    f.plan[0] = done;
+}
+
+// Blocks of children: the pages each takes.
+__global__ __launch_bounds__(kNT) void k_fork_need(Fork f, int64_t child_blocks) {
+    __shared__ int64_t red[2][kWaves];
+    for (int64_t b = blockIdx.x; b < child_blocks; b += gridDim.x) {
+        const int64_t i = b * kNT + threadIdx.x;
+        int64_t need = 0;
+        int copies = 0, too_long = 0;
+        if (i < f.children) {
+            const Child c = child_of(f, i);
+            const int64_t want = f.pages_for(c.after);
+            if (c.edge >= 0) {
+                const Mark m = f.mark[c.edge];
+                copies = !(f.new_refs[c.edge] == m.writers && m.first == i);
             }
-            need = wg_sum64(need, red);
-            const int64_t both = wg_sum64(((int64_t)too_long << 32) | copies, red);
-            if (threadIdx.x == 0) {
-                f.need_sum[b] = need;
-                f.copy_sum[b] = (int32_t)both;
-                f.long_sum[b] = (int32_t)(both >> 32);
-            }
-        } else {
-            const int64_t k = b - child_blocks, to = (k + 1) * pb.per < f.pages ? (k + 1) * pb.per : f.pages;
-            int64_t n = 0;
-            for (int64_t p = k * pb.per + threadIdx.x; p < to; p += kNT) n += f.new_refs[p] <= 0;
-            n = wg_sum64(n, red);
-            if (threadIdx.x == 0) f.free_sum[k] = (int32_t)n;
+            too_long = want > f.max_pages || c.after > INT32_MAX;
+            need = too_long ? 0 : want - f.pages_for(c.before) + copies;
+            f.need[i] = (int32_t)need | (copies << 31);
         }
+        int64_t v[2] = {need, ((int64_t)too_long << 32) | copies};
+        wg_sums(v, red);
+        if (threadIdx.x == 0) {
+            f.need_sum[b] = v[0];
+            f.copy_sum[b] = (int32_t)v[1];
+            f.long_sum[b] = (int32_t)(v[1] >> 32);
+        }
+    }
+}
+
+// The list of the taken pages, the lowest free ones: a block's part, by a
+// workgroup of NT threads.  The counts stay as they are: other workgroups of the
+// launch go by them (k_fork_write brings them up to date).
+template <int NT>
+__device__ __forceinline__ void list_block(const Fork& f, const Blocks& pb, int64_t b, int64_t rank, const Total& total,
+                                           int* red) {
+    constexpr int kW = NT / 64;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t to = (b + 1) * pb.per < f.pages ? (b + 1) * pb.per : f.pages;
+    if (!total.done()) return;
+    for (int64_t p0 = b * pb.per; p0 < to && rank < total.need; p0 += NT) {
+        const int64_t p = p0 + threadIdx.x;
+        const bool open = p < to && f.new_refs[p] <= 0;
+        const uint64_t mask = __ballot(open);
+        if (lane == 0) red[wave] = __popcll(mask);
+        __syncthreads();
+        int64_t at = rank + __popcll(mask & ((1ull << lane) - 1));
+#pragma unroll
+        for (int k = 0; k < kW; ++k) {
+            at += k < wave ? red[k] : 0;
+            rank += red[k];
+        }
+        __syncthreads();
+        if (open && at < total.need) f.list[at] = (int32_t)p;
     }
 }
 
 // Blocks of children: where each one's pages begin in the list, and the copies.
-// Blocks of pages: the list of the free ones, as many as are taken.
+// Blocks of pages: the list.
 __global__ __launch_bounds__(kNT) void k_fork_list(Fork f, Blocks pb, int64_t child_blocks) {
-    __shared__ int64_t red64[kWaves];
+    __shared__ int64_t red64[6][kWaves];
     __shared__ int red[kWaves];
-    const int64_t need = prefix_of(f.need_sum, child_blocks, 0, red64).total;
-    const int64_t room = prefix_of(f.free_sum, pb.count, 0, red64).total;
-    const int64_t late = prefix_of(f.long_sum, child_blocks, 0, red64).total;
-    const int64_t copied = prefix_of(f.copy_sum, child_blocks, 0, red64).total;
-    const bool done = need <= room && !late;
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        const int64_t lack = need - room;
-        f.status[0] = lack <= 0 ? 0 : lack < INT32_MAX ? (int32_t)lack : INT32_MAX;
-        f.status[1] = (int32_t)late;
-        f.status[2] = f.plan[1] = done ? (int32_t)copied : 0;
-        f.status[3] = done ? (int32_t)need : 0;
-        f.status[4] = done ? (int32_t)(room - need) : 0;
-        f.plan[0] = done;
-    }
     for (int64_t b = blockIdx.x; b < child_blocks + pb.count; b += gridDim.x) {
+        // need, late, copies, free; need and copies, or free, of the blocks before
+        int64_t v[6] = {0, 0, 0, 0, 0, 0};
+        for (int64_t k = threadIdx.x; k < child_blocks; k += kNT) {
+            const int64_t need = f.need_sum[k], copies = f.copy_sum[k];
+            v[0] += need;
+            v[1] += f.long_sum[k];
+            v[2] += copies;
+            v[4] += k < b ? need : 0;
+            v[5] += k < b ? copies : 0;
+        }
+        if (b >= child_blocks) v[4] = 0;
+        for (int64_t k = threadIdx.x; k < pb.count; k += kNT) {
+            const int64_t open = f.free_sum[k];
+            v[3] += open;
+            v[4] += child_blocks + k < b ? open : 0;
+        }
+        wg_sums(v, red64);
+        const Total total{v[0], v[3], v[1], v[2]};
+        if (b == 0 && threadIdx.x == 0) write_status(f, total);
         if (b < child_blocks) {
-            const int64_t need_before = prefix_of(f.need_sum, child_blocks, b, red64).before;
-            const int64_t copies_before = prefix_of(f.copy_sum, child_blocks, b, red64).before;
             const int64_t i = b * kNT + threadIdx.x;
             const int32_t n = i < f.children ? f.need[i] : 0;
             const int own = n & INT32_MAX, copy = (uint32_t)n >> 31;
             int sum;
             // a block's needs can pass 2^31 only where nothing is done
-            const int at = wg_prefix(own, red, sum);
-            const int64_t start = need_before + at;
-            const int64_t place = copies_before + wg_prefix(copy, red, sum);
+            const int64_t start = v[4] + wg_prefix(own, red, sum);
+            const int64_t place = v[5] + wg_prefix(copy, red, sum);
             if (i < f.children) f.start[i] = start;
-            if (copy && done) {
+            if (copy && total.done()) {
                 const Child c = child_of(f, i);
-                f.copies[place] = Copy{c.edge, (int32_t)start, (int32_t)(c.before % f.page_size), 0};
+                f.copies[place] = Copy{c.edge, (int32_t)start, (int32_t)f.past(c.before), 0};
             }
         } else {
-            const int64_t k = b - child_blocks, to = (k + 1) * pb.per < f.pages ? (k + 1) * pb.per : f.pages;
-            int64_t rank = prefix_of(f.free_sum, pb.count, k, red64).before;
-            for (int64_t p0 = k * pb.per; p0 < to; p0 += kNT) {
-                const int64_t p = p0 + threadIdx.x;
-                if (!done) {  // the counts as they were
-                    if (p < to) f.new_refs[p] = f.refs[p] > 0 ? f.refs[p] : 0;
-                    continue;
-                }
-                const bool open = p < to && f.new_refs[p] <= 0;
-                int sum;
-                const int64_t at = rank + wg_prefix(open, red, sum);
-                if (open) {
-                    f.new_refs[p] = at < need;
-                    if (at < need) f.list[at] = (int32_t)p;
-                }
-                rank += sum;
-            }
+            list_block<kNT>(f, pb, b - child_blocks, v[4], total, red);
         }
     }
+}
+
+// One workgroup's view of few children, one a thread.
+constexpr int kOneNT = 1024, kOneWaves = kOneNT / 64;
+struct Few {
+    Child c;
+    int64_t start, place;  // pages and copies before its own
+    int64_t need;
+    int copy;
+    Total total;  // but for the room
+};
+// Exclusive prefix over the workgroup, and the total.
+__device__ __forceinline__ int64_t one_prefix(int64_t v, int64_t& total, int64_t* red) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int64_t s = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t o = (int64_t)__shfl_up((long long)s, d);
+        s += lane >= d ? o : 0;
+    }
+    if (lane == 63) red[wave] = s;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int k = 0; k < kOneWaves; ++k) {
+        before += k < wave ? red[k] : 0;
+        total += red[k];
+    }
+    __syncthreads();
+    return before + s - v;
+}
+// Who goes on to write which page: a table in LDS by open addressing, with twice
+// as many places as there can be pages in it.
+struct Edges {
+    static constexpr int kPlaces = 2 * kOneNT;
+    int32_t page[kPlaces], writers[kPlaces], first[kPlaces];
+    __device__ __forceinline__ void clear() {
+        for (int i = threadIdx.x; i < kPlaces; i += kOneNT) {
+            page[i] = -1;
+            writers[i] = 0;
+            first[i] = INT32_MAX;
+        }
+    }
+    __device__ __forceinline__ int add(int32_t q) {
+        uint32_t at = (uint32_t)q * 2654435761u >> 21;
+        static_assert(kPlaces == 1 << 11, "");
+        for (;;) {
+            const int32_t there = atomicCAS(&page[at], -1, q);
+            if (there == -1 || there == q) break;
+            at = (at + 1) & (kPlaces - 1);
+        }
+        atomicAdd(&writers[at], 1);
+        atomicMin(&first[at], (int32_t)threadIdx.x);
+        return (int)at;
+    }
+};
+// Every thread's child, its edge page (if any) at place `at` of the table and held
+// by `count`; after a barrier.
+__device__ __forceinline__ Few few_children(const Fork& f, const Child& c, const Edges& edges, int at, int32_t count,
+                                            int64_t* red) {
+    Few o;
+    o.c = c;
+    o.copy = c.edge >= 0 && !(count == edges.writers[at] && edges.first[at] == (int32_t)threadIdx.x);
+    const int64_t want = f.pages_for(c.after);
+    const bool too_long = want > f.max_pages || c.after > INT32_MAX;
+    o.need = too_long ? 0 : want - f.pages_for(c.before) + o.copy;
+    int64_t both;
+    // a need is below 2^31, the sum of all below 2^41
+    o.start = one_prefix(o.need, o.total.need, red);
+    o.place = (int32_t)one_prefix(((int64_t)too_long << 32) | o.copy, both, red);
+    o.total.late = both >> 32;
+    o.total.copies = (int32_t)both;
+    return o;
+}
+__device__ __forceinline__ void write_few(const Fork& f, const Few& o, bool done) {
+    const int64_t i = threadIdx.x;
+    if (i >= f.children) return;
+    f.need[i] = (int32_t)o.need | (o.copy << 31);
+    f.start[i] = o.start;
+    if (done && o.copy) f.copies[o.place] = Copy{o.c.edge, (int32_t)o.start, (int32_t)f.past(o.c.before), 0};
+}
+
+// What few children take, by every workgroup, and each one's part of the list.
+__global__ __launch_bounds__(kOneNT) void k_fork_few(Fork f, Blocks pb) {
+    __shared__ Edges edges;
+    __shared__ int64_t red[kOneWaves];
+    __shared__ int red32[kOneWaves];
+    Child c{-1, 0, 0, -1};
+    edges.clear();
+    if (threadIdx.x < f.children) c = child_of(f, threadIdx.x);
+    const int32_t count = c.edge >= 0 ? f.new_refs[c.edge] : 0;
+    __syncthreads();
+    const int at = c.edge >= 0 ? edges.add(c.edge) : 0;
+    __syncthreads();
+    Few o = few_children(f, c, edges, at, count, red);
+    int64_t open = 0;
+    for (int64_t k = threadIdx.x; k < pb.count; k += kOneNT) open += f.free_sum[k];
+    one_prefix(open, o.total.room, red);
+    if (blockIdx.x == 0) {
+        write_few(f, o, o.total.done());
+        if (threadIdx.x == 0) write_status(f, o.total);
+    }
+    for (int64_t b = blockIdx.x; b < pb.count; b += gridDim.x) {
+        int64_t before = 0, rank;
+        for (int64_t k = threadIdx.x; k < b; k += kOneNT) before += f.free_sum[k];
+        one_prefix(before, rank, red);
+        list_block<kOneNT>(f, pb, b, rank, o.total, red32);
+    }
+}
+
+// A step in one workgroup but for what k_fork_write does: the counts are in LDS.
+// Up to kOnePages pages, kOneNT children and sequences, kOneEntries entries of
+// tables (their counting is this workgroup's).
+constexpr int kOnePages = 12288;
+constexpr int64_t kOneEntries = 1 << 16;
+__global__ __launch_bounds__(kOneNT) void k_fork_one(Fork f) {
+    constexpr int kEach = kOnePages / kOneNT, kAhead = 8;
+    __shared__ int32_t refs[kOnePages];
+    __shared__ int32_t kids[kOneNT], held[kOneNT];
+    __shared__ Edges edges;
+    __shared__ int64_t red[kOneWaves];
+    const int t = threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int p = i * kOneNT + t;
+        if (p < (int)f.pages) refs[p] = max(f.refs[p], 0);
+    }
+    Child c{-1, 0, 0, -1};
+    if (t < f.children) c = child_of(f, t);
+    edges.clear();
+    kids[t] = 0;
+    held[t] = t < f.seqs ? (int32_t)f.pages_for(f.tokens_of(t)) : 0;
+    __syncthreads();
+    if (c.parent >= 0) atomicAdd(&kids[c.parent], 1);
+    const int place = c.edge >= 0 ? edges.add(c.edge) : 0;
+    __syncthreads();
+    const uint32_t entries = (uint32_t)(f.seqs * f.max_pages);
+    if (entries) {
+        const Divide by_row((uint32_t)f.max_pages);
+        for (uint32_t e0 = t; e0 < entries; e0 += kOneNT * kAhead) {
+            int32_t page[kAhead], more[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const uint32_t e = e0 + i * kOneNT;
+                page[i] = -1;
+                if (e >= entries) continue;
+                const uint32_t s = by_row(e);
+                more[i] = kids[s] - 1;
+                if (more[i] && (int32_t)(e - s * (uint32_t)f.max_pages) < held[s]) page[i] = f.table[e];
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (f.is_page(page[i])) atomicAdd(&refs[page[i]], more[i]);
+        }
+    }
+    __syncthreads();
+    Few o = few_children(f, c, edges, place, c.edge >= 0 ? refs[c.edge] : 0, red);
+    int64_t open = 0;
+    const int first = t * kEach;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) open += first + i < f.pages && refs[first + i] <= 0;
+    int64_t at = one_prefix(open, o.total.room, red);
+    const bool done = o.total.done();
+    write_few(f, o, done);
+    if (t == 0) write_status(f, o.total);
+    if (done) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int p = first + i;
+            if (p < f.pages && refs[p] <= 0) {
+                refs[p] = at < o.total.need;
+                if (at < o.total.need) f.list[at] = p;
+                ++at;
+            }
+        }
+        __syncthreads();
+        if (o.copy) atomicAdd(&refs[c.edge], -1);
+    }
+    __syncthreads();
+    for (int p = t; p < (int)f.pages; p += kOneNT) f.new_refs[p] = done ? refs[p] : max(f.refs[p], 0);
 }
 
 // 16-byte columns of what one block of an array holds, `bytes` of each of its mid
@@ -313,6 +548,11 @@ __global__ __launch_bounds__(kNT) void k_fork_write(Fork f, States st) {
             if (f.counts_left && copy && done) atomicAdd(&f.new_refs[c.edge], -1);
         }
     }
+    if (f.counts_left) {
+        const int64_t t = (int64_t)blockIdx.x * kNT + threadIdx.x, step = (int64_t)gridDim.x * kNT, taken = f.plan[2];
+        for (int64_t k = t; k < taken; k += step) f.new_refs[f.list[k]] = 1;
+        for (int64_t p = t; p < f.pages && !done; p += step) f.new_refs[p] = max(f.refs[p], 0);  // as they were
+    }
     // items are tiles of a whole block; those past a copy's tokens have nothing to do
     const int64_t copies = f.plan[1];
     for (int u = 0; u < st.count; ++u) {
@@ -329,118 +569,6 @@ __global__ __launch_bounds__(kNT) void k_fork_write(Fork f, States st) {
             char* base = static_cast<char*>(s.base) + o * s.outer_stride;
             copy_tile(s, ct, c.tokens * token, base + c.from * s.row_stride, base + f.list[c.to] * s.row_stride, tile);
         }
-    }
-}
-
-// A step in one workgroup but for what k_fork_write does: the counts are in LDS.
-// Up to kOnePages pages, kOneNT children and sequences, kOneEntries entries of
-// tables (their counting is this workgroup's).
-constexpr int kOneNT = 1024, kOnePages = 12288;
-constexpr int64_t kOneEntries = 1 << 16;
-__global__ __launch_bounds__(kOneNT) void k_fork_one(Fork f) {
-    constexpr int kOneWaves = kOneNT / 64, kEach = kOnePages / kOneNT;
-    __shared__ int32_t refs[kOnePages];
-    __shared__ int32_t kids[kOneNT];
-    __shared__ int32_t edges[kOneNT];
-    __shared__ int64_t red[kOneWaves];
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    // exclusive prefix over the workgroup of two counts in the halves of 64 bits, and the total
-    auto prefix = [&](int64_t v, int64_t& total) {
-        int64_t s = v;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t o = (int64_t)__shfl_up((long long)s, d);
-            s += lane >= d ? o : 0;
-        }
-        if (lane == 63) red[wave] = s;
-        __syncthreads();
-        int64_t before = 0;
-        total = 0;
-#pragma unroll
-        for (int k = 0; k < kOneWaves; ++k) {
-            before += k < wave ? red[k] : 0;
-            total += red[k];
-        }
-        __syncthreads();
-        return before + s - v;
-    };
-    for (int p = t; p < (int)f.pages; p += kOneNT) {
-        const int32_t n = f.refs[p];
-        refs[p] = n > 0 ? n : 0;
-    }
-    kids[t] = 0;
-    Child c{-1, 0, 0, -1};
-    const bool is_child = t < f.children;
-    if (is_child) c = child_of(f, t);
-    edges[t] = c.edge;
-    __syncthreads();
-    if (c.parent >= 0) atomicAdd(&kids[c.parent], 1);
-    __syncthreads();
-    for (int s = wave; s < (int)f.seqs; s += kOneWaves) {
-        const int32_t more = kids[s] - 1;
-        if (!more) continue;
-        const int held = (int)f.pages_for(f.tokens_of(s));
-        for (int j = lane; j < held; j += 64) {
-            const int32_t q = f.table[s * f.max_pages + j];
-            if (f.is_page(q)) atomicAdd(&refs[q], more);
-        }
-    }
-    __syncthreads();
-    // who goes on to write the same page
-    int writers = 0, earlier = 0;
-    if (c.edge >= 0) {
-        for (int k = 0; k < (int)f.children; ++k) {
-            const int same = edges[k] == c.edge;
-            writers += same;
-            earlier += same && k < t;
-        }
-    }
-    const int copy = c.edge >= 0 && !(refs[c.edge] == writers && !earlier);
-    const int64_t want = f.pages_for(c.after);
-    const bool too_long = want > f.max_pages || c.after > INT32_MAX;
-    const int64_t need = too_long ? 0 : want - f.pages_for(c.before) + copy;
-    int64_t all_need, all_copies, all_free;
-    // a need is below 2^31, the sum of all below 2^41
-    const int64_t start = prefix(need, all_need);
-    const int64_t place = prefix(((int64_t)too_long << 32) | copy, all_copies);
-    int64_t open = 0;
-    const int first = t * kEach;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) open += first + i < f.pages && refs[first + i] <= 0;
-    int64_t at = prefix(open, all_free);
-    const int32_t late = (int32_t)(all_copies >> 32), copies = (int32_t)all_copies;
-    const bool done = all_need <= all_free && !late;
-    if (is_child) {
-        f.need[t] = (int32_t)need | (copy << 31);
-        f.start[t] = start;
-        if (done && copy) f.copies[(int32_t)place] = Copy{c.edge, (int32_t)start, (int32_t)(c.before % f.page_size), 0};
-    }
-    if (t == 0) {
-        const int64_t lack = all_need - all_free;
-        f.status[0] = lack <= 0 ? 0 : lack < INT32_MAX ? (int32_t)lack : INT32_MAX;
-        f.status[1] = late;
-        f.status[2] = f.plan[1] = done ? copies : 0;
-        f.status[3] = done ? (int32_t)all_need : 0;
-        f.status[4] = done ? (int32_t)(all_free - all_need) : 0;
-        f.plan[0] = done;
-    }
-    if (done) {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int p = first + i;
-            if (p < f.pages && refs[p] <= 0) {
-                refs[p] = at < all_need;
-                if (at < all_need) f.list[at] = p;
-                ++at;
-            }
-        }
-        __syncthreads();
-        if (copy) atomicAdd(&refs[c.edge], -1);
-    }
-    __syncthreads();
-    for (int p = t; p < (int)f.pages; p += kOneNT) {
-        const int32_t n = f.refs[p];
-        f.new_refs[p] = done ? refs[p] : n > 0 ? n : 0;
     }
 }
 
@@ -469,7 +597,7 @@ ForkPlan fork_plan(int64_t seqs, int64_t children, int64_t pages) {
     p.long_sum = room(p.child_blocks, 4);
     p.free_sum = room(p.pb.count, 4);
     p.copies = room(children, sizeof(Copy));
-    p.plan = room(2, 4);
+    p.plan = room(3, 4);
     p.bytes = at;
     return p;
 }
@@ -487,13 +615,15 @@ struct Compact {
 };
 
 __global__ __launch_bounds__(kNT) void k_compact_count(Compact f, Blocks pb) {
-    __shared__ int64_t red[kWaves];
+    __shared__ int64_t red[1][kWaves];
     for (int64_t b = blockIdx.x; b < pb.count; b += gridDim.x) {
         const int64_t to = (b + 1) * pb.per < f.pages ? (b + 1) * pb.per : f.pages;
-        int64_t n = 0;
-        for (int64_t p = b * pb.per + threadIdx.x; p < to; p += kNT) n += f.refs[p] > 0;
-        n = wg_sum64(n, red);
-        if (threadIdx.x == 0) f.live_sum[b] = (int32_t)n;
+        int64_t n[1] = {0};
+        for (int64_t p0 = b * pb.per + threadIdx.x; p0 < to; p0 += kPageBlock)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) n[0] += p0 + i * kNT < to && f.refs[p0 + i * kNT] > 0;
+        wg_sums(n, red);
+        if (threadIdx.x == 0) f.live_sum[b] = (int32_t)n[0];
     }
 }
 
@@ -501,28 +631,38 @@ __global__ __launch_bounds__(kNT) void k_compact_count(Compact f, Blocks pb) {
 // number p - (live before p), one at p >= n that lives moves as number
 // (live before p) - in; there are n - in of each.
 __global__ __launch_bounds__(kNT) void k_compact_map(Compact f, Blocks pb) {
-    __shared__ int64_t red64[kWaves];
+    __shared__ int64_t red64[2][kWaves];
     __shared__ int red[kWaves];
-    const int64_t n = prefix_of(f.live_sum, pb.count, 0, red64).total, border = n / pb.per;
-    int64_t in = 0;
-    for (int64_t p = border * pb.per + threadIdx.x; p < n; p += kNT) in += f.refs[p] > 0;
-    in = prefix_of(f.live_sum, pb.count, border, red64).before + wg_sum64(in, red64);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        f.status[0] = f.plan[0] = (int32_t)n;
-        f.status[1] = f.plan[1] = (int32_t)(n - in);
-    }
-    for (int64_t b = blockIdx.x; b < pb.count; b += gridDim.x) {
+    for (int64_t b = blockIdx.x; b == blockIdx.x || b < pb.count; b += gridDim.x) {
+        int64_t v[2] = {0, 0};  // live pages, those in the blocks before
+        for (int64_t k = threadIdx.x; k < pb.count; k += kNT) {
+            const int64_t live = f.live_sum[k];
+            v[0] += live;
+            v[1] += k < b ? live : 0;
+        }
+        wg_sums(v, red64);
+        const int64_t n = v[0], border = n / pb.per;
+        int64_t rank = v[1];
+        int64_t in[1] = {0};  // of the whole blocks below n, and of its own block
+        for (int64_t k = threadIdx.x; k < border; k += kNT) in[0] += f.live_sum[k];
+        for (int64_t p0 = border * pb.per + threadIdx.x; p0 < n; p0 += kPageBlock)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) in[0] += p0 + i * kNT < n && f.refs[p0 + i * kNT] > 0;
+        wg_sums(in, red64);
+        if (b == 0 && threadIdx.x == 0) {
+            f.status[0] = f.plan[0] = (int32_t)n;
+            f.status[1] = f.plan[1] = (int32_t)(n - in[0]);
+        }
         const int64_t to = (b + 1) * pb.per < f.pages ? (b + 1) * pb.per : f.pages;
-        int64_t rank = prefix_of(f.live_sum, pb.count, b, red64).before;
         for (int64_t p0 = b * pb.per; p0 < to; p0 += kNT) {
             const int64_t p = p0 + threadIdx.x;
             const bool lives = p < to && f.refs[p] > 0;
             int sum;
             const int64_t before = rank + wg_prefix(lives, red, sum);
             if (p < to) {
-                if (lives && p >= n) f.movers[before - in] = (int32_t)p;
+                if (lives && p >= n) f.movers[before - in[0]] = (int32_t)p;
                 if (!lives && p < n) f.holes[p - before] = (int32_t)p;
-                f.place[p] = !lives ? -1 : p < n ? (int32_t)p : (int32_t)(-2 - (before - in));
+                f.place[p] = !lives ? -1 : p < n ? (int32_t)p : (int32_t)(-2 - (before - in[0]));
             }
             rank += sum;
         }
@@ -579,7 +719,7 @@ CompactPlan compact_plan(int64_t pages) {
     return p;
 }
 
-constexpr int kGrid = 2048;
+constexpr int kGrid = 2048, kCopyGrid = 8192, kFewGrid = 64;
 inline dim3 grid_of(int64_t items) { return dim3((unsigned)(items < 1 ? 1 : items < kGrid ? items : kGrid)); }
 
 // A block's columns of 16 bytes fit 31 bits, items of a copy of every page 64.
@@ -640,7 +780,7 @@ int iso_pages_fork(const int32_t* table, const int32_t* length, int64_t seqs, in
     if (!aligned(workspace, 256)) return ISO_ERR_ARG;
     char* ws = static_cast<char*>(workspace);
     Fork f{table, length, refs, parent, grow, grow_all, seqs, max_pages, pages, page_size, children,
-           new_table, new_length, new_refs, status,
+           1.0 / (double)page_size, new_table, new_length, new_refs, status,
            reinterpret_cast<Mark*>(ws + pl.mark), reinterpret_cast<int32_t*>(ws + pl.kids),
            reinterpret_cast<int32_t*>(ws + pl.list), reinterpret_cast<int32_t*>(ws + pl.need),
            reinterpret_cast<int64_t*>(ws + pl.start), reinterpret_cast<int64_t*>(ws + pl.need_sum),
@@ -648,20 +788,32 @@ int iso_pages_fork(const int32_t* table, const int32_t* length, int64_t seqs, in
            reinterpret_cast<int32_t*>(ws + pl.free_sum), reinterpret_cast<Copy*>(ws + pl.copies),
            reinterpret_cast<int32_t*>(ws + pl.plan), true};
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    const int64_t blocks = pl.child_blocks + pl.pb.count;
-    const int64_t sweep = (pages > seqs ? pages : seqs) / kNT + 1;
-    if (pages <= kOnePages && children <= kOneNT && seqs <= kOneNT && seqs * max_pages <= kOneEntries) {
+    const bool few = children <= kOneNT;
+    if (few && pages <= kOnePages && seqs <= kOneNT && seqs * max_pages <= kOneEntries) {
         f.counts_left = false;
         hipLaunchKernelGGL(k_fork_one, dim3(1), dim3(kOneNT), 0, hs, f);
-        if (children) hipLaunchKernelGGL(k_fork_write, dim3(kGrid), dim3(kNT), 0, hs, f, st);
-        return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
+    } else {
+        if (few) {
+            f.mark = nullptr;
+            f.kids = nullptr;
+        }
+        const int64_t rows = few ? 0 : (seqs + kNT - 1) / kNT;
+        hipLaunchKernelGGL(k_fork_begin, grid_of(pl.pb.count > rows ? pl.pb.count : rows), dim3(kNT), 0, hs, f, pl.pb);
+        if (!few) hipLaunchKernelGGL(k_fork_count, grid_of(pl.child_blocks), dim3(kNT), 0, hs, f);
+        if (seqs) hipLaunchKernelGGL(k_fork_refs, grid_of(seqs), dim3(kNT), 0, hs, f, pl.pb);
+        if (few) {
+            hipLaunchKernelGGL(k_fork_few, dim3((unsigned)(pl.pb.count < 1 ? 1 : pl.pb.count < kFewGrid ? pl.pb.count : kFewGrid)),
+                               dim3(kOneNT), 0, hs, f, pl.pb);
+        } else {
+            hipLaunchKernelGGL(k_fork_need, grid_of(pl.child_blocks), dim3(kNT), 0, hs, f, pl.child_blocks);
+            hipLaunchKernelGGL(k_fork_list, grid_of(pl.child_blocks + pl.pb.count), dim3(kNT), 0, hs, f, pl.pb, pl.child_blocks);
+        }
     }
-    hipLaunchKernelGGL(k_fork_begin, grid_of(sweep), dim3(kNT), 0, hs, f);
-    if (children) hipLaunchKernelGGL(k_fork_count, grid_of(pl.child_blocks), dim3(kNT), 0, hs, f);
-    if (seqs) hipLaunchKernelGGL(k_fork_refs, grid_of(seqs), dim3(kNT), 0, hs, f);
-    hipLaunchKernelGGL(k_fork_need, grid_of(blocks), dim3(kNT), 0, hs, f, pl.pb, pl.child_blocks);
-    hipLaunchKernelGGL(k_fork_list, grid_of(blocks), dim3(kNT), 0, hs, f, pl.pb, pl.child_blocks);
-    if (children) hipLaunchKernelGGL(k_fork_write, dim3(kGrid), dim3(kNT), 0, hs, f, st);
+    if (children) {
+        int64_t items = children;  // a child's table; a tile of an array's block of a copied page
+        for (int i = 0; i < st.count; ++i) items += children * st.b[i].outer * ((st.b[i].inner * st.b[i].mid >> 15) + 1);
+        hipLaunchKernelGGL(k_fork_write, dim3((unsigned)(items < kCopyGrid ? items : kCopyGrid)), dim3(kNT), 0, hs, f, st);
+    }
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 
@@ -696,7 +848,7 @@ int iso_pages_compact(const int32_t* table, int64_t entries, const int32_t* refs
     hipStream_t hs = static_cast<hipStream_t>(stream);
     hipLaunchKernelGGL(k_compact_count, grid_of(pl.pb.count), dim3(kNT), 0, hs, f, pl.pb);
     hipLaunchKernelGGL(k_compact_map, grid_of(pl.pb.count), dim3(kNT), 0, hs, f, pl.pb);
-    hipLaunchKernelGGL(k_compact_write, dim3(kGrid), dim3(kNT), 0, hs, f, st);
+    hipLaunchKernelGGL(k_compact_write, dim3(kCopyGrid), dim3(kNT), 0, hs, f, st);
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 
