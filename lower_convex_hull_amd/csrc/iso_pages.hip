@@ -314,28 +314,38 @@ struct Few {
     int64_t start, place;  // pages and copies before its own
     int64_t need;
     int copy;
-    Total total;  // but for the room
+    Total total;
 };
-// Exclusive prefix over the workgroup, and the total.
-__device__ __forceinline__ int64_t one_prefix(int64_t v, int64_t& total, int64_t* red) {
+// Exclusive prefixes of N values over the workgroup, and their totals.
+template <int N>
+__device__ __forceinline__ void one_prefix(int64_t (&v)[N], int64_t (&total)[N], int64_t (*red)[kOneWaves]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int64_t s = v;
+    int64_t s[N];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int64_t o = (int64_t)__shfl_up((long long)s, d);
-        s += lane >= d ? o : 0;
-    }
-    if (lane == 63) red[wave] = s;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
+    for (int n = 0; n < N; ++n) s[n] = v[n];
 #pragma unroll
-    for (int k = 0; k < kOneWaves; ++k) {
-        before += k < wave ? red[k] : 0;
-        total += red[k];
+    for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int64_t o = (int64_t)__shfl_up((long long)s[n], d);
+            s[n] += lane >= d ? o : 0;
+        }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        if (lane == 63) red[n][wave] = s[n];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        int64_t before = 0;
+        total[n] = 0;
+#pragma unroll
+        for (int k = 0; k < kOneWaves; ++k) {
+            before += k < wave ? red[n][k] : 0;
+            total[n] += red[n][k];
+        }
+        v[n] = before + s[n] - v[n];
     }
     __syncthreads();
-    return before + s - v;
 }
 // Who goes on to write which page: a table in LDS by open addressing, with twice
 // as many places as there can be pages in it.
@@ -363,21 +373,23 @@ struct Edges {
     }
 };
 // Every thread's child, its edge page (if any) at place `at` of the table and held
-// by `count`; after a barrier.
+// by `count`; `room` the free pages it has counted, then those before them.  After
+// a barrier.
 __device__ __forceinline__ Few few_children(const Fork& f, const Child& c, const Edges& edges, int at, int32_t count,
-                                            int64_t* red) {
+                                            int64_t& room, int64_t (*red)[kOneWaves]) {
     Few o;
     o.c = c;
     o.copy = c.edge >= 0 && !(count == edges.writers[at] && edges.first[at] == (int32_t)threadIdx.x);
     const int64_t want = f.pages_for(c.after);
     const bool too_long = want > f.max_pages || c.after > INT32_MAX;
     o.need = too_long ? 0 : want - f.pages_for(c.before) + o.copy;
-    int64_t both;
-    // a need is below 2^31, the sum of all below 2^41
-    o.start = one_prefix(o.need, o.total.need, red);
-    o.place = (int32_t)one_prefix(((int64_t)too_long << 32) | o.copy, both, red);
-    o.total.late = both >> 32;
-    o.total.copies = (int32_t)both;
+    // a need is below 2^31, the sum of all below 2^41; children too long and copies share a sum
+    int64_t v[3] = {o.need, ((int64_t)too_long << 32) | o.copy, room}, total[3];
+    one_prefix(v, total, red);
+    o.start = v[0];
+    o.place = (int32_t)v[1];
+    room = v[2];
+    o.total = Total{total[0], total[2], total[1] >> 32, (int32_t)total[1]};
     return o;
 }
 __device__ __forceinline__ void write_few(const Fork& f, const Few& o, bool done) {
@@ -391,7 +403,7 @@ __device__ __forceinline__ void write_few(const Fork& f, const Few& o, bool done
 // What few children take, by every workgroup, and each one's part of the list.
 __global__ __launch_bounds__(kOneNT) void k_fork_few(Fork f, Blocks pb) {
     __shared__ Edges edges;
-    __shared__ int64_t red[kOneWaves];
+    __shared__ int64_t red[3][kOneWaves];
     __shared__ int red32[kOneWaves];
     Child c{-1, 0, 0, -1};
     edges.clear();
@@ -400,19 +412,18 @@ __global__ __launch_bounds__(kOneNT) void k_fork_few(Fork f, Blocks pb) {
     __syncthreads();
     const int at = c.edge >= 0 ? edges.add(c.edge) : 0;
     __syncthreads();
-    Few o = few_children(f, c, edges, at, count, red);
     int64_t open = 0;
     for (int64_t k = threadIdx.x; k < pb.count; k += kOneNT) open += f.free_sum[k];
-    one_prefix(open, o.total.room, red);
+    const Few o = few_children(f, c, edges, at, count, open, red);
     if (blockIdx.x == 0) {
         write_few(f, o, o.total.done());
         if (threadIdx.x == 0) write_status(f, o.total);
     }
     for (int64_t b = blockIdx.x; b < pb.count; b += gridDim.x) {
-        int64_t before = 0, rank;
-        for (int64_t k = threadIdx.x; k < b; k += kOneNT) before += f.free_sum[k];
+        int64_t before[1] = {0}, rank[1];
+        for (int64_t k = threadIdx.x; k < b; k += kOneNT) before[0] += f.free_sum[k];
         one_prefix(before, rank, red);
-        list_block<kOneNT>(f, pb, b, rank, o.total, red32);
+        list_block<kOneNT>(f, pb, b, rank[0], o.total, red32);
     }
 }
 
@@ -426,48 +437,54 @@ __global__ __launch_bounds__(kOneNT) void k_fork_one(Fork f) {
     __shared__ int32_t refs[kOnePages];
     __shared__ int32_t kids[kOneNT], held[kOneNT];
     __shared__ Edges edges;
-    __shared__ int64_t red[kOneWaves];
+    __shared__ int64_t red[3][kOneWaves];
     const int t = threadIdx.x;
+    const uint32_t entries = (uint32_t)(f.seqs * f.max_pages);
+    // entries of the tables, whether they count or not: the first are on their way with all else
+    int32_t page[kAhead];
+    auto load = [&](uint32_t e0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const uint32_t e = e0 + i * kOneNT;
+            page[i] = e < entries ? f.table[e] : -1;
+        }
+    };
+    load(t);
+    int32_t own[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int p = i * kOneNT + t;
-        if (p < (int)f.pages) refs[p] = max(f.refs[p], 0);
+        own[i] = p < (int)f.pages ? max(f.refs[p], 0) : 1;
     }
+    held[t] = t < f.seqs ? (int32_t)f.pages_for(f.tokens_of(t)) : 0;
     Child c{-1, 0, 0, -1};
     if (t < f.children) c = child_of(f, t);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) refs[i * kOneNT + t] = own[i];  // a place behind the last page: held
     edges.clear();
     kids[t] = 0;
-    held[t] = t < f.seqs ? (int32_t)f.pages_for(f.tokens_of(t)) : 0;
     __syncthreads();
     if (c.parent >= 0) atomicAdd(&kids[c.parent], 1);
     const int place = c.edge >= 0 ? edges.add(c.edge) : 0;
     __syncthreads();
-    const uint32_t entries = (uint32_t)(f.seqs * f.max_pages);
-    if (entries) {
-        const Divide by_row((uint32_t)f.max_pages);
-        for (uint32_t e0 = t; e0 < entries; e0 += kOneNT * kAhead) {
-            int32_t page[kAhead], more[kAhead];
+    const Divide by_row((uint32_t)f.max_pages);
+    for (uint32_t e0 = t; e0 < entries; e0 += kOneNT * kAhead) {
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const uint32_t e = e0 + i * kOneNT;
-                page[i] = -1;
-                if (e >= entries) continue;
-                const uint32_t s = by_row(e);
-                more[i] = kids[s] - 1;
-                if (more[i] && (int32_t)(e - s * (uint32_t)f.max_pages) < held[s]) page[i] = f.table[e];
-            }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (f.is_page(page[i])) atomicAdd(&refs[page[i]], more[i]);
+        for (int i = 0; i < kAhead; ++i) {
+            const uint32_t e = e0 + i * kOneNT;
+            if (e >= entries || !f.is_page(page[i])) continue;
+            const uint32_t s = by_row(e);
+            const int32_t more = kids[s] - 1;
+            if (more && (int32_t)(e - s * (uint32_t)f.max_pages) < held[s]) atomicAdd(&refs[page[i]], more);
         }
+        load(e0 + kOneNT * kAhead);
     }
     __syncthreads();
-    Few o = few_children(f, c, edges, place, c.edge >= 0 ? refs[c.edge] : 0, red);
-    int64_t open = 0;
+    int64_t at = 0;
     const int first = t * kEach;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) open += first + i < f.pages && refs[first + i] <= 0;
-    int64_t at = one_prefix(open, o.total.room, red);
+    for (int i = 0; i < kEach; ++i) at += refs[first + i] <= 0;
+    const Few o = few_children(f, c, edges, place, c.edge >= 0 ? refs[c.edge] : 0, at, red);
     const bool done = o.total.done();
     write_few(f, o, done);
     if (t == 0) write_status(f, o.total);
@@ -475,7 +492,7 @@ __global__ __launch_bounds__(kOneNT) void k_fork_one(Fork f) {
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int p = first + i;
-            if (p < f.pages && refs[p] <= 0) {
+            if (refs[p] <= 0) {
                 refs[p] = at < o.total.need;
                 if (at < o.total.need) f.list[at] = p;
                 ++at;
