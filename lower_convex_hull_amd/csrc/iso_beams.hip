@@ -75,8 +75,8 @@ __device__ __forceinline__ uint32_t reached_by(const uint32_t (&v)[V], int n) {
 template <typename T>
 constexpr int kLowBits = std::is_same<T, float>::value ? 0 : std::is_same<T, __bf16>::value ? 16 : 13;
 
-// Room for the candidates that reach a bound; where more do, a round of a
-// maximum each finds the best.
+// Room for the candidates that reach a bound (in a piece: 4 a thread); where more
+// do, a round of a maximum each finds the best.
 constexpr int kRoom = 1024;
 
 // How many of `found` keys in LDS are above k; the next 7 places hold keys that
@@ -145,8 +145,9 @@ __global__ __launch_bounds__(NT, 5) void k_beam_pieces(const T* __restrict__ log
                                                     Beams b, Scale sc, uint32_t splits, uint64_t* __restrict__ keys,
                                                     PieceSum* __restrict__ sums) {
     typedef typename Wide<T>::A Vec;
-    constexpr int N = Wide<T>::N, kWaves = NT / 64, kVectors = kRoom / 2;
-    __shared__ uint64_t room[kRoom + 8];
+    constexpr int N = Wide<T>::N, kWaves = NT / 64, kPlaces = NT * 4, kVectors = NT * 2;
+    static_assert(kPlaces <= kRoom, "");
+    __shared__ uint64_t room[kPlaces + 8];
     __shared__ Vec vec[kVectors];
     __shared__ int at[kVectors];
     __shared__ uint32_t most[NT];
@@ -237,15 +238,15 @@ __global__ __launch_bounds__(NT, 5) void k_beam_pieces(const T* __restrict__ log
                     const float v = first >= 0 ? (float)vec[i / N][i % N] : i % N ? -INFINITY : (float)x[k];
                     if (v >= low) {
                         const int p = atomicAdd(&count, 1);
-                        if (p < kRoom) room[p] = token_key(v, k);
+                        if (p < kPlaces) room[p] = token_key(v, k);
                     }
                 }
             }
             __syncthreads();
-            const int found = held <= kVectors ? count : kRoom + 1;
+            const int found = held <= kVectors ? count : kPlaces + 1;
             // place i of list l of a batch item at i * lists + l
             uint64_t* out = keys + (int64_t)item * lists * b.take + list;
-            if (found <= kRoom) {
+            if (found <= kPlaces) {
                 if (threadIdx.x < 8) room[found + threadIdx.x] = 0;
                 __syncthreads();
                 for (int i = threadIdx.x; i < found; i += NT) {
@@ -440,16 +441,31 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
     }
 }
 
-constexpr int kPieceNT = 256, kPieceU = 8;
+// A piece's workgroup.  Long rows in pieces of 32 KB (256 threads of 8 vectors) where
+// there are enough to fill the GPU (64 x 8 x 32000 bf16, 1024 pieces: 20.6 us, 22.8 in
+// pieces of 16 KB; 32 x 4 x 200000 f32 31.4 and 36.6), else of 16 KB (4 x 8 x 131072 bf16:
+// 13.8 us, 14.4 in pieces of 32; 8 x 4 x 32768 12.4 and 13.2; they meet at 360 pieces).
+// Rows of at most 8 KB by single waves, 4 KB each (256 x 8 x 2000 bf16: 14.2 us, 19.4 with
+// 256 threads), but where `take` is not well below a wave's lanes: their maxima would
+// bound little.  Counted by the bytes of a row, not by its type's elements.
+// Logits past half of the last-level cache are streamed (128 x 8 x 200000 f32: 149 us,
+// 172 through the caches; bf16 94 and 102).
+constexpr int64_t kWaveRow = 8 << 10, kManyPieces = 360;
+constexpr int kWaveTake = 32;
 struct SelectPlan {
+    int threads, vectors;  // of a piece: 256 x 8, 256 x 4, 64 x 4
     int splits;
     size_t off_sums, bytes;
 };
 SelectPlan select_plan(int64_t batch, int64_t beams, int64_t vocab, int64_t take, int dtype) {
-    const int64_t chunk = (int64_t)kPieceNT * kPieceU * 16 / (int64_t)size_of(dtype);
+    const int64_t size = (int64_t)size_of(dtype), row = vocab * size, rows = batch * beams;
     SelectPlan p;
+    const bool wave = row <= kWaveRow && take <= kWaveTake;
+    p.threads = wave ? 64 : 256;
+    p.vectors = !wave && rows * ((row + (32 << 10) - 1) / (32 << 10)) > kManyPieces ? 8 : 4;
+    const int64_t chunk = (int64_t)p.threads * p.vectors * 16 / size;
     p.splits = (int)((vocab + chunk - 1) / chunk);
-    const size_t items = (size_t)(batch * beams) * (size_t)p.splits;
+    const size_t items = (size_t)rows * (size_t)p.splits;
     p.off_sums = align_up(items * (size_t)take * sizeof(uint64_t));
     p.bytes = p.off_sums + align_up(items * sizeof(PieceSum));
     return p;
@@ -571,9 +587,20 @@ int iso_beam_select(const void* logits, int dtype, int64_t batch, int64_t beams,
     const dim3 grid((unsigned)(rows < kMaxGrid ? rows : kMaxGrid), (unsigned)(pl.splits < 65535 ? pl.splits : 65535));
     by_dtype(dtype, [&](auto v) {
         typedef decltype(v) T;
-        hipLaunchKernelGGL((k_beam_pieces<T, kPieceNT, kPieceU, false>), grid, dim3(kPieceNT), 0, st,
-                           static_cast<const T*>(logits), (uint32_t)rows, (int)vocab, ld, b, sc, (uint32_t)pl.splits, keys,
-                           sums);
+        auto start = [&](auto nt, auto u, auto stream) {
+            constexpr int NT = decltype(nt)::value, U = decltype(u)::value;
+            hipLaunchKernelGGL((k_beam_pieces<T, NT, U, decltype(stream)::value>), grid, dim3(NT), 0, st,
+                               static_cast<const T*>(logits), (uint32_t)rows, (int)vocab, ld, b, sc, (uint32_t)pl.splits,
+                               keys, sums);
+        };
+        typedef std::integral_constant<int, 256> Wg;
+        typedef std::integral_constant<int, 64> Wave;
+        typedef std::integral_constant<int, 4> Four;
+        typedef std::integral_constant<int, 8> Eight;
+        if (pl.threads == 64) start(Wave{}, Four{}, std::false_type{});
+        else if (pl.vectors == 4) start(Wg{}, Four{}, std::false_type{});
+        else if (streamed<T>(rows, vocab)) start(Wg{}, Eight{}, std::true_type{});
+        else start(Wg{}, Eight{}, std::false_type{});
     });
     hipLaunchKernelGGL(k_beam_join, dim3((unsigned)(batch < kMaxGrid ? batch : kMaxGrid)), dim3(kJoinNT), 0, st, batch, b,
                        sc, pl.splits, keys, sums, SelectOut{out_score, out_logp, out_parent, out_token});

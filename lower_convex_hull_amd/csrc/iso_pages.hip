@@ -686,6 +686,42 @@ __global__ __launch_bounds__(kNT) void k_compact_map(Compact f, Blocks pb) {
     }
 }
 
+// The same in one workgroup, up to kOnePages pages.
+__global__ __launch_bounds__(kOneNT) void k_compact_one(Compact f) {
+    constexpr int kEach = kOnePages / kOneNT;
+    __shared__ uint8_t lives[kOnePages];
+    __shared__ int64_t red[1][kOneWaves];
+    const int t = threadIdx.x, first = t * kEach;
+    int32_t own[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) own[i] = i * kOneNT + t < f.pages ? f.refs[i * kOneNT + t] : 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) lives[i * kOneNT + t] = own[i] > 0;
+    __syncthreads();
+    int64_t rank[1] = {0}, n[1], in[1] = {0}, all[1];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) rank[0] += lives[first + i];
+    one_prefix(rank, n, red);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) in[0] += first + i < n[0] && lives[first + i];
+    one_prefix(in, all, red);
+    int32_t before = (int32_t)rank[0];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int p = first + i;
+        if (p >= f.pages) break;
+        const bool live = lives[p];
+        if (live && p >= n[0]) f.movers[before - all[0]] = p;
+        if (!live && p < n[0]) f.holes[p - before] = p;
+        f.place[p] = !live ? -1 : p < n[0] ? p : (int32_t)(-2 - (before - all[0]));
+        before += live;
+    }
+    if (t == 0) {
+        f.status[0] = f.plan[0] = (int32_t)n[0];
+        f.status[1] = f.plan[1] = (int32_t)(n[0] - all[0]);
+    }
+}
+
 __global__ __launch_bounds__(kNT) void k_compact_write(Compact f, States st) {
     const int64_t n = f.plan[0], moves = f.plan[1];
     const int64_t t = (int64_t)blockIdx.x * kNT + threadIdx.x, step = (int64_t)gridDim.x * kNT;
@@ -863,9 +899,15 @@ int iso_pages_compact(const int32_t* table, int64_t entries, const int32_t* refs
     Compact f{table, refs, entries, pages, new_table, new_refs, moved, status,
               at(pl.live_sum), at(pl.place), at(pl.holes), at(pl.movers), at(pl.plan)};
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    hipLaunchKernelGGL(k_compact_count, grid_of(pl.pb.count), dim3(kNT), 0, hs, f, pl.pb);
-    hipLaunchKernelGGL(k_compact_map, grid_of(pl.pb.count), dim3(kNT), 0, hs, f, pl.pb);
-    hipLaunchKernelGGL(k_compact_write, dim3(kCopyGrid), dim3(kNT), 0, hs, f, st);
+    if (pages <= kOnePages) {
+        hipLaunchKernelGGL(k_compact_one, dim3(1), dim3(kOneNT), 0, hs, f);
+    } else {
+        hipLaunchKernelGGL(k_compact_count, grid_of(pl.pb.count), dim3(kNT), 0, hs, f, pl.pb);
+        hipLaunchKernelGGL(k_compact_map, grid_of(pl.pb.count), dim3(kNT), 0, hs, f, pl.pb);
+    }
+    int64_t items = (entries + kNT - 1) / kNT + (pages + kNT - 1) / kNT;
+    for (int i = 0; i < st.count; ++i) items += pages / 2 * st.b[i].outer * ((st.b[i].inner * st.b[i].mid >> 15) + 1);
+    hipLaunchKernelGGL(k_compact_write, dim3((unsigned)(items < 1 ? 1 : items < kCopyGrid ? items : kCopyGrid)), dim3(kNT), 0, hs, f, st);
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 

@@ -704,58 +704,64 @@ def beam_select(logits, score, *, take=None, weight=None, ended=None, end_token:
     return out, logp, parent, token
 
 
-def _joined(shape, stride):
+def _joined(shape, stride, begin, end):
     """(count, stride) of dimensions taken as one, None if they are not one; those of size 1 do not count."""
     n, step = 1, 0
-    for size, by in zip(shape, stride):
-        if size == 1:
-            continue
-        if n > 1 and step != size * by:
-            return None
-        n, step = n * size, by
+    for i in range(begin, end):
+        size = shape[i]
+        if size != 1:
+            if n != 1 and step != size * stride[i]:
+                return None
+            n, step = n * size, stride[i]
     return n, step
 
 
-def _blocks(launch, tensors, dims, token_dim=None):
-    """(array of Blocks, count) of tensors whose rows (or pages) are dimension
-    `dim`, with the sizes of those dimensions.  What lies behind a row is blocks
-    of adjacent elements at one stride: from `token_dim` on, or as long as they get."""
-    tensors = (tensors,) if hasattr(tensors, "data_ptr") else tuple(tensors)
-    dims = (dims,) * len(tensors) if isinstance(dims, int) else tuple(dims)
-    if len(dims) != len(tensors):
+def _block(launch, t, dim, token_dim):
+    """The Blocks of a tensor whose rows (or pages) are dimension `dim`.  What lies
+    behind a row is blocks of adjacent elements at one stride: from `token_dim` on,
+    or as long as they get."""
+    if t.get_device() != launch.index:
+        raise TypeError(f"every tensor must be on {launch.dev}")
+    shape, stride = t.shape, t.stride()
+    at = dims = len(shape)
+    if not 0 <= dim < dims:
+        raise ValueError(f"a tensor of shape {tuple(shape)} has no dimension {dim}")
+    size = inner = t.element_size()
+    last = dim + 1 if token_dim is None else token_dim
+    if not dim < last <= dims or (token_dim is not None and last == dims):
+        raise ValueError("token_dim must be behind page_dim")
+    while at > last:
+        if shape[at - 1] != 1 and stride[at - 1] * size != inner:
+            if token_dim is None:
+                break
+            raise ValueError("a page's tokens must be adjacent from token_dim on")
+        at -= 1
+        inner *= shape[at]
+    outer, mid = _joined(shape, stride, 0, dim), _joined(shape, stride, dim + 1, at)
+    if outer is None or mid is None:
+        raise ValueError("the dimensions before the rows, and those behind them, must have one stride")
+    if launch.other is not None:
+        t.record_stream(launch.other)
+    return Blocks(t.data_ptr(), outer[0], outer[1] * size, stride[dim] * size, mid[0], mid[1] * size, inner)
+
+
+def _blocks(launch, tensors, dims, rows, token_dim=None):
+    """(array of Blocks, count) of tensors that hold `rows` rows each."""
+    if hasattr(tensors, "data_ptr"):
+        tensors = (tensors,)
+    count = len(tensors)
+    if isinstance(dims, int):
+        dims = (dims,) * count
+    if len(dims) != count:
         raise ValueError("one dimension for each tensor")
-    if len(tensors) > ISO_MAX_BLOCKS:
+    if count > ISO_MAX_BLOCKS:
         raise ValueError(f"at most {ISO_MAX_BLOCKS} tensors a call")
-    out, sizes = (Blocks * max(1, len(tensors)))(), []
-    for i, (t, dim) in enumerate(zip(tensors, dims)):
-        if t.get_device() != launch.index:
-            raise TypeError(f"every tensor must be on {launch.dev}")
-        if not 0 <= dim < t.dim():
-            raise ValueError(f"a tensor of shape {tuple(t.shape)} has no dimension {dim}")
-        shape, stride, size = t.shape, t.stride(), t.element_size()
-        at, inner = len(shape), 1
-        if token_dim is None:
-            while at > dim + 1 and (shape[at - 1] == 1 or stride[at - 1] == inner):
-                at -= 1
-                inner *= shape[at]
-        else:
-            if not dim < token_dim < len(shape):
-                raise ValueError("token_dim must be behind page_dim")
-            while at > token_dim:
-                at -= 1
-                if shape[at] != 1 and stride[at] != inner:
-                    raise ValueError("a page's tokens must be adjacent from token_dim on")
-                inner *= shape[at]
-        outer, mid = _joined(shape[:dim], stride[:dim]), _joined(shape[dim + 1:at], stride[dim + 1:at])
-        if outer is None or mid is None:
-            raise ValueError("the dimensions before the rows, and those behind them, must have one stride")
-        sizes.append(shape[dim])
-        b = out[i]
-        b.base, b.inner, b.row_stride = t.data_ptr(), inner * size, stride[dim] * size
-        (b.outer, b.outer_stride), (b.mid, b.mid_stride) = (outer[0], outer[1] * size), (mid[0], mid[1] * size)
-        if launch.other is not None:
-            t.record_stream(launch.other)
-    return out, len(tensors), sizes
+    blocks = []
+    for t, dim in zip(tensors, dims):
+        blocks.append(_block(launch, t, dim, token_dim))
+        if t.shape[dim] != rows:
+            raise ValueError(f"dimension {dim} of a tensor of shape {tuple(t.shape)} must have {rows} rows or pages")
+    return (Blocks * count)(*blocks) if count else None, count
 
 
 def beam_reorder(states, parent, *, dim=0, stream=None):
@@ -769,9 +775,7 @@ def beam_reorder(states, parent, *, dim=0, stream=None):
         raise ValueError("parent must have the shape (batch, beams)")
     pr = c.use(parent, "parent", parent.shape, (c.torch.int32,))
     batch, beams = parent.shape
-    blocks, count, sizes = _blocks(c, states, dim)
-    if any(n != batch * beams for n in sizes):
-        raise ValueError("each state must have batch * beams rows")
+    blocks, count = _blocks(c, states, dim, batch * beams)
     _done(c.lib.iso_beam_reorder(blocks, count, pr, batch, beams, c.handle))
     return states
 
@@ -795,9 +799,7 @@ def pages_fork(table, length, refs, parent, *, page_size: int, grow=1, pools=(),
     rf, pr = c.use(refs, "refs", refs.shape, i32), c.use(parent, "parent", parent.shape, i32)
     pages, children = refs.shape[0], parent.shape[0]
     each, gr = (grow, None) if isinstance(grow, int) else (0, c.use(grow, "grow", parent.shape, i32))
-    blocks, count, sizes = _blocks(c, pools, page_dim, token_dim)
-    if any(n != pages for n in sizes):
-        raise ValueError("each pool must have as many pages as refs")
+    blocks, count = _blocks(c, pools, page_dim, pages, token_dim)
     for p in ((pools,) if hasattr(pools, "data_ptr") else pools):
         if p.shape[token_dim] != page_size:
             raise ValueError("each pool must have page_size tokens a page")
@@ -821,9 +823,7 @@ def pages_compact(table, refs, *, pools=(), page_dim: int = 0, stream=None):
         raise ValueError("refs must be 1-D")
     tb, rf = c.use(table, "table", table.shape, (t.int32,)), c.use(refs, "refs", refs.shape, (t.int32,))
     pages = refs.shape[0]
-    blocks, count, sizes = _blocks(c, pools, page_dim)
-    if any(n != pages for n in sizes):
-        raise ValueError("each pool must have as many pages as refs")
+    blocks, count = _blocks(c, pools, page_dim, pages)
     new_table, new_refs = c.new(t.int32, *table.shape), c.new(t.int32, pages)
     moved, status = c.new(t.int32, pages), c.new(t.int32, 2)
     nb = c.lib.iso_pages_compact_workspace_bytes(pages)

@@ -188,7 +188,7 @@ class _Fake:
 
 def as_rows(t, dim, token_dim=None):
     """Every row's bytes as the description says they lie, by rows."""
-    b = iso._blocks(_Fake(), t, dim, token_dim)[0][0]
+    b = iso._blocks(_Fake(), t, dim, t.shape[dim], token_dim)[0][0]
     rows = []
     for r in range(t.shape[dim]):
         rows.append(b"".join(ctypes.string_at(b.base + o * b.outer_stride + r * b.row_stride + m * b.mid_stride, b.inner)
@@ -211,12 +211,9 @@ def test_tensors_as_blocks():
         assert (b.outer, b.mid) == (outer, mid), (t.shape, dim)
         for r, got in enumerate(rows):
             assert got == t.select(dim, r).contiguous().numpy().tobytes()
-    for t, dim, token_dim in ((full[:, :, :2, :4], 0, None), (full[:, 1:3], 2, None), (full[..., :3], 1, 3)):
+    for t, dim, token_dim in ((full[:, :, :2, :4], 0, None), (full[:, 1:3], 2, None), (full[..., :3], 1, 3), (full, 1, 1), (full, 1, 5)):
         with pytest.raises(ValueError):
-            iso._blocks(_Fake(), t, dim, token_dim)
-    with pytest.raises(ValueError):
-        iso._blocks(_Fake(), full, 5)
-    with pytest.raises(ValueError):
-        iso._blocks(_Fake(), [full] * 17, 0)
-    with pytest.raises(ValueError):
-        iso._blocks(_Fake(), [full, base], (0, 0, 0))
+            iso._blocks(_Fake(), t, dim, t.shape[dim], token_dim)
+    for tensors, dims, rows in ((full, 5, 5), (full, -1, 5), ([full] * 17, 0, 2), ([full, base], (0, 0, 0), 2), (full, 1, 5)):
+        with pytest.raises(ValueError):
+            iso._blocks(_Fake(), tensors, dims, rows)
