@@ -486,7 +486,7 @@ struct Moves {
     int32_t to[kMaxBeams], from[kMaxBeams];
     int n;
 };
-template <bool TAIL, int U>
+template <bool TAIL, int U, bool STREAM>
 __device__ __forceinline__ void reorder_columns(const iso_blocks& s, char* base, const Moves& mv, int shift) {
     const uint32_t whole = (uint32_t)(s.inner / 16), cols = TAIL ? 1 : whole, all = (uint32_t)s.mid * cols;
     const int width = TAIL ? (int)(s.inner % 16) : 16;
@@ -504,16 +504,18 @@ __device__ __forceinline__ void reorder_columns(const iso_blocks& s, char* base,
                 const uint32_t m = TAIL ? col : by_cols(col), c = TAIL ? 0 : col - m * cols;
                 char* at = base + m * s.mid_stride + (int64_t)c * 16;
                 put[u] = at + mv.to[k] * s.row_stride;
-                v[u] = load_bytes(at + mv.from[k] * s.row_stride, width);
+                const char* got = at + mv.from[k] * s.row_stride;
+                v[u] = TAIL ? load_bytes(got, width) : load_quad<STREAM>(got);
             }
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (put[u]) store_bytes(put[u], width, v[u]);
+            if (put[u]) TAIL ? store_bytes(put[u], width, v[u]) : store_quad<STREAM>(put[u], v[u]);
     }
 }
+template <bool STREAM>
 __global__ __launch_bounds__(kReorderNT) void k_beam_reorder(States st, const int32_t* __restrict__ parent,
                                                              uint32_t batch, int beams, int shift) {
     __shared__ Moves mv;
@@ -541,8 +543,8 @@ __global__ __launch_bounds__(kReorderNT) void k_beam_reorder(States st, const in
             __syncthreads();
             if (mv.n) {
                 char* base = static_cast<char*>(s.base) + o * s.outer_stride + (int64_t)b * beams * s.row_stride;
-                reorder_columns<false, kReorderU>(s, base, mv, shift);
-                if (s.inner % 16) reorder_columns<true, 1>(s, base, mv, shift - 3);
+                reorder_columns<false, kReorderU, STREAM>(s, base, mv, shift);
+                if (s.inner % 16) reorder_columns<true, 1, false>(s, base, mv, shift - 3);
             }
             __syncthreads();  // the list is used again
         }
@@ -631,8 +633,13 @@ int iso_beam_reorder(const iso_blocks* states, int count, const int32_t* parent,
         items = batch * s.outer > items ? batch * s.outer : items;
     }
     const dim3 grid((unsigned)(tiles < 65536 ? tiles : 65536), (unsigned)(items < 16384 ? items : 16384));
-    hipLaunchKernelGGL(k_beam_reorder, grid, dim3(kReorderNT), 0, static_cast<hipStream_t>(stream), st, parent,
-                       (uint32_t)batch, (int)beams, shift);
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    auto start = [&](auto big) {
+        hipLaunchKernelGGL(k_beam_reorder<decltype(big)::value>, grid, dim3(kReorderNT), 0, hs, st, parent, (uint32_t)batch,
+                           (int)beams, shift);
+    };
+    if (streamed(st, rows)) start(std::true_type{});
+    else start(std::false_type{});
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 

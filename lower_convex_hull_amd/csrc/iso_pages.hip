@@ -514,6 +514,7 @@ struct CopyTile {
         : cols((uint32_t)((bytes + 15) / 16)), all((uint32_t)s.mid * cols) {}
     __device__ __forceinline__ uint32_t tiles() const { return (all + kNT * kCopyU - 1) / (kNT * kCopyU); }
 };
+template <bool STREAM>
 __device__ __forceinline__ void copy_tile(const iso_blocks& s, const CopyTile& c, int64_t bytes, const char* from, char* to,
                                           uint32_t tile) {
     const Divide by_cols(c.cols);
@@ -528,7 +529,7 @@ __device__ __forceinline__ void copy_tile(const iso_blocks& s, const CopyTile& c
             const uint32_t m = by_cols(col), k = col - m * c.cols;
             at[u] = m * s.mid_stride + (int64_t)k * 16;
             if (k + 1 < c.cols || rest == 16) {
-                v[u] = *reinterpret_cast<const Wide16*>(from + at[u]);
+                v[u] = load_quad<STREAM>(from + at[u]);
             } else {  // the end of a run, taken at once
                 store_bytes(to + at[u], rest, load_bytes(from + at[u], rest));
                 at[u] = -1;
@@ -537,10 +538,11 @@ __device__ __forceinline__ void copy_tile(const iso_blocks& s, const CopyTile& c
     }
 #pragma unroll
     for (int u = 0; u < kCopyU; ++u)
-        if (at[u] >= 0) *reinterpret_cast<Wide16*>(to + at[u]) = v[u];
+        if (at[u] >= 0) store_quad<STREAM>(to + at[u], v[u]);
 }
 
 // The children's tables and lengths, then the copies.
+template <bool STREAM>
 __global__ __launch_bounds__(kNT) void k_fork_write(Fork f, States st) {
     const bool done = f.plan[0];
     for (int64_t i = blockIdx.x; i < f.children; i += gridDim.x) {
@@ -584,7 +586,7 @@ __global__ __launch_bounds__(kNT) void k_fork_write(Fork f, States st) {
             const CopyTile ct(s, c.tokens * token);
             if (tile >= ct.tiles()) continue;
             char* base = static_cast<char*>(s.base) + o * s.outer_stride;
-            copy_tile(s, ct, c.tokens * token, base + c.from * s.row_stride, base + f.list[c.to] * s.row_stride, tile);
+            copy_tile<STREAM>(s, ct, c.tokens * token, base + c.from * s.row_stride, base + f.list[c.to] * s.row_stride, tile);
         }
     }
 }
@@ -722,6 +724,7 @@ __global__ __launch_bounds__(kOneNT) void k_compact_one(Compact f) {
     }
 }
 
+template <bool STREAM>
 __global__ __launch_bounds__(kNT) void k_compact_write(Compact f, States st) {
     const int64_t n = f.plan[0], moves = f.plan[1];
     const int64_t t = (int64_t)blockIdx.x * kNT + threadIdx.x, step = (int64_t)gridDim.x * kNT;
@@ -744,7 +747,7 @@ __global__ __launch_bounds__(kNT) void k_compact_write(Compact f, States st) {
         for (int64_t item = blockIdx.x; item < moves * per; item += gridDim.x) {
             const int64_t k = item / per, o = (item - k * per) / tiles;
             char* base = static_cast<char*>(s.base) + o * s.outer_stride;
-            copy_tile(s, ct, s.inner, base + f.movers[k] * s.row_stride, base + f.holes[k] * s.row_stride,
+            copy_tile<STREAM>(s, ct, s.inner, base + f.movers[k] * s.row_stride, base + f.holes[k] * s.row_stride,
                       (uint32_t)(item - k * per - o * tiles));
         }
     }
@@ -865,7 +868,9 @@ int iso_pages_fork(const int32_t* table, const int32_t* length, int64_t seqs, in
     if (children) {
         int64_t items = children;  // a child's table; a tile of an array's block of a copied page
         for (int i = 0; i < st.count; ++i) items += children * st.b[i].outer * ((st.b[i].inner * st.b[i].mid >> 15) + 1);
-        hipLaunchKernelGGL(k_fork_write, dim3((unsigned)(items < kCopyGrid ? items : kCopyGrid)), dim3(kNT), 0, hs, f, st);
+        const dim3 grid((unsigned)(items < kCopyGrid ? items : kCopyGrid));
+        if (streamed(st, pages)) hipLaunchKernelGGL(k_fork_write<true>, grid, dim3(kNT), 0, hs, f, st);
+        else hipLaunchKernelGGL(k_fork_write<false>, grid, dim3(kNT), 0, hs, f, st);
     }
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
@@ -907,7 +912,9 @@ int iso_pages_compact(const int32_t* table, int64_t entries, const int32_t* refs
     }
     int64_t items = (entries + kNT - 1) / kNT + (pages + kNT - 1) / kNT;
     for (int i = 0; i < st.count; ++i) items += pages / 2 * st.b[i].outer * ((st.b[i].inner * st.b[i].mid >> 15) + 1);
-    hipLaunchKernelGGL(k_compact_write, dim3((unsigned)(items < 1 ? 1 : items < kCopyGrid ? items : kCopyGrid)), dim3(kNT), 0, hs, f, st);
+    const dim3 grid((unsigned)(items < 1 ? 1 : items < kCopyGrid ? items : kCopyGrid));
+    if (streamed(st, pages)) hipLaunchKernelGGL(k_compact_write<true>, grid, dim3(kNT), 0, hs, f, st);
+    else hipLaunchKernelGGL(k_compact_write<false>, grid, dim3(kNT), 0, hs, f, st);
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 

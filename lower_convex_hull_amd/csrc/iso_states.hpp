@@ -81,9 +81,32 @@ typedef uint64_t Wide8 __attribute__((aligned(1), may_alias));
 typedef uint32_t Wide4 __attribute__((aligned(1), may_alias));
 typedef uint16_t Wide2 __attribute__((aligned(1), may_alias));
 
+// STREAM: without a place in the caches, for arrays that do not fit them anyway:
+// past half of the last-level cache (reordering 2.3 GB 471 -> 438 us, half of a pool of
+// 2.3 GB moved together 320 -> 302; 40 MB reordered again and again 9.8 -> 11.3).
+constexpr int64_t kStreamed = 128 << 20;
+template <bool STREAM>
+__device__ __forceinline__ Quad load_quad(const char* at) {
+    const Wide16* p = reinterpret_cast<const Wide16*>(at);
+    if constexpr (STREAM) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+template <bool STREAM>
+__device__ __forceinline__ void store_quad(char* at, const Quad& v) {
+    Wide16* p = reinterpret_cast<Wide16*>(at);
+    if constexpr (STREAM) __builtin_nontemporal_store((Wide16)v, p);
+    else *p = v;
+}
+// Whether the arrays' rows, of which there are `rows`, come to more than that.
+inline bool streamed(const States& st, int64_t rows) {
+    double bytes = 0.0;
+    for (int i = 0; i < st.count; ++i) bytes += (double)rows * st.b[i].outer * st.b[i].mid * st.b[i].inner;
+    return bytes > kStreamed;
+}
+
 // The first `left` of 16 bytes, fewer than 16 as 8, 4, 2 and 1 of them.
 __device__ __forceinline__ Quad load_bytes(const char* at, int left) {
-    if (left >= 16) return *reinterpret_cast<const Wide16*>(at);
+    if (left >= 16) return load_quad<false>(at);
     Quad v = {0, 0, 0, 0};
     if (left & 8) {
         const uint64_t x = *reinterpret_cast<const Wide8*>(at);
@@ -97,7 +120,7 @@ __device__ __forceinline__ Quad load_bytes(const char* at, int left) {
 }
 __device__ __forceinline__ void store_bytes(char* at, int left, const Quad& v) {
     if (left >= 16) {
-        *reinterpret_cast<Wide16*>(at) = v;
+        store_quad<false>(at, v);
         return;
     }
     if (left & 8) *reinterpret_cast<Wide8*>(at) = (uint64_t)v.y << 32 | v.x;
