@@ -300,7 +300,7 @@ struct SelectOut {
 // Bound by the latency of its steps; a few of the threads' keys stay in registers.
 // Keys lie by place in their lists, then by list, so that the best of all are
 // spread over the threads.
-constexpr int kJoinNT = 1024, kJoinKeep = 4;
+constexpr int kJoinNT = 1024, kJoinKeep = 2;
 __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, Scale sc, int splits,
                                                        const uint64_t* __restrict__ keys,
                                                        const PieceSum* __restrict__ sums, SelectOut o) {
@@ -352,13 +352,12 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
         // candidate e with its key; hi is 0 where there is none
         auto cand = [&](uint32_t e, uint64_t x) {
             const uint32_t list = e - by_lists(e) * lists, k = by_splits(list);
-            const RowSum& a = row[k];
-            const bool none = a.state == 1 ? !x : a.state == 0 || e != k * (uint32_t)splits;
-            if (none) return Cand{0, 0};
-            if (a.state == 2) x = 0;
+            const RowSum a = row[k];
+            // no branches: a row's values come from LDS at once
+            const bool token = a.state == 1;
             const float rank = (float)((a.score + a.logp(x, sc.inv_t)) * a.weight);
-            if (!(rank > -INFINITY)) return Cand{0, 0};
-            return Cand{((uint64_t)ordered(rank) << 32) | (uint32_t)(kMaxBeams - k), x};
+            const bool some = (token ? x != 0 : a.state == 2 && e == k * (uint32_t)splits) && rank > -INFINITY;
+            return Cand{some ? ((uint64_t)ordered(rank) << 32) | (uint32_t)(kMaxBeams - k) : 0, some && token ? x : 0};
         };
         auto each = [&](auto f) {
 #pragma unroll
