@@ -549,6 +549,13 @@ def _done(st):
         raise IsoError(st)
 
 
+def _int32(x, name):
+    """x, where 32 bits hold it (ctypes would keep the low ones of any other)."""
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{name} must be a 32-bit number")
+    return x
+
+
 def token_logp(logits, target, *, temperature: float = 1.0, entropy: bool = False, stream=None):
     """Log-probabilities of the targets under softmax(logits / temperature), row
     by row: (logp, lse), or (logp, lse, entropies) when entropy.  logits: 2-D
@@ -698,7 +705,7 @@ def beam_select(logits, score, *, take=None, weight=None, ended=None, end_token:
     parent, token = c.new(t.int32, batch, take), c.new(t.int32, batch, take)
     nb = c.lib.iso_beam_select_workspace_bytes(batch, beams, vocab, take, code)
     ws, wptr = c.workspace(nb)
-    _done(c.lib.iso_beam_select(ptr, code, batch, beams, vocab, ld, sc, wt, en, end_token, temperature, take,
+    _done(c.lib.iso_beam_select(ptr, code, batch, beams, vocab, ld, sc, wt, en, _int32(end_token, "end_token"), temperature, take,
                                 out.data_ptr(), logp.data_ptr(), parent.data_ptr(), token.data_ptr(), wptr, nb,
                                 c.handle))
     return out, logp, parent, token
@@ -798,7 +805,7 @@ def pages_fork(table, length, refs, parent, *, page_size: int, grow=1, pools=(),
     tb, ln = c.use(table, "table", table.shape, i32), c.use(length, "length", (seqs,), i32)
     rf, pr = c.use(refs, "refs", refs.shape, i32), c.use(parent, "parent", parent.shape, i32)
     pages, children = refs.shape[0], parent.shape[0]
-    each, gr = (grow, None) if isinstance(grow, int) else (0, c.use(grow, "grow", parent.shape, i32))
+    each, gr = (_int32(grow, "grow"), None) if isinstance(grow, int) else (0, c.use(grow, "grow", parent.shape, i32))
     blocks, count = _blocks(c, pools, page_dim, pages, token_dim)
     for p in ((pools,) if hasattr(pools, "data_ptr") else pools):
         if p.shape[token_dim] != page_size:

@@ -217,3 +217,10 @@ def test_tensors_as_blocks():
     for tensors, dims, rows in ((full, 5, 5), (full, -1, 5), ([full] * 17, 0, 2), ([full, base], (0, 0, 0), 2), (full, 1, 5)):
         with pytest.raises(ValueError):
             iso._blocks(_Fake(), tensors, dims, rows)
+
+
+def test_numbers_past_32_bits_are_refused():
+    assert iso._int32(-1 << 31, "x") == -1 << 31 and iso._int32((1 << 31) - 1, "x") == (1 << 31) - 1
+    for x in (1 << 31, (-1 << 31) - 1):
+        with pytest.raises(ValueError):
+            iso._int32(x, "x")
