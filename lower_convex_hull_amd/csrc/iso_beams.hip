@@ -47,11 +47,13 @@ struct Beams {
     const uint8_t* ended;  // or NULL
     int beams, take;
     int32_t end_token;
-    __device__ __forceinline__ bool counts(int64_t r) const {
-        const float w = weight ? weight[r] : 1.0f;
-        return fabsf(score[r]) < INFINITY && w > 0.0f && w < INFINITY;
+    // Row r: 0 no candidates, 1 its tokens, 2 itself.  The three are read at once.
+    __device__ __forceinline__ int state(int64_t r) const {
+        const float s = score[r], w = weight ? weight[r] : 1.0f;
+        const uint8_t e = ended ? ended[r] : (uint8_t)0;
+        const bool counts = (fabsf(s) < INFINITY) & (w > 0.0f) & (w < INFINITY);
+        return counts ? e ? 2 : 1 : 0;
     }
-    __device__ __forceinline__ bool has_ended(int64_t r) const { return ended && ended[r]; }
 };
 
 // A value t >= 1 that at least n of a wave's values (V a lane) reach, and few
@@ -157,7 +159,7 @@ __global__ __launch_bounds__(NT, 5) void k_beam_pieces(const T* __restrict__ log
     __shared__ int vectors, count;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     for (uint32_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        if (!b.counts(r) || b.has_ended(r)) continue;
+        if (b.state(r) != 1) continue;
         for (uint32_t split = blockIdx.y; split < splits; split += gridDim.y) {
             const T* x = logits + r * ld;
             const Piece<T> w(x, (int)split, Chunk<T, NT, U>::kSize, vocab);
@@ -326,9 +328,9 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
             const PieceSum none{-INFINITY, 0.0};
             // read whether the row counts or not (what is there is not used then): one latency for all
             const PieceSum head = lane < splits ? sums[r * splits + lane] : none;
-            const bool ended = b.has_ended(r), counts = b.counts(r);
-            RowSum a{0.0, 0.0, (double)b.score[r], b.weight ? (double)b.weight[r] : 1.0, counts && ended ? 2 : 0};
-            if (counts && !ended) {
+            const int state = b.state(r);
+            RowSum a{0.0, 0.0, (double)b.score[r], b.weight ? (double)b.weight[r] : 1.0, state == 2 ? 2 : 0};
+            if (state == 1) {
                 double m = head.m;
                 for (int p = lane + 64; p < splits; p += 64) m = fmax(m, sums[r * splits + p].m);
 #pragma unroll
