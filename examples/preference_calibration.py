@@ -1,5 +1,5 @@
 """Trains a small next-token model on paired answers, takes a policy step from its
-logits, and calibrates its reward margins.
+logits, calibrates its reward margins, and writes its best answers by beam search.
 
 The model is a table of logits by the token before (a bigram model), so that its
 gradient is the loss operators' own, summed by row.  One pass of training is
@@ -9,7 +9,8 @@ gradient is the loss operators' own, summed by row.  One pass of training is
 one policy step is policy_loss_logits in the logits' place, and the margins
 reward(chosen) - reward(rejected) of pairs with noisy labels become the
 probability that the first answer is preferred, a non-decreasing curve
-(calib_curve).
+(calib_curve).  The trained model's likeliest answers to a few first tokens come
+from beam_select, with the beams' tokens brought into order by beam_reorder.
 
     python examples/preference_calibration.py
 """
@@ -59,6 +60,20 @@ def margins(iso, model, ref, data):
     return (reward[0::2] - reward[1::2]).double()
 
 
+def best_answers(torch, iso, model, first, beams, length):
+    """The `beams` likeliest answers found for each first token, best first: (tokens, log-probabilities)."""
+    batch = first.numel()
+    token = first.repeat_interleave(beams)
+    history = torch.zeros(batch * beams, length, dtype=torch.int32, device="cuda")
+    score = torch.full((batch, beams), -torch.inf, device="cuda")
+    score[:, 0] = 0.0  # beams are alike at first
+    for t in range(length):
+        score, _, parent, token = iso.beam_select(model[token.view(-1).long()], score)
+        iso.beam_reorder(history, parent)
+        history[:, t] = token.view(-1)
+    return history.view(batch, beams, length), score
+
+
 def main(steps=40, pairs=2000, rate=10.0, seed=0, out=print):
     import torch
 
@@ -103,8 +118,12 @@ def main(steps=40, pairs=2000, rate=10.0, seed=0, out=print):
     brier = [float(((p - fresh[3].double()) ** 2).mean()) for p in (raw, fitted)]
     right = float(((margin > 0) == fresh[3]).double().mean())
     out(f"{right:.3f} of fresh pairs ordered; squared error of the probability {brier[0]:.4f} raw, {brier[1]:.4f} calibrated")
+
+    first = torch.arange(3, device="cuda")
+    tokens, score = best_answers(torch, iso, stepped, first, 4, 12)
+    out(f"best answer to 0: {tokens[0, 0].tolist()}, log-probability {float(score[0, 0]):.3f}")
     return {"trained": trained, "policy": (float(loss[0]), float(after[0])), "right": right, "brier": brier,
-            "curve": (xp, fp)}
+            "curve": (xp, fp), "model": stepped, "answers": (first, tokens, score)}
 
 
 if __name__ == "__main__":

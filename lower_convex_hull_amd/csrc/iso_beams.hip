@@ -41,6 +41,10 @@ struct PieceSum {
     double m, s;
 };
 
+// Keys of a batch item: place i of list l at i * stride + l.  The stride is odd, so
+// that however few lists have keys, these are spread over all threads of the join.
+__host__ __device__ __forceinline__ uint32_t key_stride(uint32_t lists) { return lists | 1u; }
+
 struct Beams {
     const float* score;
     const float* weight;   // or NULL
@@ -136,6 +140,9 @@ struct PieceTerms {
     }
 };
 
+// Bound by instruction issue and HBM together: 512 rows x 131072 bf16 (134 MB, read once)
+// in 35 us, 3.8 TB/s, 69 % of the SIMDs' issue cycles VALU; f32 at 128 x 8 x 200000 is read
+// at 5.5 TB/s.  Few rows by the latency of one piece (6 us).
 // A workgroup takes a piece of a row, held in its registers: the piece's maximum
 // and sum, and its `take` best tokens.  A value that `take` threads' maxima reach
 // bounds the take-th best token from below.  The few vectors that reach it go
@@ -205,7 +212,7 @@ __global__ __launch_bounds__(NT, 5) void k_beam_pieces(const T* __restrict__ log
             s += far * terms.rest;
             c.forget();
             s = wg_sum<NT>(s, red_sum);
-            const uint32_t lists = (uint32_t)b.beams * splits, item = r / (uint32_t)b.beams;
+            const uint32_t stride = key_stride((uint32_t)b.beams * splits), item = r / (uint32_t)b.beams;
             const uint32_t list = (r - item * (uint32_t)b.beams) * splits + split;
             if (threadIdx.x == 0) sums[(int64_t)r * splits + split] = PieceSum{(double)m, s};
             // every number reaches the lowest one
@@ -246,17 +253,16 @@ __global__ __launch_bounds__(NT, 5) void k_beam_pieces(const T* __restrict__ log
             }
             __syncthreads();
             const int found = held <= kVectors ? count : kPlaces + 1;
-            // place i of list l of a batch item at i * lists + l
-            uint64_t* out = keys + (int64_t)item * lists * b.take + list;
+            uint64_t* out = keys + (int64_t)item * stride * b.take + list;
             if (found <= kPlaces) {
                 if (threadIdx.x < 8) room[found + threadIdx.x] = 0;
                 __syncthreads();
                 for (int i = threadIdx.x; i < found; i += NT) {
                     const uint64_t k = room[i];
                     const int rank = rank_of(room, found, [&](uint64_t o) { return o > k; });
-                    if (rank < b.take) out[(int64_t)rank * lists] = k;
+                    if (rank < b.take) out[(int64_t)rank * stride] = k;
                 }
-                for (int i = found + threadIdx.x; i < b.take; i += NT) out[(int64_t)i * lists] = 0;
+                for (int i = found + threadIdx.x; i < b.take; i += NT) out[(int64_t)i * stride] = 0;
             } else {
                 uint64_t last = ~0ull;
                 for (int i = 0; i < b.take; ++i) {
@@ -273,7 +279,7 @@ __global__ __launch_bounds__(NT, 5) void k_beam_pieces(const T* __restrict__ log
                     __syncthreads();
 #pragma unroll
                     for (int k = 0; k < kWaves; ++k) best = room[k] > best ? room[k] : best;
-                    if (threadIdx.x == 0) out[(int64_t)i * lists] = best;
+                    if (threadIdx.x == 0) out[(int64_t)i * stride] = best;
                     last = best;  // 0: nothing is below it
                 }
             }
@@ -299,7 +305,10 @@ struct SelectOut {
     float *score, *logp;
     int32_t *parent, *token;
 };
-// Bound by the latency of its steps; a few of the threads' keys stay in registers.
+// Bound by the latency of its steps, one workgroup an item: 7 to 8 us at 8 beams of 8
+// pieces and 16 keys each, 24 us at 32 beams of 7 pieces and 64 keys (14336 f64 ranks,
+// twice).  With 512 threads the latter took 10 us longer, with 4, 8 or 16 of a thread's
+// keys or ranks in registers small calls took 0.5 to 5 us longer.
 // Keys lie by place in their lists, then by list, so that the best of all are
 // spread over the threads.
 constexpr int kJoinNT = 1024, kJoinKeep = 2;
@@ -313,8 +322,8 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
     __shared__ uint32_t bound;
     __shared__ int count;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t lists = (uint32_t)b.beams * (uint32_t)splits, all = lists * (uint32_t)b.take;
-    const Divide by_lists(lists), by_splits((uint32_t)splits);
+    const uint32_t lists = (uint32_t)b.beams * (uint32_t)splits, stride = key_stride(lists), all = stride * (uint32_t)b.take;
+    const Divide by_stride(stride), by_splits((uint32_t)splits);
     for (int64_t item = blockIdx.x; item < batch; item += gridDim.x) {
         const uint64_t* key = keys + item * all;
         uint64_t kept[kJoinKeep];
@@ -353,12 +362,12 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
         __syncthreads();
         // candidate e with its key; hi is 0 where there is none
         auto cand = [&](uint32_t e, uint64_t x) {
-            const uint32_t list = e - by_lists(e) * lists, k = by_splits(list);
+            const uint32_t place = e - by_stride(e) * stride, list = min(place, lists - 1), k = by_splits(list);
             const RowSum a = row[k];
             // no branches: a row's values come from LDS at once
             const bool token = a.state == 1;
             const float rank = (float)((a.score + a.logp(x, sc.inv_t)) * a.weight);
-            const bool some = (token ? x != 0 : a.state == 2 && e == k * (uint32_t)splits) && rank > -INFINITY;
+            const bool some = place < lists && (token ? x != 0 : a.state == 2 && e == k * (uint32_t)splits) && rank > -INFINITY;
             return Cand{some ? ((uint64_t)ordered(rank) << 32) | (uint32_t)(kMaxBeams - k) : 0, some && token ? x : 0};
         };
         auto each = [&](auto f) {
@@ -467,7 +476,8 @@ SelectPlan select_plan(int64_t batch, int64_t beams, int64_t vocab, int64_t take
     const int64_t chunk = (int64_t)p.threads * p.vectors * 16 / size;
     p.splits = (int)((vocab + chunk - 1) / chunk);
     const size_t items = (size_t)rows * (size_t)p.splits;
-    p.off_sums = align_up(items * (size_t)take * sizeof(uint64_t));
+    const size_t stride = key_stride((uint32_t)(beams * p.splits));
+    p.off_sums = align_up((size_t)batch * stride * (size_t)take * sizeof(uint64_t));
     p.bytes = p.off_sums + align_up(items * sizeof(PieceSum));
     return p;
 }
@@ -477,6 +487,9 @@ bool select_sizes_ok(int64_t batch, int64_t beams, int64_t vocab, int64_t take, 
            vocab <= (1LL << 30) && batch <= 0x7fffffffLL / beams && dtype >= ISO_DT_F32 && dtype <= ISO_DT_BF16;  // an item's keys: 2^31 at most
 }
 
+// Bound by HBM: what moved rows come from read, they written, 2344 MB in 421 to 448 us,
+// 5.2 to 5.6 TB/s (a copy reaches 4.7 to 5.1).  Rows held in arrays of registers instead
+// spilled from 8 rows on (835 us with scratch).
 // A workgroup takes 2^`shift` columns of 16 bytes through all rows of a batch
 // item: it reads what the moved rows come from, waits until all of it has come,
 // and only then writes.  No other workgroup reads or writes there, so rows may

@@ -122,6 +122,8 @@ __device__ __forceinline__ Child child_of(const Fork& f, int64_t i) {
     return c;
 }
 
+// All but the copies is bound by launches and latency: a step of 1024 sequences over 84000
+// pages moves 1.2 MB, its four kernels take 3.5, 6.5, 10.4 and 4.2 us.
 // A step of any size takes six launches: the counts copied and the free pages
 // counted by block; each sequence's children counted, and who goes on to write
 // which page; the counts of the pages of sequences with other than one child;
@@ -427,7 +429,9 @@ __global__ __launch_bounds__(kOneNT) void k_fork_few(Fork f, Blocks pb) {
     }
 }
 
-// A step in one workgroup but for what k_fork_write does: the counts are in LDS.
+// A step in one workgroup but for what k_fork_write does: the counts are in LDS.  Bound by
+// the latency of its steps: 7.7 us for four sequences, 14.6 for 256 over 12280 pages (as
+// four launches 20 and more; with each child's page compared with every other's 27).
 // Up to kOnePages pages, kOneNT children and sequences, kOneEntries entries of
 // tables (their counting is this workgroup's).
 constexpr int kOnePages = 12288;
@@ -506,7 +510,9 @@ __global__ __launch_bounds__(kOneNT) void k_fork_one(Fork f) {
 }
 
 // 16-byte columns of what one block of an array holds, `bytes` of each of its mid
-// runs, by the workgroup: kCopyU of them a thread are on their way at a time.
+// runs, by the workgroup: kCopyU of them a thread are on their way at a time (half of a
+// 2.3 GB pool, 1562 MB moved: 298 us, 5.2 TB/s; with 4 on their way 389 us, with a quarter
+// of the workgroups 395, byte by byte 822).
 constexpr int kCopyU = 8;
 struct CopyTile {
     uint32_t cols, all;  // columns of a run, of all of them

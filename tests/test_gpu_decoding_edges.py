@@ -84,6 +84,20 @@ def test_select_of_few_different_logits(torch, name, vocab, take):
         assert n(one[3])[0, :len(want)].tolist() == want.tolist()
 
 
+@pytest.mark.parametrize("beams,take,live", [(128, 128, 1), (64, 64, 2), (128, 128, 128), (32, 64, 1), (7, 128, 1)])
+def test_select_of_few_live_beams(torch, beams, take, live):
+    """A first step of many beams: the keys of few lists."""
+    vocab = 70001
+    say(f"[decoding] {live} of {beams} beams live, take {take}")
+    gen = torch.Generator().manual_seed(beams)
+    x = torch.randn(live, vocab, generator=gen).repeat(beams // live, 1)
+    x = torch.cat([x, x[:beams - len(x)]]).bfloat16()
+    score = torch.full((1, beams), -float("inf"))
+    score[0, beams - live:] = -torch.rand(live, generator=gen)
+    got = iso.beam_select(place(torch, x, torch.bfloat16, 1, 0), score.cuda(), take=take)
+    check_select(got, x.double().numpy(), score, take)
+
+
 def test_select_of_extreme_logits(torch):
     """The largest finite values, subnormals, and temperatures at their ends."""
     f32 = torch.finfo(torch.float32)
