@@ -142,7 +142,7 @@ struct PieceTerms {
 
 // Bound by instruction issue and HBM together: 512 rows x 131072 bf16 (134 MB, read once)
 // in 35 us, 3.8 TB/s, 69 % of the SIMDs' issue cycles VALU; f32 at 128 x 8 x 200000 is read
-// at 5.5 TB/s.  Few rows by the latency of one piece (6 us).
+// at 6.0 TB/s.  Few rows by the latency of one piece (6 us).
 // A workgroup takes a piece of a row, held in its registers: the piece's maximum
 // and sum, and its `take` best tokens.  A value that `take` threads' maxima reach
 // bounds the take-th best token from below.  The few vectors that reach it go
@@ -150,7 +150,7 @@ struct PieceTerms {
 // reach it are brought into order by counting.  A row with a NaN has no
 // candidates (its sum is NaN), whatever is found in it.
 template <typename T, int NT, int U, bool STREAM>
-__global__ __launch_bounds__(NT, 5) void k_beam_pieces(const T* __restrict__ logits, uint32_t rows, int vocab, int64_t ld,
+__global__ __launch_bounds__(NT, U >= 16 ? 4 : 5) void k_beam_pieces(const T* __restrict__ logits, uint32_t rows, int vocab, int64_t ld,
                                                     Beams b, Scale sc, uint32_t splits, uint64_t* __restrict__ keys,
                                                     PieceSum* __restrict__ sums) {
     typedef typename Wide<T>::A Vec;
@@ -459,11 +459,14 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
 // 256 threads), but where `take` is not well below a wave's lanes: their maxima would
 // bound little.  Counted by the bytes of a row, not by its type's elements.
 // Logits past half of the last-level cache are streamed (128 x 8 x 200000 f32: 149 us,
-// 172 through the caches; bf16 94 and 102).
+// 172 through the caches; bf16 94 and 102), then by 128 threads of 16 vectors, half the
+// waves for the same piece (f32 137, bf16 86; on chip they fill the GPU less evenly: 64 x 8
+// x 32000 bf16 21.7 us, 20.1 with 256 x 8).
 constexpr int64_t kWaveRow = 8 << 10, kManyPieces = 360;
 constexpr int kWaveTake = 32;
 struct SelectPlan {
-    int threads, vectors;  // of a piece: 256 x 8, 256 x 4, 64 x 4
+    int threads, vectors;  // of a piece: 128 x 16, 256 x 8, 256 x 4, 64 x 4
+    bool stream;
     int splits;
     size_t off_sums, bytes;
 };
@@ -473,6 +476,11 @@ SelectPlan select_plan(int64_t batch, int64_t beams, int64_t vocab, int64_t take
     const bool wave = row <= kWaveRow && take <= kWaveTake;
     p.threads = wave ? 64 : 256;
     p.vectors = !wave && rows * ((row + (32 << 10) - 1) / (32 << 10)) > kManyPieces ? 8 : 4;
+    p.stream = p.vectors == 8 && rows * row > kStreamed;
+    if (p.stream && take <= kWaveTake) {
+        p.threads = 128;
+        p.vectors = 16;
+    }
     const int64_t chunk = (int64_t)p.threads * p.vectors * 16 / size;
     p.splits = (int)((vocab + chunk - 1) / chunk);
     const size_t items = (size_t)rows * (size_t)p.splits;
@@ -613,9 +621,12 @@ int iso_beam_select(const void* logits, int dtype, int64_t batch, int64_t beams,
         typedef std::integral_constant<int, 64> Wave;
         typedef std::integral_constant<int, 4> Four;
         typedef std::integral_constant<int, 8> Eight;
-        if (pl.threads == 64) start(Wave{}, Four{}, std::false_type{});
+        typedef std::integral_constant<int, 16> Sixteen;
+        typedef std::integral_constant<int, 128> Half;
+        if (pl.vectors == 16) start(Half{}, Sixteen{}, std::true_type{});
+        else if (pl.threads == 64) start(Wave{}, Four{}, std::false_type{});
         else if (pl.vectors == 4) start(Wg{}, Four{}, std::false_type{});
-        else if (streamed<T>(rows, vocab)) start(Wg{}, Eight{}, std::true_type{});
+        else if (pl.stream) start(Wg{}, Eight{}, std::true_type{});
         else start(Wg{}, Eight{}, std::false_type{});
     });
     hipLaunchKernelGGL(k_beam_join, dim3((unsigned)(batch < kMaxGrid ? batch : kMaxGrid)), dim3(kJoinNT), 0, st, batch, b,

@@ -48,11 +48,12 @@ def test_select_at_the_borders_of_its_pieces(torch, name, take):
                     check_select(pick, x[b * beams:(b + 1) * beams].double().numpy(), score[b:b + 1], take)
 
 
+@pytest.mark.parametrize("take", [18, 33])
 @pytest.mark.parametrize("name", ["f32", "f16", "bf16"])
-def test_select_of_many_streamed_rows(torch, name):
+def test_select_of_many_streamed_rows(torch, name, take):
     """Logits past half of the last-level cache."""
     dtype = dtype_of(torch, name)
-    batch, beams, vocab, take = 70, 9, 60001 if name == "f32" else 120001, 18
+    batch, beams, vocab = 70, 9, 60001 if name == "f32" else 120001
     say(f"[decoding] streamed {name}")
     gen = torch.Generator(device="cuda").manual_seed(5)
     x = (torch.randn(batch * beams, vocab, generator=gen, device="cuda") * 2).to(dtype)
