@@ -455,8 +455,10 @@ int iso_policy_loss_logits(const void* logits, int dtype, int64_t rows, int64_t 
  *            [batch*take] int32.  Places past an item's last candidate hold
  *            -infinity, -infinity, -1 and -1.
  * A row with a NaN or +infinity, or of -infinity alone, has no candidates, nor
- * has what ranks at -infinity (below f32).  Sums are as in iso_token_logp, the
- * score and the rank f64 until they are rounded.
+ * has what ranks at -infinity (below f32).  Terms of sums are f32, the sums f64,
+ * but that up to eight terms below half of the largest are added in f32 first;
+ * the score and the rank are f64 until they are rounded.  How a row's terms are
+ * grouped goes by its address modulo 16.
  *
  * Arrays of states.  An iso_blocks describes, for rows (beams) or pages, the
  * blocks row r holds: `inner` bytes each, block (o, m) at

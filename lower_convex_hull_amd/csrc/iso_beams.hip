@@ -490,9 +490,10 @@ SelectPlan select_plan(int64_t batch, int64_t beams, int64_t vocab, int64_t take
     return p;
 }
 
+// (An item's keys are 2^31 at most, and one place of padding.)
 bool select_sizes_ok(int64_t batch, int64_t beams, int64_t vocab, int64_t take, int dtype) {
     return batch >= 0 && beams >= 1 && beams <= kMaxBeams && take >= 1 && take <= kMaxTake && vocab >= 1 &&
-           vocab <= (1LL << 30) && batch <= 0x7fffffffLL / beams && dtype >= ISO_DT_F32 && dtype <= ISO_DT_BF16;  // an item's keys: 2^31 at most
+           vocab <= (1LL << 30) && batch <= 0x7fffffffLL / beams && dtype >= ISO_DT_F32 && dtype <= ISO_DT_BF16;
 }
 
 // Bound by HBM: what moved rows come from read, they written, 2344 MB in 421 to 448 us,
