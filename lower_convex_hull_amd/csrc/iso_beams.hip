@@ -41,9 +41,16 @@ struct PieceSum {
     double m, s;
 };
 
-// Keys of a batch item: place i of list l at i * stride + l.  The stride is odd, so
-// that however few lists have keys, these are spread over all threads of the join.
+// Keys of a batch item: place i of list l at i * stride + (l + i * turn) mod stride.
+// The best keys are the first ones of a few lists; a stride that is odd and a turn
+// of 5/8 of it spread them over the threads of the join, whose maxima bound little
+// where few threads hold them all (without the turn 128 x 32000 bf16, 128 of them,
+// went through the rounds of a maximum: 4377 us).
 __host__ __device__ __forceinline__ uint32_t key_stride(uint32_t lists) { return lists | 1u; }
+__device__ __forceinline__ uint32_t key_turn(uint32_t stride) { return stride * 5u / 8u; }  // strides are below 2^25
+__device__ __forceinline__ int64_t key_at(uint32_t i, uint32_t list, uint32_t stride) {
+    return (int64_t)i * stride + (list + i * key_turn(stride)) % stride;
+}
 
 struct Beams {
     const float* score;
@@ -253,16 +260,16 @@ __global__ __launch_bounds__(NT, U >= 16 ? 4 : 5) void k_beam_pieces(const T* __
             }
             __syncthreads();
             const int found = held <= kVectors ? count : kPlaces + 1;
-            uint64_t* out = keys + (int64_t)item * stride * b.take + list;
+            uint64_t* out = keys + (int64_t)item * stride * b.take;
             if (found <= kPlaces) {
                 if (threadIdx.x < 8) room[found + threadIdx.x] = 0;
                 __syncthreads();
                 for (int i = threadIdx.x; i < found; i += NT) {
                     const uint64_t k = room[i];
                     const int rank = rank_of(room, found, [&](uint64_t o) { return o > k; });
-                    if (rank < b.take) out[(int64_t)rank * stride] = k;
+                    if (rank < b.take) out[key_at(rank, list, stride)] = k;
                 }
-                for (int i = found + threadIdx.x; i < b.take; i += NT) out[(int64_t)i * stride] = 0;
+                for (int i = found + threadIdx.x; i < b.take; i += NT) out[key_at(i, list, stride)] = 0;
             } else {
                 uint64_t last = ~0ull;
                 for (int i = 0; i < b.take; ++i) {
@@ -279,12 +286,92 @@ __global__ __launch_bounds__(NT, U >= 16 ? 4 : 5) void k_beam_pieces(const T* __
                     __syncthreads();
 #pragma unroll
                     for (int k = 0; k < kWaves; ++k) best = room[k] > best ? room[k] : best;
-                    if (threadIdx.x == 0) out[(int64_t)i * stride] = best;
+                    if (threadIdx.x == 0) out[key_at(i, list, stride)] = best;
                     last = best;  // 0: nothing is below it
                 }
             }
             __syncthreads();  // the shared arrays are used again
         }
+    }
+}
+
+// A row's lists of keys into one, of its `take` best tokens, found as in a piece.
+// Bound by latency: 6 us for 224 rows of 7 lists of 64.
+constexpr int kMergeNT = 256;
+__global__ __launch_bounds__(kMergeNT) void k_beam_merge(uint32_t rows, Beams b, uint32_t splits,
+                                                         const uint64_t* __restrict__ keys, uint64_t* __restrict__ merged) {
+    constexpr int kWaves = kMergeNT / 64;
+    __shared__ uint64_t room[kRoom + 8];
+    __shared__ uint32_t most[kMergeNT];
+    __shared__ uint32_t bound;
+    __shared__ int count;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const uint32_t stride = key_stride((uint32_t)b.beams * splits), all = splits * (uint32_t)b.take;
+    const uint32_t row_stride = key_stride((uint32_t)b.beams);
+    const Divide by_splits(splits);
+    for (uint32_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        if (b.state(r) != 1) continue;
+        const uint32_t item = r / (uint32_t)b.beams, k = r - item * (uint32_t)b.beams;
+        const uint64_t* key = keys + (int64_t)item * stride * b.take;
+        uint64_t* out = merged + (int64_t)item * row_stride * b.take;
+        auto at = [&](uint32_t e) {
+            const uint32_t i = by_splits(e);
+            return key[key_at(i, k * splits + (e - i * splits), stride)];
+        };
+        uint32_t mine = 0;
+#pragma unroll 4
+        for (uint32_t e = threadIdx.x; e < all; e += kMergeNT) mine = max(mine, (uint32_t)(at(e) >> 32));
+        most[threadIdx.x] = mine;
+        if (threadIdx.x == 0) count = 0;
+        __syncthreads();
+        if (wave == 0) {
+            uint32_t v[kWaves];
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) v[i] = most[i * 64 + lane];
+            const uint32_t t = reached_by<0>(v, b.take);
+            if (lane == 0) bound = t;
+        }
+        __syncthreads();
+        if (mine >= bound) {
+#pragma unroll 4
+            for (uint32_t e = threadIdx.x; e < all; e += kMergeNT) {
+                const uint64_t x = at(e);
+                if ((uint32_t)(x >> 32) >= bound) {
+                    const int p = atomicAdd(&count, 1);
+                    if (p < kRoom) room[p] = x;
+                }
+            }
+        }
+        __syncthreads();
+        const int found = count;
+        if (found <= kRoom) {
+            if (threadIdx.x < 8) room[found + threadIdx.x] = 0;
+            __syncthreads();
+            for (int i = threadIdx.x; i < found; i += kMergeNT) {
+                const uint64_t x = room[i];
+                const int rank = rank_of(room, found, [&](uint64_t o) { return o > x; });
+                if (rank < b.take) out[key_at(rank, k, row_stride)] = x;
+            }
+            for (int i = found + threadIdx.x; i < b.take; i += kMergeNT) out[key_at(i, k, row_stride)] = 0;
+        } else {
+            uint64_t last = ~0ull;
+            for (int i = 0; i < b.take; ++i) {
+                uint64_t best = 0;
+                for (uint32_t e = threadIdx.x; e < all; e += kMergeNT) {
+                    const uint64_t x = at(e);
+                    best = x < last && x > best ? x : best;
+                }
+                best = wave_max(best);
+                __syncthreads();
+                if (lane == 0) room[wave] = best;
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kWaves; ++j) best = room[j] > best ? room[j] : best;
+                if (threadIdx.x == 0) out[key_at(i, k, row_stride)] = best;
+                last = best;
+            }
+        }
+        __syncthreads();  // the shared arrays are used again
     }
 }
 
@@ -305,25 +392,25 @@ struct SelectOut {
     float *score, *logp;
     int32_t *parent, *token;
 };
-// Bound by the latency of its steps, one workgroup an item: 7 to 8 us at 8 beams of 8
-// pieces and 16 keys each, 24 us at 32 beams of 7 pieces and 64 keys (14336 f64 ranks,
-// twice).  With 512 threads the latter took 10 us longer, with 4, 8 or 16 of a thread's
-// keys or ranks in registers small calls took 0.5 to 5 us longer.
-// Keys lie by place in their lists, then by list, so that the best of all are
-// spread over the threads.
+// Bound by the latency of its steps, one workgroup an item: 7 to 9 us at 8 beams of 8
+// pieces and 16 keys each, 13 us at 32 beams of 64.  With 512 threads, or more of a
+// thread's keys or ranks in registers, small calls took 0.5 to 5 us longer.
+// Keys lie by place in their lists, so that the best of all are spread over the threads.
 constexpr int kJoinNT = 1024, kJoinKeep = 2;
-__global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, Scale sc, int splits,
+__global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, Scale sc, int splits, int per,
                                                        const uint64_t* __restrict__ keys,
                                                        const PieceSum* __restrict__ sums, SelectOut o) {
     constexpr int kWaves = kJoinNT / 64, kGroups = kJoinNT / 4;
     __shared__ RowSum row[kMaxBeams];
     __shared__ Cand room[kRoom + 8];
-    __shared__ uint32_t most[kGroups];
+    __shared__ uint32_t most[kJoinNT];
     __shared__ uint32_t bound;
     __shared__ int count;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t lists = (uint32_t)b.beams * (uint32_t)splits, stride = key_stride(lists), all = stride * (uint32_t)b.take;
-    const Divide by_stride(stride), by_splits((uint32_t)splits);
+    // `per` lists of keys a beam: a list a piece, or one
+    const uint32_t lists = (uint32_t)b.beams * (uint32_t)per, stride = key_stride(lists), all = stride * (uint32_t)b.take;
+    const uint32_t turn = key_turn(stride);
+    const Divide by_stride(stride), by_per((uint32_t)per);
     for (int64_t item = blockIdx.x; item < batch; item += gridDim.x) {
         const uint64_t* key = keys + item * all;
         uint64_t kept[kJoinKeep];
@@ -362,12 +449,14 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
         __syncthreads();
         // candidate e with its key; hi is 0 where there is none
         auto cand = [&](uint32_t e, uint64_t x) {
-            const uint32_t place = e - by_stride(e) * stride, list = min(place, lists - 1), k = by_splits(list);
+            const uint32_t i = by_stride(e), turned = i * turn, off = turned - by_stride(turned) * stride;
+            const uint32_t place = e - i * stride + (e - i * stride < off ? stride : 0u) - off;
+            const uint32_t list = min(place, lists - 1), k = by_per(list);
             const RowSum a = row[k];
             // no branches: a row's values come from LDS at once
             const bool token = a.state == 1;
             const float rank = (float)((a.score + a.logp(x, sc.inv_t)) * a.weight);
-            const bool some = place < lists && (token ? x != 0 : a.state == 2 && e == k * (uint32_t)splits) && rank > -INFINITY;
+            const bool some = place < lists && (token ? x != 0 : a.state == 2 && e == k * (uint32_t)per) && rank > -INFINITY;
             return Cand{some ? ((uint64_t)ordered(rank) << 32) | (uint32_t)(kMaxBeams - k) : 0, some && token ? x : 0};
         };
         auto each = [&](auto f) {
@@ -391,14 +480,17 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
         };
         uint32_t mine = 0;
         each([&](const Cand& c) { mine = max(mine, (uint32_t)(c.hi >> 32)); });
-        uint32_t group = max(mine, (uint32_t)__shfl_xor((int)mine, 1));
-        group = max(group, (uint32_t)__shfl_xor((int)group, 2));
-        if ((threadIdx.x & 3) == 0) most[threadIdx.x >> 2] = group;
+        most[threadIdx.x] = mine;
         __syncthreads();
         if (wave == 0) {
+            // maxima of four threads each, that are not neighbours
             uint32_t v[kGroups / 64];
 #pragma unroll
-            for (int k = 0; k < kGroups / 64; ++k) v[k] = most[k * 64 + lane];
+            for (int k = 0; k < kGroups / 64; ++k) {
+                v[k] = most[k * 64 + lane];
+#pragma unroll
+                for (int j = 1; j < 4; ++j) v[k] = max(v[k], most[j * kGroups + k * 64 + lane]);
+            }
             const uint32_t t = reached_by<0>(v, b.take);
             if (lane == 0) bound = t;
         }
@@ -464,11 +556,16 @@ __global__ __launch_bounds__(kJoinNT) void k_beam_join(int64_t batch, Beams b, S
 // x 32000 bf16 21.7 us, 20.1 with 256 x 8).
 constexpr int64_t kWaveRow = 8 << 10, kManyPieces = 360;
 constexpr int kWaveTake = 32;
+// A row's lists are merged first where an item has many keys, which its join ranks in
+// f64 in one workgroup (1 x 16 x 200000 bf16, 64 of them, 13312 keys: 24.9 us, 40.7 by the
+// join alone; 40 x 16 x 50000, 2048 keys, 36.7 and 33.7; they meet at 4000 to 6000).
+constexpr size_t kMergedKeys = 6144;
 struct SelectPlan {
     int threads, vectors;  // of a piece: 128 x 16, 256 x 8, 256 x 4, 64 x 4
     bool stream;
     int splits;
-    size_t off_sums, bytes;
+    bool merge;
+    size_t off_merged, off_sums, bytes;
 };
 SelectPlan select_plan(int64_t batch, int64_t beams, int64_t vocab, int64_t take, int dtype) {
     const int64_t size = (int64_t)size_of(dtype), row = vocab * size, rows = batch * beams;
@@ -485,7 +582,9 @@ SelectPlan select_plan(int64_t batch, int64_t beams, int64_t vocab, int64_t take
     p.splits = (int)((vocab + chunk - 1) / chunk);
     const size_t items = (size_t)rows * (size_t)p.splits;
     const size_t stride = key_stride((uint32_t)(beams * p.splits));
-    p.off_sums = align_up((size_t)batch * stride * (size_t)take * sizeof(uint64_t));
+    p.off_merged = align_up((size_t)batch * stride * (size_t)take * sizeof(uint64_t));
+    p.merge = p.splits > 1 && stride * (size_t)take > kMergedKeys;
+    p.off_sums = p.off_merged + (p.merge ? align_up((size_t)batch * key_stride((uint32_t)beams) * (size_t)take * sizeof(uint64_t)) : 0);
     p.bytes = p.off_sums + align_up(items * sizeof(PieceSum));
     return p;
 }
@@ -630,8 +729,12 @@ int iso_beam_select(const void* logits, int dtype, int64_t batch, int64_t beams,
         else if (pl.stream) start(Wg{}, Eight{}, std::true_type{});
         else start(Wg{}, Eight{}, std::false_type{});
     });
+    uint64_t* merged = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + pl.off_merged);
+    if (pl.merge)
+        hipLaunchKernelGGL(k_beam_merge, dim3((unsigned)(rows < kMaxGrid ? rows : kMaxGrid)), dim3(kMergeNT), 0, st,
+                           (uint32_t)rows, b, (uint32_t)pl.splits, keys, merged);
     hipLaunchKernelGGL(k_beam_join, dim3((unsigned)(batch < kMaxGrid ? batch : kMaxGrid)), dim3(kJoinNT), 0, st, batch, b,
-                       sc, pl.splits, keys, sums, SelectOut{out_score, out_logp, out_parent, out_token});
+                       sc, pl.splits, pl.merge ? 1 : pl.splits, pl.merge ? merged : keys, sums, SelectOut{out_score, out_logp, out_parent, out_token});
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 

@@ -99,6 +99,27 @@ def test_select_of_few_live_beams(torch, beams, take, live):
     check_select(got, x.double().numpy(), score, take)
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("batch,beams,vocab,take", [(2, 32, 50003, 64), (1, 128, 16390, 128), (3, 5, 200001, 100), (1, 1, 400000, 128)])
+def test_select_of_many_keys(torch, name, batch, beams, vocab, take):
+    """Items with more keys than one workgroup ranks: each row's are merged first."""
+    say(f"[decoding] many keys {name} {batch}x{beams}x{vocab} take {take}")
+    dtype, gen = dtype_of(torch, name), torch.Generator().manual_seed(vocab)
+    x = (torch.randn(batch * beams, vocab, generator=gen) * 2).to(dtype)
+    x[torch.rand(batch * beams, vocab, generator=gen) < 0.3] = -float("inf")
+    score = -20 * torch.rand(batch, beams, generator=gen)
+    ended = torch.rand(batch, beams, generator=gen) < 0.2
+    weight = 0.3 + torch.rand(batch, beams, generator=gen)
+    got = iso.beam_select(place(torch, x, dtype, 1, 1), score.cuda(), take=take, weight=weight.cuda(), ended=ended.cuda(), end_token=7)
+    check_select(got, x.double().numpy(), score, take, weight, ended, 7)
+    # every value the same: the lowest tokens of the best beam
+    x.zero_()
+    score[:, 0] = 1.0
+    out = iso.beam_select(place(torch, x, dtype, 0, 1), score.cuda(), take=take)
+    assert n(out[3])[:, :take].tolist() == [list(range(take))] * batch
+    assert n(out[2]).tolist() == [[b * beams] * take for b in range(batch)]
+
+
 def test_select_of_extreme_logits(torch):
     """The largest finite values, subnormals, and temperatures at their ends."""
     f32 = torch.finfo(torch.float32)
