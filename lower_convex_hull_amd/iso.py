@@ -723,12 +723,25 @@ def _joined(shape, stride, begin, end):
     return n, step
 
 
+def _grad_mode():
+    import torch
+
+    return torch.is_grad_enabled()
+
+
+def _written(launch, tensors):
+    """Tells autograd that a call has written the tensors: a backward pass that saved one raises."""
+    launch.torch._C._increment_version((tensors,) if hasattr(tensors, "data_ptr") else tensors)
+
+
 def _block(launch, t, dim, token_dim):
     """The Blocks of a tensor whose rows (or pages) are dimension `dim`.  What lies
     behind a row is blocks of adjacent elements at one stride: from `token_dim` on,
-    or as long as they get."""
+    or as long as they get.  The call writes the tensor and records nothing for autograd."""
     if t.get_device() != launch.index:
         raise TypeError(f"every tensor must be on {launch.dev}")
+    if t.requires_grad and _grad_mode():
+        raise ValueError("a tensor that is written in place may not require grad (but under torch.no_grad)")
     shape, stride = t.shape, t.stride()
     at = dims = len(shape)
     if not 0 <= dim < dims:
@@ -776,7 +789,8 @@ def beam_reorder(states, parent, *, dim=0, stream=None):
     becomes what row parent[r] was.  states: a tensor or several, of any type,
     whose dimension `dim` (one for all, or one each) holds the rows; parent:
     (batch, beams) int32 as beam_select gives, rows of the same item (any other
-    value: the row stays).  Returns states."""
+    value: the row stays).  Returns states.  A state may not require grad (but
+    under torch.no_grad); a backward pass that saved one raises."""
     c = _Launch(parent, stream)
     if parent.dim() != 2:
         raise ValueError("parent must have the shape (batch, beams)")
@@ -784,6 +798,7 @@ def beam_reorder(states, parent, *, dim=0, stream=None):
     batch, beams = parent.shape
     blocks, count = _blocks(c, states, dim, batch * beams)
     _done(c.lib.iso_beam_reorder(blocks, count, pr, batch, beams, c.handle))
+    _written(c, states)
     return states
 
 
@@ -794,7 +809,7 @@ def pages_fork(table, length, refs, parent, *, page_size: int, grow=1, pools=(),
     more tokens (an int, or int32 shaped like parent); sequences without a child
     are freed.  table: (sequences, max_pages) int32; length, refs, parent: 1-D
     int32.  pools: the tensors of the pages' tokens, pages at dimension page_dim,
-    a page's tokens at token_dim.  status (int32): pages lacking, children too
+    a page's tokens at token_dim; as beam_reorder's states for autograd.  status (int32): pages lacking, children too
     long (nothing is done if either is not 0), pages copied, taken, left free."""
     c = _Launch(table, stream)
     t = c.torch
@@ -817,12 +832,13 @@ def pages_fork(table, length, refs, parent, *, page_size: int, grow=1, pools=(),
     _done(c.lib.iso_pages_fork(tb, ln, seqs, most, rf, pages, page_size, pr, gr, each, children, blocks, count,
                                new_table.data_ptr(), new_length.data_ptr(), new_refs.data_ptr(), status.data_ptr(),
                                wptr, nb, c.handle))
+    _written(c, pools)
     return new_table, new_length, new_refs, status
 
 
 def pages_compact(table, refs, *, pools=(), page_dim: int = 0, stream=None):
     """The live pages (refs > 0) of a paged cache moved together, in place in
-    the pools: (table, refs, moved, status), the cache after it; moved: where
+    the pools (as pages_fork's): (table, refs, moved, status), the cache after it; moved: where
     each page is now (-1: free); status (int32): live pages, pages moved."""
     c = _Launch(table, stream)
     t = c.torch
@@ -837,4 +853,5 @@ def pages_compact(table, refs, *, pools=(), page_dim: int = 0, stream=None):
     ws, wptr = c.workspace(nb)
     _done(c.lib.iso_pages_compact(tb, table.numel(), rf, pages, blocks, count, new_table.data_ptr(),
                                   new_refs.data_ptr(), moved.data_ptr(), status.data_ptr(), wptr, nb, c.handle))
+    _written(c, pools)
     return new_table, new_refs, moved, status
