@@ -499,9 +499,13 @@ int iso_policy_loss_logits(const void* logits, int dtype, int64_t rows, int64_t 
  *   status [5] int32, written: pages lacking, children longer than max_pages
  *            allow, pages copied, pages taken, pages left free.
  * If one of the first two is not 0 nothing is done: new_length is 0, new_table
- * -1, new_refs is refs, no token is copied, and the old cache stands.
+ * -1, new_refs is refs, the other statuses are 0, no token is copied, and the old
+ * cache stands.
  * What breaks the above is held inside the arrays: lengths to [0, max_pages *
- * page_size], negative refs to 0, an entry outside [0, pages) holds no page.
+ * page_size], negative refs to 0, an entry outside [0, pages) holds no page.  Where
+ * refs are below what the tables hold, a page that children go on to write has
+ * them as holders at least, and other counts end at 0: such a page is free, also
+ * where a table still holds it.  Counts stay below 2^31, after the step too.
  * seqs and children at most 2^20.
  *
  * iso_pages_compact - the live pages (refs > 0) moved together: with n of them,

@@ -86,7 +86,8 @@ struct Fork {
     int32_t* long_sum;  // [blocks of children]
     int32_t* free_sum;  // [blocks of pages]
     Copy* copies;       // [children]
-    int32_t* plan;      // [3]: done or not, copies, pages taken
+    int32_t* gap;       // [children] what a kept page's count lacks, or NULL: k_fork_write adds it
+    int32_t* plan;      // [4]: done or not, copies, pages taken, counts below 0 or none
     bool counts_left;   // k_fork_write brings the counts up to date
 
     __device__ __forceinline__ int64_t tokens_of(int64_t s) const {
@@ -151,6 +152,7 @@ __global__ __launch_bounds__(kNT) void k_fork_begin(Fork f, Blocks pb) {
     }
     if (f.kids)
         for (int64_t s = t; s < f.seqs; s += step) f.kids[s] = 0;
+    if (t == 0) f.plan[3] = 0;
 }
 
 __global__ __launch_bounds__(kNT) void k_fork_count(Fork f) {
@@ -190,6 +192,7 @@ __global__ __launch_bounds__(kNT) void k_fork_refs(Fork f, Blocks pb) {
             if (!f.is_page(q)) continue;
             const int32_t was = atomicAdd(&f.new_refs[q], more), is = was + more;
             if ((was <= 0) != (is <= 0)) atomicAdd(&f.free_sum[q / pb.per], is <= 0 ? 1 : -1);
+            if (is < 0) f.plan[3] = 1;  // fewer holders counted than the tables have
         }
     }
 }
@@ -210,8 +213,11 @@ __device__ __forceinline__ void write_status(const Fork& f, const Total& t) {
     f.plan[0] = done;
 }
 
-// Blocks of children: the pages each takes.
-__global__ __launch_bounds__(kNT) void k_fork_need(Fork f, int64_t child_blocks) {
+// Blocks of children: the pages each takes.  A page that children go on to write
+// has them as holders at least, however few are counted (the first of them brings
+// its count up, the others find it no larger than themselves before and after): it
+// is not free, so that nobody's copy goes where another is read.
+__global__ __launch_bounds__(kNT) void k_fork_need(Fork f, Blocks pb, int64_t child_blocks) {
     __shared__ int64_t red[2][kWaves];
     for (int64_t b = blockIdx.x; b < child_blocks; b += gridDim.x) {
         const int64_t i = b * kNT + threadIdx.x;
@@ -222,7 +228,12 @@ __global__ __launch_bounds__(kNT) void k_fork_need(Fork f, int64_t child_blocks)
             const int64_t want = f.pages_for(c.after);
             if (c.edge >= 0) {
                 const Mark m = f.mark[c.edge];
-                copies = !(f.new_refs[c.edge] == m.writers && m.first == i);
+                const int32_t held = f.new_refs[c.edge];
+                copies = !(held <= m.writers && m.first == i);
+                if (held < m.writers && m.first == i) {
+                    f.new_refs[c.edge] = m.writers;
+                    if (held <= 0) atomicAdd(&f.free_sum[c.edge / pb.per], -1);
+                }
             }
             too_long = want > f.max_pages || c.after > INT32_MAX;
             need = too_long ? 0 : want - f.pages_for(c.before) + copies;
@@ -240,17 +251,22 @@ __global__ __launch_bounds__(kNT) void k_fork_need(Fork f, int64_t child_blocks)
 
 // The list of the taken pages, the lowest free ones: a block's part, by a
 // workgroup of NT threads.  The counts stay as they are: other workgroups of the
-// launch go by them (k_fork_write brings them up to date).
-template <int NT>
+// launch go by them (k_fork_write brings them up to date), but that those below 0
+// (is there one: `below`) of pages nobody goes on to write become 0.  Pages for
+// which `kept` are not free though their count may say so (does one: `some`).
+template <int NT, typename K>
 __device__ __forceinline__ void list_block(const Fork& f, const Blocks& pb, int64_t b, int64_t rank, const Total& total,
-                                           int* red) {
+                                           int* red, bool below, bool some, K kept) {
     constexpr int kW = NT / 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t to = (b + 1) * pb.per < f.pages ? (b + 1) * pb.per : f.pages;
     if (!total.done()) return;
+    if (below)
+        for (int64_t p = b * pb.per + threadIdx.x; p < to; p += NT)
+            if (f.new_refs[p] < 0 && !kept(p)) f.new_refs[p] = 0;
     for (int64_t p0 = b * pb.per; p0 < to && rank < total.need; p0 += NT) {
         const int64_t p = p0 + threadIdx.x;
-        const bool open = p < to && f.new_refs[p] <= 0;
+        const bool open = p < to && f.new_refs[p] <= 0 && !(some && kept(p));
         const uint64_t mask = __ballot(open);
         if (lane == 0) red[wave] = __popcll(mask);
         __syncthreads();
@@ -270,6 +286,7 @@ __device__ __forceinline__ void list_block(const Fork& f, const Blocks& pb, int6
 __global__ __launch_bounds__(kNT) void k_fork_list(Fork f, Blocks pb, int64_t child_blocks) {
     __shared__ int64_t red64[6][kWaves];
     __shared__ int red[kWaves];
+    const bool below = f.plan[3];
     for (int64_t b = blockIdx.x; b < child_blocks + pb.count; b += gridDim.x) {
         // need, late, copies, free; need and copies, or free, of the blocks before
         int64_t v[6] = {0, 0, 0, 0, 0, 0};
@@ -304,7 +321,7 @@ __global__ __launch_bounds__(kNT) void k_fork_list(Fork f, Blocks pb, int64_t ch
                 f.copies[place] = Copy{c.edge, (int32_t)start, (int32_t)f.past(c.before), 0};
             }
         } else {
-            list_block<kNT>(f, pb, b - child_blocks, v[4], total, red);
+            list_block<kNT>(f, pb, b - child_blocks, v[4], total, red, below, false, [](int64_t) { return false; });
         }
     }
 }
@@ -316,6 +333,7 @@ struct Few {
     int64_t start, place;  // pages and copies before its own
     int64_t need;
     int copy;
+    int32_t gap;  // what the count of its edge page lacks, at the first of the page's writers
     Total total;
 };
 // Exclusive prefixes of N values over the workgroup, and their totals.
@@ -373,15 +391,25 @@ struct Edges {
         atomicMin(&first[at], (int32_t)threadIdx.x);
         return (int)at;
     }
+    __device__ __forceinline__ bool has(int32_t q) const {
+        uint32_t at = (uint32_t)q * 2654435761u >> 21;
+        while (page[at] != -1 && page[at] != q) at = (at + 1) & (kPlaces - 1);
+        return page[at] == q;
+    }
 };
 // Every thread's child, its edge page (if any) at place `at` of the table and held
-// by `count`; `room` the free pages it has counted, then those before them.  After
-// a barrier.
+// by `count`, its writers at least (as in k_fork_need); `room` the free pages it has
+// counted, such a page among them where `count` is not above 0, then those before
+// them.  After a barrier.
 __device__ __forceinline__ Few few_children(const Fork& f, const Child& c, const Edges& edges, int at, int32_t count,
                                             int64_t& room, int64_t (*red)[kOneWaves]) {
     Few o;
     o.c = c;
-    o.copy = c.edge >= 0 && !(count == edges.writers[at] && edges.first[at] == (int32_t)threadIdx.x);
+    const int32_t writers = edges.writers[at];
+    const bool first = c.edge >= 0 && edges.first[at] == (int32_t)threadIdx.x;
+    o.copy = c.edge >= 0 && !(count <= writers && first);
+    o.gap = first && count < writers ? writers - count : 0;
+    room -= o.gap && count <= 0;
     const int64_t want = f.pages_for(c.after);
     const bool too_long = want > f.max_pages || c.after > INT32_MAX;
     o.need = too_long ? 0 : want - f.pages_for(c.before) + o.copy;
@@ -399,6 +427,7 @@ __device__ __forceinline__ void write_few(const Fork& f, const Few& o, bool done
     if (i >= f.children) return;
     f.need[i] = (int32_t)o.need | (o.copy << 31);
     f.start[i] = o.start;
+    f.gap[i] = o.gap;
     if (done && o.copy) f.copies[o.place] = Copy{o.c.edge, (int32_t)o.start, (int32_t)f.past(o.c.before), 0};
 }
 
@@ -408,6 +437,7 @@ __global__ __launch_bounds__(kOneNT) void k_fork_few(Fork f, Blocks pb) {
     __shared__ int64_t red[3][kOneWaves];
     __shared__ int red32[kOneWaves];
     Child c{-1, 0, 0, -1};
+    const bool below = f.plan[3];
     edges.clear();
     if (threadIdx.x < f.children) c = child_of(f, threadIdx.x);
     const int32_t count = c.edge >= 0 ? f.new_refs[c.edge] : 0;
@@ -417,6 +447,8 @@ __global__ __launch_bounds__(kOneNT) void k_fork_few(Fork f, Blocks pb) {
     int64_t open = 0;
     for (int64_t k = threadIdx.x; k < pb.count; k += kOneNT) open += f.free_sum[k];
     const Few o = few_children(f, c, edges, at, count, open, red);
+    const bool lost = o.gap && count <= 0;  // its edge page was counted as free
+    const bool some = __syncthreads_count(lost) > 0;
     if (blockIdx.x == 0) {
         write_few(f, o, o.total.done());
         if (threadIdx.x == 0) write_status(f, o.total);
@@ -424,8 +456,9 @@ __global__ __launch_bounds__(kOneNT) void k_fork_few(Fork f, Blocks pb) {
     for (int64_t b = blockIdx.x; b < pb.count; b += gridDim.x) {
         int64_t before[1] = {0}, rank[1];
         for (int64_t k = threadIdx.x; k < b; k += kOneNT) before[0] += f.free_sum[k];
+        before[0] -= lost && c.edge / pb.per < b;
         one_prefix(before, rank, red);
-        list_block<kOneNT>(f, pb, b, rank[0], o.total, red32);
+        list_block<kOneNT>(f, pb, b, rank[0], o.total, red32, below, some, [&](int64_t p) { return edges.has((int32_t)p); });
     }
 }
 
@@ -483,6 +516,8 @@ __global__ __launch_bounds__(kOneNT) void k_fork_one(Fork f) {
         }
         load(e0 + kOneNT * kAhead);
     }
+    __syncthreads();
+    if (c.edge >= 0) atomicMax(&refs[c.edge], edges.writers[place]);
     __syncthreads();
     int64_t at = 0;
     const int first = t * kEach;
@@ -555,6 +590,7 @@ __global__ __launch_bounds__(kNT) void k_fork_write(Fork f, States st) {
         const Child c = child_of(f, i);
         const int64_t held = f.pages_for(c.before), want = done ? f.pages_for(c.after) : 0;
         const bool copy = f.need[i] < 0;
+        const int32_t gap = f.gap ? f.gap[i] : 0;
         const int64_t edge = copy ? held - 1 : -1, start = f.start[i];
         for (int64_t j = threadIdx.x; j < f.max_pages; j += kNT) {
             int32_t q = -1;
@@ -570,7 +606,8 @@ __global__ __launch_bounds__(kNT) void k_fork_write(Fork f, States st) {
         }
         if (threadIdx.x == 0) {
             f.new_length[i] = done ? (int32_t)c.after : 0;
-            if (f.counts_left && copy && done) atomicAdd(&f.new_refs[c.edge], -1);
+            const int32_t more = f.counts_left && done ? gap - copy : 0;
+            if (more) atomicAdd(&f.new_refs[c.edge], more);
         }
     }
     if (f.counts_left) {
@@ -600,7 +637,7 @@ __global__ __launch_bounds__(kNT) void k_fork_write(Fork f, States st) {
 struct ForkPlan {
     Blocks pb;
     int64_t child_blocks;
-    size_t mark, kids, list, need, start, need_sum, copy_sum, long_sum, free_sum, copies, plan, bytes;
+    size_t mark, kids, list, need, start, need_sum, copy_sum, long_sum, free_sum, copies, gap, plan, bytes;
 };
 ForkPlan fork_plan(int64_t seqs, int64_t children, int64_t pages) {
     ForkPlan p;
@@ -622,7 +659,8 @@ ForkPlan fork_plan(int64_t seqs, int64_t children, int64_t pages) {
     p.long_sum = room(p.child_blocks, 4);
     p.free_sum = room(p.pb.count, 4);
     p.copies = room(children, sizeof(Copy));
-    p.plan = room(3, 4);
+    p.gap = room(children, 4);
+    p.plan = room(4, 4);
     p.bytes = at;
     return p;
 }
@@ -848,7 +886,7 @@ int iso_pages_fork(const int32_t* table, const int32_t* length, int64_t seqs, in
            reinterpret_cast<int64_t*>(ws + pl.start), reinterpret_cast<int64_t*>(ws + pl.need_sum),
            reinterpret_cast<int32_t*>(ws + pl.copy_sum), reinterpret_cast<int32_t*>(ws + pl.long_sum),
            reinterpret_cast<int32_t*>(ws + pl.free_sum), reinterpret_cast<Copy*>(ws + pl.copies),
-           reinterpret_cast<int32_t*>(ws + pl.plan), true};
+           reinterpret_cast<int32_t*>(ws + pl.gap), reinterpret_cast<int32_t*>(ws + pl.plan), true};
     hipStream_t hs = static_cast<hipStream_t>(stream);
     const bool few = children <= kOneNT;
     if (few && pages <= kOnePages && seqs <= kOneNT && seqs * max_pages <= kOneEntries) {
@@ -858,6 +896,8 @@ int iso_pages_fork(const int32_t* table, const int32_t* length, int64_t seqs, in
         if (few) {
             f.mark = nullptr;
             f.kids = nullptr;
+        } else {
+            f.gap = nullptr;
         }
         const int64_t rows = few ? 0 : (seqs + kNT - 1) / kNT;
         hipLaunchKernelGGL(k_fork_begin, grid_of(pl.pb.count > rows ? pl.pb.count : rows), dim3(kNT), 0, hs, f, pl.pb);
@@ -867,7 +907,7 @@ int iso_pages_fork(const int32_t* table, const int32_t* length, int64_t seqs, in
             hipLaunchKernelGGL(k_fork_few, dim3((unsigned)(pl.pb.count < 1 ? 1 : pl.pb.count < kFewGrid ? pl.pb.count : kFewGrid)),
                                dim3(kOneNT), 0, hs, f, pl.pb);
         } else {
-            hipLaunchKernelGGL(k_fork_need, grid_of(pl.child_blocks), dim3(kNT), 0, hs, f, pl.child_blocks);
+            hipLaunchKernelGGL(k_fork_need, grid_of(pl.child_blocks), dim3(kNT), 0, hs, f, pl.pb, pl.child_blocks);
             hipLaunchKernelGGL(k_fork_list, grid_of(pl.child_blocks + pl.pb.count), dim3(kNT), 0, hs, f, pl.pb, pl.child_blocks);
         }
     }

@@ -90,6 +90,8 @@ def pages_fork(table, length, refs, parent, page_size, grow, pools=(), page_dim=
     for p, before, after in kids:
         q = int(table[p, before // page_size]) if after > before and before % page_size else -1
         edge.append(q if page(q) else -1)
+    for q in set(edge) - {-1}:
+        new[q] = max(new[q], edge.count(q))  # however few holders are counted, these hold it
     copies = []
     for i, q in enumerate(edge):
         alone = q >= 0 and new[q] == edge.count(q) and edge.index(q) == i
