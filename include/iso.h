@@ -468,7 +468,8 @@ int iso_policy_loss_logits(const void* logits, int dtype, int64_t rows, int64_t 
  * count has outer = layers, mid = heads, inner = t * dim * element size.
  * Blocks may not overlap; arrays of one call may not either, from the first to
  * the last byte each (two interleaved arrays are one, with a larger outer or
- * mid).  At most ISO_MAX_BLOCKS arrays a call; any element type and alignment.
+ * mid).  At most ISO_MAX_BLOCKS arrays a call (a launch for every 16); any element
+ * type and alignment.
  *
  * iso_beam_reorder - row r of every array becomes what row parent[r] was, in
  * place.  parent [batch*beams] int32: a row of the same item (r / beams); any
@@ -516,7 +517,7 @@ int iso_policy_loss_logits(const void* logits, int dtype, int64_t rows, int64_t 
  *   pools    as above; whole pages are moved, in place.
  *   status [2] int32, written: live pages, pages moved.
  */
-#define ISO_MAX_BLOCKS 16
+#define ISO_MAX_BLOCKS 512
 typedef struct iso_blocks {
     void* base;
     int64_t outer, outer_stride, row_stride, mid, mid_stride, inner;

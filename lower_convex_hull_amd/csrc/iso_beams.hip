@@ -744,31 +744,36 @@ int iso_beam_reorder(const iso_blocks* states, int count, const int32_t* parent,
     if (batch < 0 || beams < 1 || beams > kMaxBeams || batch > 0x7fffffffLL / beams) return ISO_ERR_ARG;
     const int64_t rows = batch * beams;
     const Span other[] = {{parent, (size_t)rows * 4}};
-    States st;
-    if (!take_states(states, count, rows, other, st)) return ISO_ERR_ARG;
+    Arrays all;
+    if (!take_states(states, count, rows, other, all)) return ISO_ERR_ARG;
     if (rows && !parent) return ISO_ERR_ARG;
     if (!aligned(parent, 4)) return ISO_ERR_ARG;
-    if (!st.count) return ISO_OK;
+    if (!all.count) return ISO_OK;
     int shift = 0;  // a workgroup's loads go over the rows first
     while (shift < 11 && (beams << (shift + 1)) <= kReorderNT * kReorderU) ++shift;
     // columns of an array's rows, rows over its outer blocks: 31 bits each
-    int64_t tiles = 1, items = 1;
-    for (int i = 0; i < st.count; ++i) {
-        const iso_blocks& s = st.b[i];
-        const int64_t cols = (s.inner + 15) / 16;
-        if (cols > 0x7fffffffLL / s.mid || s.outer > 0x7fffffffLL / batch) return ISO_ERR_ARG;
-        const int64_t t = ((s.mid * cols - 1) >> shift) + 1;
-        tiles = t > tiles ? t : tiles;
-        items = batch * s.outer > items ? batch * s.outer : items;
+    for (int i = 0; i < all.count; ++i) {
+        const iso_blocks& s = all.b[i];
+        if ((s.inner + 15) / 16 > 0x7fffffffLL / s.mid || s.outer > 0x7fffffffLL / batch) return ISO_ERR_ARG;
     }
-    const dim3 grid((unsigned)(tiles < 65536 ? tiles : 65536), (unsigned)(items < 16384 ? items : 16384));
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    auto start = [&](auto big) {
-        hipLaunchKernelGGL(k_beam_reorder<decltype(big)::value>, grid, dim3(kReorderNT), 0, hs, st, parent, (uint32_t)batch,
-                           (int)beams, shift);
-    };
-    if (streamed(st, rows)) start(std::true_type{});
-    else start(std::false_type{});
+    const bool stream_all = streamed(all, rows);
+    all.each_launch([&](const States& st, bool) {
+        int64_t tiles = 1, items = 1;
+        for (int i = 0; i < st.count; ++i) {
+            const iso_blocks& s = st.b[i];
+            const int64_t t = ((s.mid * ((s.inner + 15) / 16) - 1) >> shift) + 1;
+            tiles = t > tiles ? t : tiles;
+            items = batch * s.outer > items ? batch * s.outer : items;
+        }
+        const dim3 grid((unsigned)(tiles < 65536 ? tiles : 65536), (unsigned)(items < 16384 ? items : 16384));
+        auto start = [&](auto big) {
+            hipLaunchKernelGGL(k_beam_reorder<decltype(big)::value>, grid, dim3(kReorderNT), 0, hs, st, parent,
+                               (uint32_t)batch, (int)beams, shift);
+        };
+        if (stream_all) start(std::true_type{});
+        else start(std::false_type{});
+    });
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 

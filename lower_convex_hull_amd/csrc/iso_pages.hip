@@ -823,7 +823,7 @@ constexpr int kGrid = 2048, kCopyGrid = 8192, kFewGrid = 64;
 inline dim3 grid_of(int64_t items) { return dim3((unsigned)(items < 1 ? 1 : items < kGrid ? items : kGrid)); }
 
 // A block's columns of 16 bytes fit 31 bits, items of a copy of every page 64.
-bool pools_ok(const States& st, int64_t pages, int64_t page_size) {
+bool pools_ok(const Arrays& st, int64_t pages, int64_t page_size) {
     for (int i = 0; i < st.count; ++i) {
         const iso_blocks& s = st.b[i];
         if (s.inner % page_size) return false;
@@ -833,7 +833,7 @@ bool pools_ok(const States& st, int64_t pages, int64_t page_size) {
     return true;
 }
 // Runs that follow each other without a gap are one.
-void join_runs(States& st) {
+void join_runs(Arrays& st) {
     for (int i = 0; i < st.count; ++i) {
         iso_blocks& s = st.b[i];
         if (s.mid > 1 && s.mid_stride == s.inner) {
@@ -873,8 +873,8 @@ int iso_pages_fork(const int32_t* table, const int32_t* length, int64_t seqs, in
     const Span all[] = {out[0], out[1], out[2], out[3], in[0], in[1], in[2], in[3], in[4]};
     for (const Span& s : all)
         if (!aligned(s.p, 4)) return ISO_ERR_ARG;
-    States st;
-    if (!take_states(pools, count, pages, all, st) || !pools_ok(st, pages, page_size)) return ISO_ERR_ARG;
+    Arrays arrays;
+    if (!take_states(pools, count, pages, all, arrays) || !pools_ok(arrays, pages, page_size)) return ISO_ERR_ARG;
     const ForkPlan pl = fork_plan(seqs, children, pages);
     if (!workspace || workspace_bytes < pl.bytes) return ISO_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return ISO_ERR_ARG;
@@ -911,13 +911,18 @@ int iso_pages_fork(const int32_t* table, const int32_t* length, int64_t seqs, in
             hipLaunchKernelGGL(k_fork_list, grid_of(pl.child_blocks + pl.pb.count), dim3(kNT), 0, hs, f, pl.pb, pl.child_blocks);
         }
     }
-    if (children) {
-        int64_t items = children;  // a child's table; a tile of an array's block of a copied page
+    const bool stream_all = streamed(arrays, pages);
+    if (children) arrays.each_launch([&](const States& st, bool first) {
+        if (!first) {  // copies only: tables and counts are written
+            f.children = 0;
+            f.counts_left = false;
+        }
+        int64_t items = f.children;  // a child's table; a tile of an array's block of a copied page
         for (int i = 0; i < st.count; ++i) items += children * st.b[i].outer * ((st.b[i].inner * st.b[i].mid >> 15) + 1);
         const dim3 grid((unsigned)(items < kCopyGrid ? items : kCopyGrid));
-        if (streamed(st, pages)) hipLaunchKernelGGL(k_fork_write<true>, grid, dim3(kNT), 0, hs, f, st);
+        if (stream_all) hipLaunchKernelGGL(k_fork_write<true>, grid, dim3(kNT), 0, hs, f, st);
         else hipLaunchKernelGGL(k_fork_write<false>, grid, dim3(kNT), 0, hs, f, st);
-    }
+    });
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 
@@ -939,9 +944,9 @@ int iso_pages_compact(const int32_t* table, int64_t entries, const int32_t* refs
     const Span all[] = {out[0], out[1], out[2], out[3], in[0], in[1]};
     for (const Span& s : all)
         if (!aligned(s.p, 4)) return ISO_ERR_ARG;
-    States st;
-    if (!take_states(pools, count, pages, all, st) || !pools_ok(st, pages, 1)) return ISO_ERR_ARG;
-    join_runs(st);
+    Arrays arrays;
+    if (!take_states(pools, count, pages, all, arrays) || !pools_ok(arrays, pages, 1)) return ISO_ERR_ARG;
+    join_runs(arrays);
     const CompactPlan pl = compact_plan(pages);
     if (!workspace || workspace_bytes < pl.bytes) return ISO_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return ISO_ERR_ARG;
@@ -956,11 +961,15 @@ int iso_pages_compact(const int32_t* table, int64_t entries, const int32_t* refs
         hipLaunchKernelGGL(k_compact_count, grid_of(pl.pb.count), dim3(kNT), 0, hs, f, pl.pb);
         hipLaunchKernelGGL(k_compact_map, grid_of(pl.pb.count), dim3(kNT), 0, hs, f, pl.pb);
     }
-    int64_t items = (entries + kNT - 1) / kNT + (pages + kNT - 1) / kNT;
-    for (int i = 0; i < st.count; ++i) items += pages / 2 * st.b[i].outer * ((st.b[i].inner * st.b[i].mid >> 15) + 1);
-    const dim3 grid((unsigned)(items < 1 ? 1 : items < kCopyGrid ? items : kCopyGrid));
-    if (streamed(st, pages)) hipLaunchKernelGGL(k_compact_write<true>, grid, dim3(kNT), 0, hs, f, st);
-    else hipLaunchKernelGGL(k_compact_write<false>, grid, dim3(kNT), 0, hs, f, st);
+    const bool stream_all = streamed(arrays, pages);
+    arrays.each_launch([&](const States& st, bool first) {
+        if (!first) f.entries = f.pages = 0;  // moves only: tables are written (the moved counts once more)
+        int64_t items = (f.entries + kNT - 1) / kNT + (f.pages + kNT - 1) / kNT;
+        for (int i = 0; i < st.count; ++i) items += pages / 2 * st.b[i].outer * ((st.b[i].inner * st.b[i].mid >> 15) + 1);
+        const dim3 grid((unsigned)(items < 1 ? 1 : items < kCopyGrid ? items : kCopyGrid));
+        if (stream_all) hipLaunchKernelGGL(k_compact_write<true>, grid, dim3(kNT), 0, hs, f, st);
+        else hipLaunchKernelGGL(k_compact_write<false>, grid, dim3(kNT), 0, hs, f, st);
+    });
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }
 

@@ -5,11 +5,29 @@
 #include "../../include/iso.h"
 #include "iso_losses.hpp"
 
+#include <algorithm>
+
 namespace iso {
 
+// What one launch takes, as an argument of 900 bytes.
 struct States {
+    iso_blocks b[16];
+    int count;
+};
+// A call's arrays, those without bytes left out, and their launches: one for every
+// sixteen, and at least one.
+struct Arrays {
+    static constexpr int kLaunch = sizeof(States::b) / sizeof(iso_blocks);
     iso_blocks b[ISO_MAX_BLOCKS];
     int count;
+    template <typename F>
+    void each_launch(F f) const {
+        for (int i = 0; i == 0 || i < count; i += kLaunch) {
+            States st{};
+            for (; st.count < kLaunch && i + st.count < count; ++st.count) st.b[st.count] = b[i + st.count];
+            f(st, i == 0);
+        }
+    }
 };
 
 // Bytes from the first to the last of `rows` rows' blocks, 0 for none, or -1:
@@ -45,9 +63,9 @@ inline int64_t blocks_extent(const iso_blocks& b, int64_t rows) {
 // The arrays of a call, those without bytes left out; false if one is not
 // right, or two overlap, or one overlaps one of `other`.
 template <int N>
-bool take_states(const iso_blocks* from, int count, int64_t rows, const Span (&other)[N], States& to) {
+bool take_states(const iso_blocks* from, int count, int64_t rows, const Span (&other)[N], Arrays& to) {
     if (count < 0 || count > ISO_MAX_BLOCKS || (count && !from)) return false;
-    to = States{};
+    to.count = 0;
     Span at[ISO_MAX_BLOCKS];
     for (int i = 0; i < count; ++i) {
         const int64_t bytes = blocks_extent(from[i], rows);
@@ -55,13 +73,15 @@ bool take_states(const iso_blocks* from, int count, int64_t rows, const Span (&o
         if (!bytes) continue;
         const Span s{from[i].base, (size_t)bytes};
         if (!s.p) return false;
-        for (int k = 0; k < to.count; ++k)
-            if (overlap(s, at[k])) return false;
         for (int k = 0; k < N; ++k)
             if (overlap(s, other[k])) return false;
         at[to.count] = s;
         to.b[to.count++] = from[i];
     }
+    // by their first bytes: where any two overlap, two neighbours do
+    std::sort(at, at + to.count, [](const Span& a, const Span& b) { return (uintptr_t)a.p < (uintptr_t)b.p; });
+    for (int k = 1; k < to.count; ++k)
+        if (overlap(at[k - 1], at[k])) return false;
     return true;
 }
 
@@ -98,7 +118,7 @@ __device__ __forceinline__ void store_quad(char* at, const Quad& v) {
     else *p = v;
 }
 // Whether the arrays' rows, of which there are `rows`, come to more than that.
-inline bool streamed(const States& st, int64_t rows) {
+inline bool streamed(const Arrays& st, int64_t rows) {
     double bytes = 0.0;
     for (int i = 0; i < st.count; ++i) bytes += (double)rows * st.b[i].outer * st.b[i].mid * st.b[i].inner;
     return bytes > kStreamed;

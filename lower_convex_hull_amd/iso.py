@@ -64,7 +64,8 @@ EXPORTS = ("iso_fit", "iso_fit_ex", "iso_fit_noalloc", "iso_workspace_bytes", "i
            "iso_beam_reorder", "iso_pages_fork", "iso_pages_fork_workspace_bytes", "iso_pages_compact",
            "iso_pages_compact_workspace_bytes")
 
-ISO_MAX_BLOCKS = 16
+ISO_MAX_BLOCKS = 512
+LAUNCH_BLOCKS = 16  # arrays that one launch takes
 
 
 class Blocks(ctypes.Structure):
@@ -766,7 +767,7 @@ def _block(launch, t, dim, token_dim):
 
 
 def _blocks(launch, tensors, dims, rows, token_dim=None):
-    """(array of Blocks, count) of tensors that hold `rows` rows each."""
+    """(array of Blocks, count) of tensors that hold `rows` rows each, of one launch."""
     if hasattr(tensors, "data_ptr"):
         tensors = (tensors,)
     count = len(tensors)
@@ -774,14 +775,31 @@ def _blocks(launch, tensors, dims, rows, token_dim=None):
         dims = (dims,) * count
     if len(dims) != count:
         raise ValueError("one dimension for each tensor")
-    if count > ISO_MAX_BLOCKS:
-        raise ValueError(f"at most {ISO_MAX_BLOCKS} tensors a call")
+    if count > LAUNCH_BLOCKS:
+        raise ValueError(f"at most {LAUNCH_BLOCKS} tensors a launch")
     blocks = []
     for t, dim in zip(tensors, dims):
         blocks.append(_block(launch, t, dim, token_dim))
         if t.shape[dim] != rows:
             raise ValueError(f"dimension {dim} of a tensor of shape {tuple(t.shape)} must have {rows} rows or pages")
     return (Blocks * count)(*blocks) if count else None, count
+
+
+def _arrays(launch, tensors, dims, rows, token_dim=None):
+    """_blocks of the tensors of a call, which may be those of several launches."""
+    count = 1 if hasattr(tensors, "data_ptr") else len(tensors)
+    if count <= LAUNCH_BLOCKS:
+        return _blocks(launch, tensors, dims, rows, token_dim)
+    if count > ISO_MAX_BLOCKS:
+        raise ValueError(f"at most {ISO_MAX_BLOCKS} tensors a call")
+    if not isinstance(dims, int) and len(dims) != count:
+        raise ValueError("one dimension for each tensor")
+    out = (Blocks * count)()
+    for i in range(0, count, LAUNCH_BLOCKS):
+        part = dims if isinstance(dims, int) else dims[i:i + LAUNCH_BLOCKS]
+        some, n = _blocks(launch, tensors[i:i + LAUNCH_BLOCKS], part, rows, token_dim)
+        out[i:i + n] = some
+    return out, count
 
 
 def beam_reorder(states, parent, *, dim=0, stream=None):
@@ -796,7 +814,7 @@ def beam_reorder(states, parent, *, dim=0, stream=None):
         raise ValueError("parent must have the shape (batch, beams)")
     pr = c.use(parent, "parent", parent.shape, (c.torch.int32,))
     batch, beams = parent.shape
-    blocks, count = _blocks(c, states, dim, batch * beams)
+    blocks, count = _arrays(c, states, dim, batch * beams)
     _done(c.lib.iso_beam_reorder(blocks, count, pr, batch, beams, c.handle))
     _written(c, states)
     return states
@@ -821,7 +839,7 @@ def pages_fork(table, length, refs, parent, *, page_size: int, grow=1, pools=(),
     rf, pr = c.use(refs, "refs", refs.shape, i32), c.use(parent, "parent", parent.shape, i32)
     pages, children = refs.shape[0], parent.shape[0]
     each, gr = (_int32(grow, "grow"), None) if isinstance(grow, int) else (0, c.use(grow, "grow", parent.shape, i32))
-    blocks, count = _blocks(c, pools, page_dim, pages, token_dim)
+    blocks, count = _arrays(c, pools, page_dim, pages, token_dim)
     for p in ((pools,) if hasattr(pools, "data_ptr") else pools):
         if p.shape[token_dim] != page_size:
             raise ValueError("each pool must have page_size tokens a page")
@@ -846,7 +864,7 @@ def pages_compact(table, refs, *, pools=(), page_dim: int = 0, stream=None):
         raise ValueError("refs must be 1-D")
     tb, rf = c.use(table, "table", table.shape, (t.int32,)), c.use(refs, "refs", refs.shape, (t.int32,))
     pages = refs.shape[0]
-    blocks, count = _blocks(c, pools, page_dim, pages)
+    blocks, count = _arrays(c, pools, page_dim, pages)
     new_table, new_refs = c.new(t.int32, *table.shape), c.new(t.int32, pages)
     moved, status = c.new(t.int32, pages), c.new(t.int32, 2)
     nb = c.lib.iso_pages_compact_workspace_bytes(pages)
