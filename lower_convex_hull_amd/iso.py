@@ -735,10 +735,14 @@ def _written(launch, tensors):
     launch.torch._C._increment_version((tensors,) if hasattr(tensors, "data_ptr") else tensors)
 
 
-def _block(launch, t, dim, token_dim):
-    """The Blocks of a tensor whose rows (or pages) are dimension `dim`.  What lies
-    behind a row is blocks of adjacent elements at one stride: from `token_dim` on,
-    or as long as they get.  The call writes the tensor and records nothing for autograd."""
+_ONE = (1, 0)
+
+
+def _block(launch, t, dim, rows, token_dim):
+    """The fields of a Blocks: a tensor whose `rows` rows (or pages) are dimension
+    `dim`.  What lies behind a row is blocks of adjacent elements at one stride: from
+    `token_dim` on, or as long as they get.  The call writes the tensor and records
+    nothing for autograd."""
     if t.get_device() != launch.index:
         raise TypeError(f"every tensor must be on {launch.dev}")
     if t.requires_grad and _grad_mode():
@@ -747,6 +751,8 @@ def _block(launch, t, dim, token_dim):
     at = dims = len(shape)
     if not 0 <= dim < dims:
         raise ValueError(f"a tensor of shape {tuple(shape)} has no dimension {dim}")
+    if shape[dim] != rows:
+        raise ValueError(f"dimension {dim} of a tensor of shape {tuple(shape)} must have {rows} rows or pages")
     size = inner = t.element_size()
     last = dim + 1 if token_dim is None else token_dim
     if not dim < last <= dims or (token_dim is not None and last == dims):
@@ -758,12 +764,13 @@ def _block(launch, t, dim, token_dim):
             raise ValueError("a page's tokens must be adjacent from token_dim on")
         at -= 1
         inner *= shape[at]
-    outer, mid = _joined(shape, stride, 0, dim), _joined(shape, stride, dim + 1, at)
+    outer = _joined(shape, stride, 0, dim) if dim else _ONE
+    mid = _joined(shape, stride, dim + 1, at) if at > dim + 1 else _ONE
     if outer is None or mid is None:
         raise ValueError("the dimensions before the rows, and those behind them, must have one stride")
     if launch.other is not None:
         t.record_stream(launch.other)
-    return Blocks(t.data_ptr(), outer[0], outer[1] * size, stride[dim] * size, mid[0], mid[1] * size, inner)
+    return t.data_ptr(), outer[0], outer[1] * size, stride[dim] * size, mid[0], mid[1] * size, inner
 
 
 def _blocks(launch, tensors, dims, rows, token_dim=None):
@@ -777,11 +784,7 @@ def _blocks(launch, tensors, dims, rows, token_dim=None):
         raise ValueError("one dimension for each tensor")
     if count > LAUNCH_BLOCKS:
         raise ValueError(f"at most {LAUNCH_BLOCKS} tensors a launch")
-    blocks = []
-    for t, dim in zip(tensors, dims):
-        blocks.append(_block(launch, t, dim, token_dim))
-        if t.shape[dim] != rows:
-            raise ValueError(f"dimension {dim} of a tensor of shape {tuple(t.shape)} must have {rows} rows or pages")
+    blocks = [_block(launch, t, dim, rows, token_dim) for t, dim in zip(tensors, dims)]
     return (Blocks * count)(*blocks) if count else None, count
 
 
