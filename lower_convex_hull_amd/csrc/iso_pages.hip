@@ -463,12 +463,18 @@ __global__ __launch_bounds__(kOneNT) void k_fork_few(Fork f, Blocks pb) {
 }
 
 // A step in one workgroup but for what k_fork_write does: the counts are in LDS.  Bound by
-// the latency of its steps: 7.7 us for four sequences, 14.6 for 256 over 12280 pages (as
-// four launches 20 and more; with each child's page compared with every other's 27).
-// Up to kOnePages pages, kOneNT children and sequences, kOneEntries entries of
-// tables (their counting is this workgroup's).
+// the latency of its steps: 7.7 us for four sequences, 14.6 for 256 over 12280 pages (with
+// each child's page compared with every other's 27).
+// Up to kOnePages pages: a step in which every sequence goes on by itself then takes what
+// four launches take (with k_fork_write, 64 sequences: 8192 pages 13.1 us and 14.3, 12288
+// 14.6 and 14.1; 1024 sequences 14.8 and 16.5, 16.5 and 16.5), one whose beams all change
+// parents less (12288 pages 15.2 and 28.0); room for 16384 would cost every step 3 us.
+// Up to kOneEntries entries of tables, which this workgroup alone walks: 256 sequences of
+// 96, 24576 in all, 15.4 us and 15.7, of 128 17.3 and 15.7, of 192 17.8 and 15.7; beams
+// 16.3 and 25.1, 18.5 and 25.1, 18.6 and 25.1 (6000 pages).  Up to kOneNT children and
+// sequences, one a thread.
 constexpr int kOnePages = 12288;
-constexpr int64_t kOneEntries = 1 << 16;
+constexpr int64_t kOneEntries = 1 << 15;
 __global__ __launch_bounds__(kOneNT) void k_fork_one(Fork f) {
     constexpr int kEach = kOnePages / kOneNT, kAhead = 8;
     __shared__ int32_t refs[kOnePages];
@@ -732,10 +738,14 @@ __global__ __launch_bounds__(kNT) void k_compact_map(Compact f, Blocks pb) {
     }
 }
 
-// The same in one workgroup, up to kOnePages pages.
+// The same in one workgroup, up to kCompactPages pages: with k_compact_write 6.2 us for
+// 165 pages, 7.7 for 2048 and 8.6 for 4096, as three launches 7.0, 10.4 and 10.5.  Room for
+// 8192 would cost small pools a microsecond (7.1, 8.5 and 9.9) and lose at 8192 (12.4 and
+// 10.8).
+constexpr int kCompactPages = 4096;
 __global__ __launch_bounds__(kOneNT) void k_compact_one(Compact f) {
-    constexpr int kEach = kOnePages / kOneNT;
-    __shared__ uint8_t lives[kOnePages];
+    constexpr int kEach = kCompactPages / kOneNT;
+    __shared__ uint8_t lives[kCompactPages];
     __shared__ int64_t red[1][kOneWaves];
     const int t = threadIdx.x, first = t * kEach;
     int32_t own[kEach];
@@ -955,7 +965,7 @@ int iso_pages_compact(const int32_t* table, int64_t entries, const int32_t* refs
     Compact f{table, refs, entries, pages, new_table, new_refs, moved, status,
               at(pl.live_sum), at(pl.place), at(pl.holes), at(pl.movers), at(pl.plan)};
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    if (pages <= kOnePages) {
+    if (pages <= kCompactPages) {
         hipLaunchKernelGGL(k_compact_one, dim3(1), dim3(kOneNT), 0, hs, f);
     } else {
         hipLaunchKernelGGL(k_compact_count, grid_of(pl.pb.count), dim3(kNT), 0, hs, f, pl.pb);
