@@ -588,8 +588,10 @@ __device__ __forceinline__ void copy_tile(const iso_blocks& s, const CopyTile& c
         if (at[u] >= 0) store_quad<STREAM>(to + at[u], v[u]);
 }
 
-// The children's tables and lengths, then the copies.
-template <bool STREAM>
+// The children's tables and lengths, then the copies.  These go through the caches,
+// however many there are: who forks reads them next, and they are no slower (cold, from
+// pools past 128 MB: 235 MB copied and read 257 us, streamed 273; 470 MB 461 and 476;
+// 2.2 GB, past every cache, 1768 both, the fork itself 770 and 782).
 __global__ __launch_bounds__(kNT) void k_fork_write(Fork f, States st) {
     const bool done = f.plan[0];
     for (int64_t i = blockIdx.x; i < f.children; i += gridDim.x) {
@@ -635,7 +637,7 @@ __global__ __launch_bounds__(kNT) void k_fork_write(Fork f, States st) {
             const CopyTile ct(s, c.tokens * token);
             if (tile >= ct.tiles()) continue;
             char* base = static_cast<char*>(s.base) + o * s.outer_stride;
-            copy_tile<STREAM>(s, ct, c.tokens * token, base + c.from * s.row_stride, base + f.list[c.to] * s.row_stride, tile);
+            copy_tile<false>(s, ct, c.tokens * token, base + c.from * s.row_stride, base + f.list[c.to] * s.row_stride, tile);
         }
     }
 }
@@ -921,7 +923,6 @@ int iso_pages_fork(const int32_t* table, const int32_t* length, int64_t seqs, in
             hipLaunchKernelGGL(k_fork_list, grid_of(pl.child_blocks + pl.pb.count), dim3(kNT), 0, hs, f, pl.pb, pl.child_blocks);
         }
     }
-    const bool stream_all = streamed(arrays, pages);
     if (children) arrays.each_launch([&](const States& st, bool first) {
         if (!first) {  // copies only: tables and counts are written
             f.children = 0;
@@ -930,8 +931,7 @@ int iso_pages_fork(const int32_t* table, const int32_t* length, int64_t seqs, in
         int64_t items = f.children;  // a child's table; a tile of an array's block of a copied page
         for (int i = 0; i < st.count; ++i) items += children * st.b[i].outer * ((st.b[i].inner * st.b[i].mid >> 15) + 1);
         const dim3 grid((unsigned)(items < kCopyGrid ? items : kCopyGrid));
-        if (stream_all) hipLaunchKernelGGL(k_fork_write<true>, grid, dim3(kNT), 0, hs, f, st);
-        else hipLaunchKernelGGL(k_fork_write<false>, grid, dim3(kNT), 0, hs, f, st);
+        hipLaunchKernelGGL(k_fork_write, grid, dim3(kNT), 0, hs, f, st);
     });
     return hipGetLastError() == hipSuccess ? ISO_OK : ISO_ERR_HIP;
 }

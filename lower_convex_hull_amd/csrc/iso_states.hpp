@@ -101,8 +101,8 @@ typedef uint64_t Wide8 __attribute__((aligned(1), may_alias));
 typedef uint32_t Wide4 __attribute__((aligned(1), may_alias));
 typedef uint16_t Wide2 __attribute__((aligned(1), may_alias));
 
-// STREAM: without a place in the caches, for arrays that do not fit them anyway:
-// past half of the last-level cache (reordering 2.3 GB 471 -> 438 us, half of a pool of
+// STREAM: without a place in the caches, for arrays that do not fit them anyway and
+// are reordered or moved together as a whole: past half of the last-level cache (reordering 2.3 GB 471 -> 438 us, half of a pool of
 // 2.3 GB moved together 320 -> 302; 40 MB reordered again and again 9.8 -> 11.3).
 constexpr int64_t kStreamed = 128 << 20;
 template <bool STREAM>

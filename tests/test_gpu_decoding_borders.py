@@ -40,3 +40,27 @@ def test_compact_where_one_workgroup_ends(torch, pages):
     for live in (0.02, 0.5, 0.98):
         refs = np.where(rng.random(pages) < live, rng.integers(1, 4, pages), rng.integers(-1, 1, pages)).astype(np.int32)
         run_compact(torch, rng.integers(-2, pages + 2, (5, 9)).astype(np.int32), refs, pools_of(torch, gen, pages, 2, True)[0])
+
+
+def test_fork_of_a_large_pool(torch):
+    """A pool past 128 MB of which little and of which much is copied."""
+    page, pages, seqs = 4, 3000, 24
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    pool = torch.randint(-100, 100, (2, pages, page, 6001), generator=gen, device="cuda", dtype=torch.int8)
+    keep = pool.clone()
+    table = torch.arange(seqs, dtype=torch.int32, device="cuda")[:, None] * 7
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    refs[table[:, 0].long()] = 1
+    length = torch.full((seqs,), 3, dtype=torch.int32, device="cuda")
+    for children in (30, 2000):
+        print(f"[decoding] large pool, {children} children", flush=True)
+        parent = torch.arange(children, dtype=torch.int32, device="cuda") % seqs
+        table2 = torch.cat([table, table * 0 - 1], 1).contiguous()
+        out, ln, new, status = iso.pages_fork(table2, length, refs, parent, page_size=page, pools=pool, page_dim=1, token_dim=2)
+        assert status.tolist()[:4] == [0, 0, children - min(children, seqs), children - min(children, seqs)]
+        at = out[:, 0].long()
+        assert torch.equal(pool[:, at, :3], keep[:, table[parent.long(), 0].long(), :3])
+        rest = torch.ones(pages, dtype=torch.bool, device="cuda")
+        rest[at] = False
+        assert torch.equal(pool[:, rest], keep[:, rest]) and torch.equal(pool[:, :, 3], keep[:, :, 3])
+        pool.copy_(keep)
