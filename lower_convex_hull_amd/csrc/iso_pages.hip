@@ -334,6 +334,8 @@ struct Few {
     int64_t need;
     int copy;
     int32_t gap;  // what the count of its edge page lacks, at the first of the page's writers
+    bool lost;    // such a page was counted as free
+    int losts;    // how many were
     Total total;
 };
 // Exclusive prefixes of N values over the workgroup, and their totals.
@@ -409,17 +411,18 @@ __device__ __forceinline__ Few few_children(const Fork& f, const Child& c, const
     const bool first = c.edge >= 0 && edges.first[at] == (int32_t)threadIdx.x;
     o.copy = c.edge >= 0 && !(count <= writers && first);
     o.gap = first && count < writers ? writers - count : 0;
-    room -= o.gap && count <= 0;
+    o.lost = o.gap && count <= 0;
     const int64_t want = f.pages_for(c.after);
     const bool too_long = want > f.max_pages || c.after > INT32_MAX;
     o.need = too_long ? 0 : want - f.pages_for(c.before) + o.copy;
-    // a need is below 2^31, the sum of all below 2^41; children too long and copies share a sum
-    int64_t v[3] = {o.need, ((int64_t)too_long << 32) | o.copy, room}, total[3];
+    // a need is below 2^31, the sum of all below 2^41; children too long and copies share a sum, free pages and lost ones
+    int64_t v[3] = {o.need, ((int64_t)too_long << 32) | o.copy, ((int64_t)o.lost << 32) | room}, total[3];
     one_prefix(v, total, red);
     o.start = v[0];
     o.place = (int32_t)v[1];
-    room = v[2];
-    o.total = Total{total[0], total[2], total[1] >> 32, (int32_t)total[1]};
+    room = (uint32_t)v[2];
+    o.losts = (int)(total[2] >> 32);
+    o.total = Total{total[0], (int64_t)(uint32_t)total[2] - o.losts, total[1] >> 32, (int32_t)total[1]};
     return o;
 }
 __device__ __forceinline__ void write_few(const Fork& f, const Few& o, bool done) {
@@ -447,8 +450,6 @@ __global__ __launch_bounds__(kOneNT) void k_fork_few(Fork f, Blocks pb) {
     int64_t open = 0;
     for (int64_t k = threadIdx.x; k < pb.count; k += kOneNT) open += f.free_sum[k];
     const Few o = few_children(f, c, edges, at, count, open, red);
-    const bool lost = o.gap && count <= 0;  // its edge page was counted as free
-    const bool some = __syncthreads_count(lost) > 0;
     if (blockIdx.x == 0) {
         write_few(f, o, o.total.done());
         if (threadIdx.x == 0) write_status(f, o.total);
@@ -456,9 +457,9 @@ __global__ __launch_bounds__(kOneNT) void k_fork_few(Fork f, Blocks pb) {
     for (int64_t b = blockIdx.x; b < pb.count; b += gridDim.x) {
         int64_t before[1] = {0}, rank[1];
         for (int64_t k = threadIdx.x; k < b; k += kOneNT) before[0] += f.free_sum[k];
-        before[0] -= lost && c.edge / pb.per < b;
+        before[0] -= o.lost && c.edge / pb.per < b;
         one_prefix(before, rank, red);
-        list_block<kOneNT>(f, pb, b, rank[0], o.total, red32, below, some, [&](int64_t p) { return edges.has((int32_t)p); });
+        list_block<kOneNT>(f, pb, b, rank[0], o.total, red32, below, o.losts > 0, [&](int64_t p) { return edges.has((int32_t)p); });
     }
 }
 
