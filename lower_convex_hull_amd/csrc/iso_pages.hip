@@ -562,7 +562,7 @@ struct CopyTile {
         : cols((uint32_t)((bytes + 15) / 16)), all((uint32_t)s.mid * cols) {}
     __device__ __forceinline__ uint32_t tiles() const { return (all + kNT * kCopyU - 1) / (kNT * kCopyU); }
 };
-template <bool STREAM>
+template <bool STREAM_LOADS, bool STREAM_STORES>
 __device__ __forceinline__ void copy_tile(const iso_blocks& s, const CopyTile& c, int64_t bytes, const char* from, char* to,
                                           uint32_t tile) {
     const Divide by_cols(c.cols);
@@ -577,7 +577,7 @@ __device__ __forceinline__ void copy_tile(const iso_blocks& s, const CopyTile& c
             const uint32_t m = by_cols(col), k = col - m * c.cols;
             at[u] = m * s.mid_stride + (int64_t)k * 16;
             if (k + 1 < c.cols || rest == 16) {
-                v[u] = load_quad<STREAM>(from + at[u]);
+                v[u] = load_quad<STREAM_LOADS>(from + at[u]);
             } else {  // the end of a run, taken at once
                 store_bytes(to + at[u], rest, load_bytes(from + at[u], rest));
                 at[u] = -1;
@@ -586,13 +586,15 @@ __device__ __forceinline__ void copy_tile(const iso_blocks& s, const CopyTile& c
     }
 #pragma unroll
     for (int u = 0; u < kCopyU; ++u)
-        if (at[u] >= 0) store_quad<STREAM>(to + at[u], v[u]);
+        if (at[u] >= 0) store_quad<STREAM_STORES>(to + at[u], v[u]);
 }
 
-// The children's tables and lengths, then the copies.  These go through the caches,
-// however many there are: who forks reads them next, and they are no slower (cold, from
-// pools past 128 MB: 235 MB copied and read 257 us, streamed 273; 470 MB 461 and 476;
-// 2.2 GB, past every cache, 1768 both, the fork itself 770 and 782).
+// The children's tables and lengths, then the copies: their loads through the caches,
+// their stores past them, however large the pool is.  Cold, with a read of the copied
+// pages behind them: 14.7 MB 33.1 and 44.0 us (both through the caches 33.0 and 43.0, both
+// past them 34.9 and 45.9), 235 MB 156 and 253 (152 and 258, 169 and 271), 470 MB 252 and
+// 449 (249 and 461, 274 and 478); one after another the same 22 MB a step leave the tables
+// in the caches (25.2 us a step, 26.4, 25.1).
 __global__ __launch_bounds__(kNT) void k_fork_write(Fork f, States st) {
     const bool done = f.plan[0];
     for (int64_t i = blockIdx.x; i < f.children; i += gridDim.x) {
@@ -638,7 +640,7 @@ __global__ __launch_bounds__(kNT) void k_fork_write(Fork f, States st) {
             const CopyTile ct(s, c.tokens * token);
             if (tile >= ct.tiles()) continue;
             char* base = static_cast<char*>(s.base) + o * s.outer_stride;
-            copy_tile<false>(s, ct, c.tokens * token, base + c.from * s.row_stride, base + f.list[c.to] * s.row_stride, tile);
+            copy_tile<false, true>(s, ct, c.tokens * token, base + c.from * s.row_stride, base + f.list[c.to] * s.row_stride, tile);
         }
     }
 }
@@ -804,7 +806,7 @@ __global__ __launch_bounds__(kNT) void k_compact_write(Compact f, States st) {
         for (int64_t item = blockIdx.x; item < moves * per; item += gridDim.x) {
             const int64_t k = item / per, o = (item - k * per) / tiles;
             char* base = static_cast<char*>(s.base) + o * s.outer_stride;
-            copy_tile<STREAM>(s, ct, s.inner, base + f.movers[k] * s.row_stride, base + f.holes[k] * s.row_stride,
+            copy_tile<STREAM, STREAM>(s, ct, s.inner, base + f.movers[k] * s.row_stride, base + f.holes[k] * s.row_stride,
                       (uint32_t)(item - k * per - o * tiles));
         }
     }
