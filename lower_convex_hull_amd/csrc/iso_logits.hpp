@@ -117,8 +117,6 @@ struct Chunk {
     }
 };
 
-inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
-
 inline size_t size_of(int dtype) { return dtype == ISO_DT_F32 ? 4 : 2; }
 
 // log2(e)/T and lse T (up to 21 T past the largest logit) stay inside f32.

@@ -288,5 +288,6 @@ bool disjoint(const Span (&out)[NO], const Span (&in)[NI]) {
     return true;
 }
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace iso

@@ -5,8 +5,6 @@
 namespace iso {
 namespace {
 
-inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
-
 constexpr int kNT = 256, kWaves = kNT / 64;
 constexpr int64_t kMaxSeqs = 1 << 20;
 
@@ -707,7 +705,7 @@ __global__ __launch_bounds__(kNT) void k_compact_count(Compact f, Blocks pb) {
 __global__ __launch_bounds__(kNT) void k_compact_map(Compact f, Blocks pb) {
     __shared__ int64_t red64[2][kWaves];
     __shared__ int red[kWaves];
-    for (int64_t b = blockIdx.x; b == blockIdx.x || b < pb.count; b += gridDim.x) {
+    for (int64_t b = blockIdx.x; b < pb.count; b += gridDim.x) {
         int64_t v[2] = {0, 0};  // live pages, those in the blocks before
         for (int64_t k = threadIdx.x; k < pb.count; k += kNT) {
             const int64_t live = f.live_sum[k];

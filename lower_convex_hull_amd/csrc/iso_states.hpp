@@ -124,9 +124,8 @@ inline bool streamed(const Arrays& st, int64_t rows) {
     return bytes > kStreamed;
 }
 
-// The first `left` of 16 bytes, fewer than 16 as 8, 4, 2 and 1 of them.
+// The first `left` of 16 bytes, fewer than 16, as 8, 4, 2 and 1 of them.
 __device__ __forceinline__ Quad load_bytes(const char* at, int left) {
-    if (left >= 16) return load_quad<false>(at);
     Quad v = {0, 0, 0, 0};
     if (left & 8) {
         const uint64_t x = *reinterpret_cast<const Wide8*>(at);
@@ -139,10 +138,6 @@ __device__ __forceinline__ Quad load_bytes(const char* at, int left) {
     return v;
 }
 __device__ __forceinline__ void store_bytes(char* at, int left, const Quad& v) {
-    if (left >= 16) {
-        store_quad<false>(at, v);
-        return;
-    }
     if (left & 8) *reinterpret_cast<Wide8*>(at) = (uint64_t)v.y << 32 | v.x;
     if (left & 4) *reinterpret_cast<Wide4*>(at + (left & 8)) = v.z;
     if (left & 2) *reinterpret_cast<Wide2*>(at + (left & 12)) = (uint16_t)v.w;
