@@ -458,7 +458,9 @@ int iso_policy_loss_logits(const void* logits, int dtype, int64_t rows, int64_t 
  * has what ranks at -infinity (below f32).  Terms of sums are f32, the sums f64,
  * but that up to eight terms below half of the largest are added in f32 first;
  * the score and the rank are f64 until they are rounded.  How a row's terms are
- * grouped goes by its address modulo 16.
+ * grouped goes by its address modulo 16.  Tokens are masked by -infinity: a finite
+ * value gives the same answers, but where stretches of some thousand tokens hold
+ * nothing else, `take` passes over each of them.
  *
  * Arrays of states.  An iso_blocks describes, for rows (beams) or pages, the
  * blocks row r holds: `inner` bytes each, block (o, m) at

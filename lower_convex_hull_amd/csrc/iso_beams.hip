@@ -89,7 +89,9 @@ template <typename T>
 constexpr int kLowBits = std::is_same<T, float>::value ? 0 : std::is_same<T, __bf16>::value ? 16 : 13;
 
 // Room for the candidates that reach a bound (in a piece: 4 a thread); where more
-// do, a round of a maximum each finds the best.
+// do, a round of a maximum each finds the best.  That is slow, and masks of a finite
+// value come to it where a piece holds little else (64 x 8 x 131072 bf16, 16 each, all but
+// 100 tokens at the lowest value: 1278 us; at -infinity, which reaches no bound, 40).
 constexpr int kRoom = 1024;
 
 // How many of `found` keys in LDS are above k; the next 7 places hold keys that
@@ -147,9 +149,10 @@ struct PieceTerms {
     }
 };
 
-// Bound by instruction issue and HBM together: 512 rows x 131072 bf16 (134 MB, read once)
-// in 35 us, 3.8 TB/s, 69 % of the SIMDs' issue cycles VALU; f32 at 128 x 8 x 200000 is read
-// at 6.0 TB/s.  Few rows by the latency of one piece (6 us).
+// 512 rows x 131072 bf16 (134 MB, read once) take 35 us: 3.8 TB/s and 69 % of the SIMDs'
+// issue cycles, neither at its limit; waves wait at the barriers around the bound, which
+// one of them seeks.  f32 at 128 x 8 x 200000 is bound by HBM (133 us, 6.1 TB/s), few rows
+// by the latency of one piece (6 us).
 // A workgroup takes a piece of a row, held in its registers: the piece's maximum
 // and sum, and its `take` best tokens.  A value that `take` threads' maxima reach
 // bounds the take-th best token from below.  The few vectors that reach it go
@@ -595,8 +598,8 @@ bool select_sizes_ok(int64_t batch, int64_t beams, int64_t vocab, int64_t take, 
            vocab <= (1LL << 30) && batch <= 0x7fffffffLL / beams && dtype >= ISO_DT_F32 && dtype <= ISO_DT_BF16;
 }
 
-// Bound by HBM: what moved rows come from read, they written, 2344 MB in 421 to 448 us,
-// 5.2 to 5.6 TB/s (a copy reaches 4.7 to 5.1).  Rows held in arrays of registers instead
+// Bound by HBM: what moved rows come from read, they written, 2344 MB in 424 to 454 us,
+// 5.2 to 5.5 TB/s (a copy reaches 4.7 to 5.1).  Rows held in arrays of registers instead
 // spilled from 8 rows on (835 us with scratch).
 // A workgroup takes 2^`shift` columns of 16 bytes through all rows of a batch
 // item: it reads what the moved rows come from, waits until all of it has come,

@@ -122,7 +122,7 @@ __device__ __forceinline__ Child child_of(const Fork& f, int64_t i) {
 }
 
 // All but the copies is bound by launches and latency: a step of 1024 sequences over 84000
-// pages moves 1.2 MB, its four kernels take 3.5, 6.5, 10.4 and 4.2 us.
+// pages moves 1.2 MB, its four kernels take 3.4, 6.4, 10.0 and 5.1 us.
 // A step of any size takes six launches: the counts copied and the free pages
 // counted by block; each sequence's children counted, and who goes on to write
 // which page; the counts of the pages of sequences with other than one child;
@@ -462,8 +462,9 @@ __global__ __launch_bounds__(kOneNT) void k_fork_few(Fork f, Blocks pb) {
 }
 
 // A step in one workgroup but for what k_fork_write does: the counts are in LDS.  Bound by
-// the latency of its steps: 7.7 us for four sequences, 14.6 for 256 over 12280 pages (with
-// each child's page compared with every other's 27).
+// the latency of its steps: 7.7 us for four sequences, 14.2 for 256 over 12280 pages, 16
+// where a step's copies came before and the tables are not in the caches (with each
+// child's page compared with every other's 27).
 // Up to kOnePages pages: a step in which every sequence goes on by itself then takes what
 // four launches take (with k_fork_write, 64 sequences: 8192 pages 13.1 us and 14.3, 12288
 // 14.6 and 14.1; 1024 sequences 14.8 and 16.5, 16.5 and 16.5), one whose beams all change
@@ -551,7 +552,7 @@ __global__ __launch_bounds__(kOneNT) void k_fork_one(Fork f) {
 
 // 16-byte columns of what one block of an array holds, `bytes` of each of its mid
 // runs, by the workgroup: kCopyU of them a thread are on their way at a time (half of a
-// 2.3 GB pool, 1562 MB moved: 298 us, 5.2 TB/s; with 4 on their way 389 us, with a quarter
+// 2.3 GB pool, 1562 MB moved: 294 us, 5.3 TB/s; with 4 on their way 389 us, with a quarter
 // of the workgroups 395, byte by byte 822).
 constexpr int kCopyU = 8;
 struct CopyTile {
