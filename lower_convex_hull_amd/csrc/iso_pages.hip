@@ -188,7 +188,8 @@ __global__ __launch_bounds__(kNT) void k_fork_refs(Fork f, Blocks pb) {
         for (int64_t j = threadIdx.x; j < held; j += kNT) {
             const int32_t q = f.table[s * f.max_pages + j];
             if (!f.is_page(q)) continue;
-            const int32_t was = atomicAdd(&f.new_refs[q], more), is = was + more;
+            // past 32 bits as the count in memory: the free pages stay those that are counted
+            const int32_t was = atomicAdd(&f.new_refs[q], more), is = (int32_t)((uint32_t)was + (uint32_t)more);
             if ((was <= 0) != (is <= 0)) atomicAdd(&f.free_sum[q / pb.per], is <= 0 ? 1 : -1);
             if (is < 0) f.plan[3] = 1;  // fewer holders counted than the tables have
         }
@@ -408,7 +409,7 @@ __device__ __forceinline__ Few few_children(const Fork& f, const Child& c, const
     const int32_t writers = edges.writers[at];
     const bool first = c.edge >= 0 && edges.first[at] == (int32_t)threadIdx.x;
     o.copy = c.edge >= 0 && !(count <= writers && first);
-    o.gap = first && count < writers ? writers - count : 0;
+    o.gap = first && count < writers ? (int32_t)((uint32_t)writers - (uint32_t)count) : 0;
     o.lost = o.gap && count <= 0;
     const int64_t want = f.pages_for(c.after);
     const bool too_long = want > f.max_pages || c.after > INT32_MAX;

@@ -85,3 +85,29 @@ def test_fork_of_counts_that_are_too_low(torch, seqs, children, most, pages):
         got, want = run_fork(torch, table, length, refs, parent, page, grow, pools, token_dim)
         again, _ = run_fork(torch, table, length, refs, parent, page, grow, pools, token_dim)
         assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seqs,children,pages", [(12, 30, 200), (12, 30, 13001), (60, 900, 20000), (40, 1500, 6000)])
+def test_counts_that_pass_32_bits(torch, seqs, children, pages):
+    """Counts at the ends of their type, of pages with many holders more and fewer: what is given out are pages, each once."""
+    rng = np.random.default_rng(seqs + pages)
+    top = 2 ** 31 - 1
+    i = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    for trial in range(6):
+        print(f"[decoding] counts past 32 bits {seqs} to {children} of {pages}, {trial}", flush=True)
+        table, length, refs, parent, grow = short_cache(rng, seqs, 4, 3, pages, children)
+        table[:, :2] = rng.choice(table[:4, 0], (seqs, 2))  # a few pages that all hold
+        held = np.unique(table)
+        refs[held] = rng.choice([top, top - 1, top - 20, 0, 1, 5], len(held))
+        pool = torch.zeros(pages, 3, 2, dtype=torch.uint8, device="cuda")
+        out, ln, new, status = iso.pages_fork(i(table), i(length), i(refs), i(parent), page_size=3, grow=i(grow), pools=pool)
+        out, new, status = out.cpu().numpy(), new.cpu().numpy(), status.tolist()
+        assert out.min() >= -1 and out.max() < pages
+        if status[:2] == [0, 0]:
+            given = []
+            for k, p in enumerate(parent):
+                before = int(length[p]) if p >= 0 else 0
+                given += out[k, -(-before // 3):-(-(before + int(grow[k])) // 3)].tolist()
+            assert len(set(given)) == len(given) and status[3] == len(given) + status[2]
+            assert status[3] + status[4] <= pages
